@@ -7,6 +7,9 @@
  *   H-Net style:   bllm_route -> bllm_compact -> ... -> bllm_dechunk_ema
  *   ByteFlow:      bllm_coding_rate -> bllm_topk_select -> bllm_compact (gather)
  *                  -> ... -> bllm_upsample_bins
+ * and, for the encoder beside them, a mixer block in serving:
+ *   bllm_rmsnorm_q8 -> bllm_linear_i8 -> bllm_gated_delta (or _step)
+ *                  -> bllm_rmsnorm_q8 -> bllm_linear_i8
  *
  * Sources of the operations (page titles; sections as on the page):
  *   [BG]  "ByteGen: A Tokenizer-Free Generative Model for Orderbook Events in
@@ -369,6 +372,130 @@ int bllm_upsample_plan(const int32_t* idx, int64_t nseq, int64_t T, int64_t K, i
 int bllm_upsample_apply(const void* g, const void* W, const void* h, int dtype, int64_t nseq, int64_t T,
                         int64_t K, int64_t d_global, int64_t d_local, int64_t nbins, void* s_out,
                         const void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * One mixer block of the byte-level encoder in serving: the RMS norm with the
+ * residual's addition and 8-bit rows, the 8-bit projections around the mixer,
+ * and the gated delta rule over prompts and one byte at a time.  The blocks
+ * produce the rows that bllm_route scores.
+ */
+
+/*
+ * bllm_rmsnorm -- RMS norm of rows with the residual's addition:
+ *   s = x + residual (fp32; s = x without one),
+ *   y = (s * w) / sqrt(mean(s^2) + eps).
+ * x, residual : [rows x d] of dtype; residual may be NULL.  w : [d] of dtype.
+ * residual_out: [rows x d] of dtype or NULL (must be NULL without a
+ *               residual): s rounded, the next block's residual.
+ * y_out       : [rows x d] of dtype.
+ * The outputs may be the same memory as x or residual (row for row); any
+ * other overlap is an error of the caller.  The sum of squares is fp32, so
+ * rows of fp32 values beyond 1e18 overflow it and give y = 0.  A NaN in a row
+ * makes the row NaN.
+ * Errors : BLLM_E_INVAL for null x/w/y_out (x and y_out may be NULL when rows
+ *          = 0), rows < 0, d < 1, eps < 0 or NaN, residual_out without
+ *          residual; BLLM_E_NOTSUP for a bad dtype, rows not a multiple of 16
+ *          bytes, unaligned pointers, d >= 2^24 or rows >= 2^31.
+ */
+int bllm_rmsnorm(const void* x, const void* residual, const void* w, int dtype, int64_t rows, int64_t d,
+                 double eps, void* residual_out, void* y_out, void* stream);
+
+/*
+ * bllm_rmsnorm_q8 -- bllm_rmsnorm with each row of y in 8 bits and a scale:
+ *   t = s * w (fp32), a = max |t| of the row,
+ *   q_out = rne(t * (127 * (1 / a))) in -127 .. 127 (each operation rounded to fp32),
+ *   scale_out = a / (127 sqrt(mean(s^2) + eps)),
+ * so y ~ q_out * scale_out.  The norm's divisor cancels in q_out, which is
+ * therefore the same for every order of the sums.  Rows with a < 1e-30 give
+ * q = 0 and scale = 0.  A row that holds a NaN or an infinity gets a scale
+ * that is not finite (and unspecified q).
+ * q_out : int8 [rows x d]; scale_out : fp32 [rows].  Other arguments and
+ * errors as bllm_rmsnorm; q_out and scale_out overlap no other argument.
+ */
+int bllm_rmsnorm_q8(const void* x, const void* residual, const void* w, int dtype, int64_t rows, int64_t d,
+                    double eps, void* residual_out, int8_t* q_out, float* scale_out, void* stream);
+
+/*
+ * bllm_quant_rows_q8 -- rows in 8 bits with a scale, without a norm:
+ *   a = max |x| of the row, q_out = rne(x * (127 * (1 / a))), scale_out = a / 127.
+ * For the weights of bllm_linear_i8 (once) and for rows that no norm
+ * precedes.  Arguments, small and non-finite rows and errors as
+ * bllm_rmsnorm_q8.
+ */
+int bllm_quant_rows_q8(const void* x, int dtype, int64_t rows, int64_t d, int8_t* q_out, float* scale_out,
+                       void* stream);
+
+/*
+ * bllm_linear_i8 -- product of 8-bit rows with 8-bit weights:
+ *   y[i, j] = (sum_l xq[i, l] * wq[j, l]) * (x_scale[i] * w_scale[j]) + bias[j]
+ * The sum is exact (32-bit integers); scales and bias are applied in fp32 and
+ * y is rounded once to dtype.
+ * xq : int8 [m x k], x_scale : fp32 [m] (each token's scale);
+ * wq : int8 [n x k] (one row for each output channel), w_scale : fp32 [n];
+ * bias : fp32 [n] or NULL; y_out : [m x n] of dtype.
+ * ws : bllm_linear_i8_workspace(m, n, k) bytes (0 for most sizes; then ws
+ *      may be NULL).
+ * Errors : BLLM_E_INVAL for null pointers (xq, x_scale and y_out may be NULL
+ *          when m = 0), m < 0, n < 1, k < 1; BLLM_E_NOTSUP for a bad dtype, k
+ *          not a multiple of 16 or above 131056, m or n >= 2^31, unaligned
+ *          xq, wq or y_out; BLLM_E_WS.
+ */
+size_t bllm_linear_i8_workspace(int64_t m, int64_t n, int64_t k);
+int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
+                   const float* bias, int dtype, int64_t m, int64_t n, int64_t k, void* y_out, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * bllm_gated_delta -- the gated delta rule over a ragged batch.  Per sequence
+ * and value head, with a state S [dk x dv] (fp32):
+ *   u_t = beta_t (v_t - e^{g_t} S_{t-1}^T k_t)
+ *   S_t = e^{g_t} S_{t-1} + k_t u_t^T
+ *   o_t = scale S_t^T q_t
+ * Value head h uses key head h / (hv / hk).  With unit_qk != 0 every q and k
+ * row of a head is first scaled to unit length, x / sqrt(|x|^2 + 1e-6); the
+ * recurrence is stable for beta in [0, 2], g <= 0 and unit keys.
+ * q, k     : bf16, token t of head i at t * q_stride + i * dk (elements);
+ *            v likewise with v_stride and dv: column slices of a wider
+ *            projection output need no copy.  Strides are multiples of 8.
+ * g, beta  : fp32 [total x hv].  g = -inf forgets the state.
+ * offsets  : int64 [nseq+1] device; sequences of length 0 pass their state on.
+ * state_in : fp32 [nseq x hv x dk x dv] or NULL (zero); state_out : the same
+ *            shape or NULL; may equal state_in (updated in place).
+ * o_out    : bf16 [total x hv x dv], dense.
+ * ws       : bllm_gated_delta_workspace(nseq, total, hv, dk, dv) bytes.
+ * Errors   : BLLM_E_INVAL for null pointers (q, k, v, g, beta and o_out may
+ *            be NULL when total = 0), sizes below 1, hv not a multiple of hk,
+ *            strides shorter than the heads, NaN scale; BLLM_E_NOTSUP for a
+ *            dtype other than bf16, dk not a multiple of 8 or above 128, dv
+ *            not a multiple of 8 or above 1024, hv above 1024, nseq above
+ *            65535, total >= 2^31, strides or pointers off 16 bytes;
+ *            BLLM_E_WS.
+ */
+size_t bllm_gated_delta_workspace(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv);
+int bllm_gated_delta(const void* q, const void* k, const void* v, const float* g, const float* beta, int dtype,
+                     const int64_t* offsets, int64_t nseq, int64_t total, int64_t hk, int64_t hv, int64_t dk,
+                     int64_t dv, int64_t q_stride, int64_t k_stride, int64_t v_stride, double scale, int unit_qk,
+                     const float* state_in, float* state_out, void* o_out, void* ws, size_t ws_bytes,
+                     void* stream);
+
+/*
+ * bllm_gated_delta_step -- one token of each of nseq streams: row s of q, k,
+ * v, g, beta and o_out belongs to stream s, whose state is row slots[s] (row
+ * s without slots) of state_in and is written to the same row of state_out.
+ * state_in, state_out : fp32 [nslots x hv x dk x dv]; may be equal (updated in
+ *            place), else the rows of state_out that no slot names are left.
+ * slots    : int32 [nseq] device or NULL.  A slot outside [0, nslots) holds
+ *            no state: it counts as zero and is not written.  The same slot
+ *            twice is an error of the caller.
+ * Other arguments and errors as bllm_gated_delta (total = nseq);
+ * BLLM_E_INVAL also for null states, nslots < 1, or nslots < nseq without
+ * slots.
+ */
+int bllm_gated_delta_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                          int dtype, int64_t nseq, int64_t hk, int64_t hv, int64_t dk, int64_t dv,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, double scale, int unit_qk,
+                          const float* state_in, float* state_out, const int32_t* slots, int64_t nslots,
+                          void* o_out, void* stream);
 
 #ifdef __cplusplus
 }

@@ -37,3 +37,4 @@ from .hnet import route, boundary_mask, stage_quantile, compact, dechunk_ema, de
 from .byteflow import (  # noqa: F401
     alpha_of, coding_rate, coding_rate_at, coding_rate_stream, topk_select, topk_select_window, topk_mask, gather, chunk_bins, upsample_bins,
 )
+from .mixer import rmsnorm, rmsnorm_q8, quant_rows_q8, linear_i8, gated_delta  # noqa: F401
