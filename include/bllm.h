@@ -468,7 +468,8 @@ int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, con
  *            strides shorter than the heads, NaN scale; BLLM_E_NOTSUP for a
  *            dtype other than bf16, dk not a multiple of 8 or above 128, dv
  *            not a multiple of 8 or above 1024, hv above 1024, nseq above
- *            65535, total >= 2^31, strides or pointers off 16 bytes;
+ *            65535, total >= 2^31, strides >= 2^22, strides or pointers off 16
+ *            bytes;
  *            BLLM_E_WS.
  */
 size_t bllm_gated_delta_workspace(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv);

@@ -209,6 +209,8 @@ DELTA = [
     ([1], 1, 1, 8, 8), ([5], 1, 1, 16, 16), ([63, 64, 65], 1, 2, 64, 64), ([0, 3, 0, 130, 1], 2, 2, 128, 128),
     ([200], 2, 6, 32, 40), ([77, 128], 3, 3, 40, 24), ([300, 17], 1, 1, 128, 256), ([129], 2, 2, 96, 72),
     ([7] * 40, 1, 4, 64, 32), ([520], 1, 1, 72, 136), ([1000, 0, 10], 1, 1, 64, 128),
+    # enough heads and columns that a workgroup takes 64 columns
+    ([70, 0, 9, 64] * 8, 2, 8, 128, 72), ([65, 3] * 20, 1, 8, 24, 40),
 ]
 
 
