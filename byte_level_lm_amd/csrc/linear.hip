@@ -5,17 +5,27 @@
 // does not depend on its order; the scales and the bias are applied in fp32
 // and y is rounded once.
 //
-// A wave owns a 32 x 32 tile of y as 2 x 2 tiles of v_mfma_i32_16x16x64_i8 and
-// reads its operands straight from memory: both are row-major along K, so a
-// lane's 16 bytes of a row are one load.
+// Products run on v_mfma_i32_16x16x64_i8 with the weights as its rows and the
+// tokens as its columns: a lane then holds one token's consecutive channels.
+// The rows of a pair of weight tiles interleave in fours, which makes those
+// eight channels, one 16-byte store in bf16.
+#include <algorithm>
+
 #include "common.h"
 
 namespace bllm {
 namespace {
 
 typedef int intx4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx8 __attribute__((ext_vector_type(8)));
+typedef __amdgpu_buffer_rsrc_t Buffer;
 
 constexpr int64_t kMaxK = (1 << 17) - 16;  // 128 * 128 * kMaxK < 2^31
+constexpr int64_t kMaxRows = INT32_MAX - 1024, kMaxOut = int64_t(1) << 44;  // tile and row numbers fit 32 bits
+constexpr int kCus = 256, kXcds = 8;
+constexpr int kBK = 64;            // bytes of K in a step
+constexpr int kOutside = 1 << 30;  // a buffer offset that reads as zero
 
 struct LinArgs {
   const int8_t* xq;
@@ -28,48 +38,333 @@ struct LinArgs {
   int k;
 };
 
-// element r of a lane's 16 x 16 accumulator: row 4 (lane / 16) + r, column lane % 16
+// channel of row r of weight tile j: pairs of tiles interleave in fours
+__device__ inline int chan(int j, int r) { return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3); }
+
+// eight channels of one token from a lane's two accumulators: one store of 16
+// bytes (32 in fp32) at any alignment, rows of y may start anywhere
 template <int DT>
-__device__ inline void store_y(const LinArgs& a, int64_t row, int64_t col, int acc) {
-  float v = static_cast<float>(acc) * (a.sx[row] * a.sw[col]);
-  if (a.bias) v += a.bias[col];
-  if (DT == BLLM_F32)
-    static_cast<float*>(a.y)[row * a.n + col] = v;
-  else
-    static_cast<uint16_t*>(a.y)[row * a.n + col] = f32_to_bf16(v);
+__device__ inline void store_whole(const LinArgs& a, int64_t at, float sx, const float* sw, const float* bias,
+                                   const intx4& lo, const intx4& hi) {
+  floatx8 v;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(i < 4 ? lo[i] : hi[i - 4]) * (sx * sw[i]) + bias[i];
+  if constexpr (DT == BLLM_F32) {
+    __builtin_memcpy(static_cast<float*>(a.y) + at, &v, 32);
+  } else {
+    const bf16x8 b = __builtin_convertvector(v, bf16x8);
+    __builtin_memcpy(static_cast<uint16_t*>(a.y) + at, &b, 16);
+  }
+}
+// the same at the right edge, where only some of the channels exist
+template <int DT>
+__device__ inline void store_some(const LinArgs& a, int64_t at, float sx, const float* sw, const float* bias,
+                                  const intx4& lo, const intx4& hi, int count) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float u = static_cast<float>(i < 4 ? lo[i] : hi[i - 4]) * (sx * sw[i]) + bias[i];
+    if (i < count) {
+      if constexpr (DT == BLLM_F32)
+        static_cast<float*>(a.y)[at + i] = u;
+      else
+        static_cast<uint16_t*>(a.y)[at + i] = f32_to_bf16(u);
+    }
+  }
+}
+// scales and biases of eight channels, zero past the last
+__device__ inline void channel_scales(const LinArgs& a, int64_t col, float* sw, float* bias) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool in = col + i < a.n;
+    sw[i] = in ? a.sw[col + i] : 0.0f;
+    bias[i] = in && a.bias ? a.bias[col + i] : 0.0f;
+  }
 }
 
-template <int DT>
-__global__ __launch_bounds__(256) void linear_direct(LinArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 64 + (wave >> 1) * 32;
-  const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 64 + (wave & 1) * 32;
-  const int kk = (lane >> 4) * 16;
-  const int8_t* pa[2];
-  const int8_t* pb[2];
-  for (int i = 0; i < 2; ++i) {
-    const int64_t r = row0 + 16 * i + (lane & 15), c = col0 + 16 * i + (lane & 15);
-    pa[i] = a.xq + (r < a.m ? r : a.m - 1) * a.k;
-    pb[i] = a.wq + (c < a.n ? c : a.n - 1) * a.k;
-  }
-  intx4 acc[2][2] = {};
-  for (int k0 = 0; k0 < a.k; k0 += 64) {
-    intx4 fa[2] = {}, fb[2] = {};
-    if (k0 + kk < a.k) {
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = *reinterpret_cast<const intx4*>(pa[i] + k0 + kk);
-        fb[i] = *reinterpret_cast<const intx4*>(pb[i] + k0 + kk);
-      }
-    }
-    for (int i = 0; i < 2; ++i)
-      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
-  }
-  for (int i = 0; i < 2; ++i)
+// ---------------------------------------------------------------- few tokens
+
+// A workgroup owns 16 MT tokens and 32 channels; its eight waves take K in
+// turns of 64 bytes, straight from memory (weights are read once by the chip,
+// tokens come from L2), and add their sums in LDS.
+template <int DT, int MT>
+__global__ __launch_bounds__(512) void linear_few(LinArgs a) {
+  constexpr int NW = 8;
+  __shared__ intx4 sAcc[NW / 2][2 * MT][64];
+  const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 16 * MT, col0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int8_t *pw[2], *px[MT];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) pw[j] = a.wq + min(col0 + chan(j, n), a.n - 1) * a.k + 16 * gq;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) px[i] = a.xq + min(row0 + 16 * i + n, a.m - 1) * a.k + 16 * gq;
+  intx4 acc[2][MT] = {};
+  const int whole = a.k & ~63;
+#pragma unroll 2
+  for (int k = 64 * w; k < whole; k += 64 * NW) {
+    intx4 fw[2], fx[MT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fw[j] = *reinterpret_cast<const intx4*>(pw[j] + k);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fx[i] = *reinterpret_cast<const intx4*>(px[i] + k);
+#pragma unroll
     for (int j = 0; j < 2; ++j)
-      for (int r = 0; r < 4; ++r) {
-        const int64_t row = row0 + 16 * i + 4 * (lane >> 4) + r, col = col0 + 16 * j + (lane & 15);
-        if (row < a.m && col < a.n) store_y<DT>(a, row, col, acc[i][j][r]);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[j][i], 0, 0, 0);
+  }
+  if (whole < a.k && ((whole >> 6) & (NW - 1)) == w) {  // the last, partial 64 bytes
+    const bool in = whole + 16 * gq < a.k;
+    intx4 fw[2], fx[MT];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fw[j] = in ? *reinterpret_cast<const intx4*>(pw[j] + whole) : intx4{};
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fx[i] = in ? *reinterpret_cast<const intx4*>(px[i] + whole) : intx4{};
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[j][i], 0, 0, 0);
+  }
+  for (int half = NW / 2; half >= 1; half >>= 1) {
+    if (w >= half && w < 2 * half) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sAcc[w - half][j * MT + i][lane] = acc[j][i];
+    }
+    __syncthreads();
+    if (w < half) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] += sAcc[w][j * MT + i][lane];
+    }
+    __syncthreads();
+  }
+  if (w) return;
+  const int64_t col = col0 + 8 * gq;
+  const int count = static_cast<int>(min(a.n - col, int64_t(8)));
+  if (count < 1) return;
+  float sw[8], bias[8];
+  channel_scales(a, col, sw, bias);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = row0 + 16 * i + n;
+    if (row >= a.m) continue;
+    if (count == 8)
+      store_whole<DT>(a, row * a.n + col, a.sx[row], sw, bias, acc[0][i], acc[1][i]);
+    else
+      store_some<DT>(a, row * a.n + col, a.sx[row], sw, bias, acc[0][i], acc[1][i], count);
+  }
+}
+
+// ---------------------------------------------------------------- tiles
+
+// 16-byte piece p of row r of a staged tile (rows of kBK bytes) lies at piece
+// p ^ (r / 4 % 4): the sixteen rows of a fragment read start in different banks
+__device__ inline int swz(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
+
+__device__ inline void to_lds(Buffer b, int at, int k, int8_t* lds) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void*)lds, 16, at, k, 0, 0);
+}
+
+// At most N vector memory operations and no LDS operation of this wave are
+// outstanding, then the workgroup's barrier.  (A fence would wait for every
+// load into LDS, also those for later steps.)
+template <int N>
+__device__ inline void wait_and_meet() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x70 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
+// Tile t of the product: XCD x has the x-th eighth of them, and its workgroups
+// take neighbours at a time, token tiles first in groups of kGroup, so that
+// what its L2 holds at one time is a few row blocks of either side.
+constexpr int kGroup = 8;
+struct Where {
+  int row, col;
+};
+__device__ inline Where tile_at(int t, int mt, int nt, int TM, int TN) {
+  const int g = t / (kGroup * nt), first = g * kGroup, gm = min(mt - first, kGroup);
+  const int in = t - g * kGroup * nt, j = in / gm;
+  return {(first + in - j * gm) * TM, j * TN};
+}
+
+// Tiles of TM tokens and TN channels, 2 x WN waves.  K goes by in steps
+// of kBK bytes through a ring of kRing LDS buffers, filled without registers
+// three steps ahead.  In a step a wave multiplies weight tile by weight tile;
+// once it has read the step's last fragment it meets the others, refills the
+// buffer they have all read and reads the next step's fragments under the
+// rest of the products.  The loop runs over all steps of all the workgroup's
+// tiles, so the next tile's first steps are on their way while one is written.
+constexpr int kRing = 4;
+
+template <int DT, int TM, int TN, int WN>
+__global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int nt) {
+  constexpr int NW = 2 * WN;                              // waves, as 2 x WN
+  constexpr int MT = TM / 32, NT = TN / WN / 16;          // 16 x 16 tiles of a wave
+  constexpr int UX = TM * kBK / (1024 * NW), U = UX + TN * kBK / (1024 * NW);  // loads of 1 KB a wave makes for a step
+  constexpr int JB = NT / 2 - 1;                          // the weight tile before which the waves meet
+  struct Stage {
+    int8_t X[TM * kBK], W[TN * kBK];
+  };
+  __shared__ __align__(1024) Stage ring[kRing];
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, gq = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / WN * (TM / 2), wc = w % WN * (TN / WN);
+  const int tiles = mt * nt, per = (tiles + kXcds - 1) / kXcds;
+  const int group = gridDim.x / kXcds;     // the grid is a multiple of kXcds
+  const int lo = (blockIdx.x % kXcds) * per, hi = min(lo + per, tiles);
+  int t = lo + blockIdx.x / kXcds;         // this workgroup's tile
+  if (t >= hi) return;
+  const int steps = (a.k + kBK - 1) / kBK;
+  int left = (hi - t + group - 1) / group * steps;  // steps of all its tiles
+
+  // Loads: where the lane's piece of each 1 KB lies, for the tile the loads are at.
+  // Sixteen rows of four pieces are one load; rows past the end repeat the last.
+  int lt = t, lk = 0, off[U];
+  Buffer bx, bw;
+  const int prow = lane >> 2, pk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+  const auto aim = [&]() __attribute__((always_inline)) {
+    const Where at = tile_at(lt, mt, nt, TM, TN);
+    const int rx = min(static_cast<int>(a.m) - at.row, TM), rw = min(static_cast<int>(a.n) - at.col, TN);
+    bx = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.xq + static_cast<int64_t>(at.row) * a.k), 0, rx * a.k,
+                                           0x00027000);
+    bw = __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(a.wq + static_cast<int64_t>(at.col) * a.k), 0, rw * a.k,
+                                           0x00027000);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = ((u < UX ? u : u - UX) * NW + w) * 16 + prow;
+      off[u] = min(row, (u < UX ? rx : rw) - 1) * a.k + pk;
+    }
+  };
+  const auto load = [&](int u, int8_t* X, int8_t* W) __attribute__((always_inline)) {
+    const bool x = u < UX;
+    const bool out = lk + pk >= a.k;  // pieces past the end of K read as zero
+    to_lds(x ? bx : bw, out ? kOutside : off[u], lk, (x ? X : W) + ((x ? u : u - UX) * NW + w) * 1024);
+  };
+  const auto advance = [&]() __attribute__((always_inline)) {
+    lk += kBK;
+    if (lk >= a.k) {
+      lk = 0;
+      lt += group;
+      if (lt < hi) aim();
+    }
+  };
+
+  intx4 acc[NT][MT] = {};
+  intx4 fx[MT], fw[NT];
+  const int rx0 = swz(wr + n, gq), rw0 = swz(wc + chan(0, n), gq), rw1 = swz(wc + chan(1, n), gq);
+  const auto read_x = [&](int i, const int8_t* X) __attribute__((always_inline)) {
+    return *reinterpret_cast<const intx4*>(X + rx0 + 16 * i * kBK);  // 16 rows on, the pieces are exchanged alike
+  };
+  const auto read_w = [&](int j, const int8_t* W) __attribute__((always_inline)) {
+    return *reinterpret_cast<const intx4*>(W + (j & 1 ? rw1 : rw0) + 32 * (j >> 1) * kBK);
+  };
+  // One step, with `more` if there is one to load.  The buffers are restrict
+  // arguments: no fragment read has to wait for loads that fill another one.
+  const auto step = [&](int left, int8_t* dX, int8_t* dW, const int8_t* __restrict__ cW,
+                        const int8_t* __restrict__ nX, const int8_t* __restrict__ nW) __attribute__((always_inline)) {
+    intx4 gx[MT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      if (j < JB) {
+#pragma unroll
+        for (int q = 2 + (NT - 2) * j / JB; q < 2 + (NT - 2) * (j + 1) / JB; ++q) fw[q] = read_w(q, cW);
       }
+      if (j == JB) {
+        if (left > 3)
+          wait_and_meet<2 * U>();
+        else
+          wait_and_meet<0>();
+      }
+      if (j >= JB) {
+        constexpr int M = NT - JB;
+        if (left > 4) {
+#pragma unroll
+          for (int u = U * (j - JB) / M; u < U * (j - JB + 1) / M; ++u) load(u, dX, dW);
+        }
+#pragma unroll
+        for (int i = MT * (j - JB) / M; i < MT * (j - JB + 1) / M; ++i) gx[i] = read_x(i, nX);
+        if (j == JB + 1) fw[0] = read_w(0, nW);
+        if (j == JB + 2) fw[1] = read_w(1, nW);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[j], fx[i], acc[j][i], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fx[i] = gx[i];
+    if (left > 4) advance();
+  };
+
+  aim();
+#pragma unroll 1
+  for (int i = 0; i < min(kRing, left); ++i) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, ring[i].X, ring[i].W);
+    advance();
+  }
+  if (left > 3)
+    wait_and_meet<3 * U>();
+  else
+    wait_and_meet<0>();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) fx[i] = read_x(i, ring[0].X);
+  fw[0] = read_w(0, ring[0].W);
+  fw[1] = read_w(1, ring[0].W);
+#pragma unroll 1
+  for (int i = 0, k = 0; left > 0; ++i, --left) {
+    Stage &c = ring[i & (kRing - 1)], &nx = ring[(i + 1) & (kRing - 1)];
+    step(left, c.X, c.W, c.W, nx.X, nx.W);
+    if (++k < steps) continue;
+    k = 0;
+    const Where at = tile_at(t, mt, nt, TM, TN);
+    t += group;
+    const int m = static_cast<int>(a.m), row0 = at.row + wr + n;
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      const int col = at.col + wc + 16 * j + 8 * gq, count = min(static_cast<int>(a.n) - col, 8);
+      float sw[8], bias[8];
+      channel_scales(a, col, sw, bias);
+#pragma unroll
+      for (int r = 0; r < MT; ++r) {
+        const int row = row0 + 16 * r;
+        if (row < m && count > 0) {
+          const float sx = a.sx[row];
+          const int64_t to = static_cast<int64_t>(row) * a.n + col;
+          if (count == 8)
+            store_whole<DT>(a, to, sx, sw, bias, acc[j][r], acc[j + 1][r]);
+          else
+            store_some<DT>(a, to, sx, sw, bias, acc[j][r], acc[j + 1][r], count);
+        }
+        acc[j][r] = acc[j + 1][r] = intx4{};
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+template <int MT>
+void few_launch(const LinArgs& a, int dtype, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, 32)), static_cast<unsigned>(ceil_div(a.m, 16 * MT)));
+  if (dtype == BLLM_F32)
+    hipLaunchKernelGGL((linear_few<BLLM_F32, MT>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((linear_few<BLLM_BF16, MT>), grid, dim3(512), 0, st, a);
+}
+
+template <int TM, int TN, int WN>
+void tiles_launch(const LinArgs& a, int dtype, hipStream_t st) {
+  const int mt = static_cast<int>(ceil_div(a.m, TM)), nt = static_cast<int>(ceil_div(a.n, TN));
+  // as many workgroups as the LDS of all CUs holds at once, each with several tiles
+  const int64_t most = kCus * (160 * 1024 / (kRing * (TM + TN) * kBK));
+  const dim3 grid(static_cast<unsigned>(std::min(ceil_div(int64_t(mt) * nt, kXcds) * kXcds, most)));
+  if (dtype == BLLM_F32)
+    hipLaunchKernelGGL((linear_tiles<BLLM_F32, TM, TN, WN>), grid, dim3(128 * WN), 0, st, a, mt, nt);
+  else
+    hipLaunchKernelGGL((linear_tiles<BLLM_BF16, TM, TN, WN>), grid, dim3(128 * WN), 0, st, a, mt, nt);
 }
 
 }  // namespace
@@ -83,18 +378,21 @@ extern "C" int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8
                               const float* bias, int dtype, int64_t m, int64_t n, int64_t k, void* y_out,
                               void* ws, size_t ws_bytes, void* stream) {
   if (m < 0 || n < 1 || k < 1 || !wq || !w_scale || (m > 0 && (!xq || !x_scale || !y_out))) return BLLM_E_INVAL;
-  if (!valid_dtype(dtype) || k % 16 != 0 || k > kMaxK || m >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) ||
+  if (!valid_dtype(dtype) || k % 16 != 0 || k > kMaxK || m > kMaxRows || n > kMaxRows || m * n > kMaxOut ||
       !aligned16(xq) || !aligned16(wq) || !aligned16(y_out))
     return BLLM_E_NOTSUP;
   if (m == 0) return BLLM_OK;
   LinArgs a{xq, x_scale, wq, w_scale, bias, y_out, m, n, static_cast<int>(k)};
-  const int64_t gy = ceil_div(m, 64), gx = ceil_div(n, 64);
-  if (gy > 65535) return BLLM_E_NOTSUP;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-  if (dtype == BLLM_F32)
-    hipLaunchKernelGGL(linear_direct<BLLM_F32>, grid, dim3(256), 0, st, a);
+  if (m <= 16)
+    few_launch<1>(a, dtype, st);
+  else if (m <= 32)
+    few_launch<2>(a, dtype, st);
+  else if (ceil_div(m, 128) * ceil_div(n, 128) < 64)
+    few_launch<4>(a, dtype, st);
+  else if (ceil_div(m, 256) * ceil_div(n, 256) < kCus)
+    tiles_launch<128, 128, 2>(a, dtype, st);
   else
-    hipLaunchKernelGGL(linear_direct<BLLM_BF16>, grid, dim3(256), 0, st, a);
+    tiles_launch<256, 256, 4>(a, dtype, st);
   return launch_status();
 }

@@ -437,8 +437,8 @@ int bllm_quant_rows_q8(const void* x, int dtype, int64_t rows, int64_t d, int8_t
  *      may be NULL).
  * Errors : BLLM_E_INVAL for null pointers (xq, x_scale and y_out may be NULL
  *          when m = 0), m < 0, n < 1, k < 1; BLLM_E_NOTSUP for a bad dtype, k
- *          not a multiple of 16 or above 131056, m or n >= 2^31, unaligned
- *          xq, wq or y_out; BLLM_E_WS.
+ *          not a multiple of 16 or above 131056, m or n above 2^31 - 1025, m n
+ *          above 2^44, unaligned xq, wq or y_out; BLLM_E_WS.
  */
 size_t bllm_linear_i8_workspace(int64_t m, int64_t n, int64_t k);
 int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
