@@ -41,22 +41,42 @@ struct LinArgs {
 // channel of row r of weight tile j: pairs of tiles interleave in fours
 __device__ inline int chan(int j, int r) { return 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3); }
 
-// eight channels of one token from a lane's two accumulators: one store of 16
-// bytes (32 in fp32) at any alignment, rows of y may start anywhere
+// scales and biases of N channels from col; past the last channel it is repeated
+template <int N>
+__device__ inline void channel_scales(const LinArgs& a, int64_t col, float* sw, float* bias) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) sw[i] = a.sw[min(col + i, a.n - 1)];
+#pragma unroll
+  for (int i = 0; i < N; ++i) bias[i] = 0.0f;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) bias[i] = a.bias[min(col + i, a.n - 1)];
+  }
+}
+
+// Eight channels of one token from a lane's two accumulators: one store of 16
+// bytes (two in fp32) at any alignment, rows of y may start anywhere.
 template <int DT>
 __device__ inline void store_whole(const LinArgs& a, int64_t at, float sx, const float* sw, const float* bias,
                                    const intx4& lo, const intx4& hi) {
+  typedef uint32_t loose4 __attribute__((ext_vector_type(4), aligned(2)));
   floatx8 v;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(i < 4 ? lo[i] : hi[i - 4]) * (sx * sw[i]) + bias[i];
+  loose4 u[2];
+  loose4* to;
   if constexpr (DT == BLLM_F32) {
-    __builtin_memcpy(static_cast<float*>(a.y) + at, &v, 32);
+    __builtin_memcpy(u, &v, 32);
+    to = reinterpret_cast<loose4*>(static_cast<float*>(a.y) + at);
   } else {
     const bf16x8 b = __builtin_convertvector(v, bf16x8);
-    __builtin_memcpy(static_cast<uint16_t*>(a.y) + at, &b, 16);
+    __builtin_memcpy(u, &b, 16);
+    to = reinterpret_cast<loose4*>(static_cast<uint16_t*>(a.y) + at);
   }
+#pragma unroll
+  for (int i = 0; i < (DT == BLLM_F32 ? 2 : 1); ++i) to[i] = u[i];
 }
-// the same at the right edge, where only some of the channels exist
+// the same at the right edge, where only `count` of the channels exist
 template <int DT>
 __device__ inline void store_some(const LinArgs& a, int64_t at, float sx, const float* sw, const float* bias,
                                   const intx4& lo, const intx4& hi, int count) {
@@ -69,15 +89,6 @@ __device__ inline void store_some(const LinArgs& a, int64_t at, float sx, const 
       else
         static_cast<uint16_t*>(a.y)[at + i] = f32_to_bf16(u);
     }
-  }
-}
-// scales and biases of eight channels, zero past the last
-__device__ inline void channel_scales(const LinArgs& a, int64_t col, float* sw, float* bias) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool in = col + i < a.n;
-    sw[i] = in ? a.sw[col + i] : 0.0f;
-    bias[i] = in && a.bias ? a.bias[col + i] : 0.0f;
   }
 }
 
@@ -145,7 +156,7 @@ __global__ __launch_bounds__(512) void linear_few(LinArgs a) {
   const int count = static_cast<int>(min(a.n - col, int64_t(8)));
   if (count < 1) return;
   float sw[8], bias[8];
-  channel_scales(a, col, sw, bias);
+  channel_scales<8>(a, col, sw, bias);
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t row = row0 + 16 * i + n;
@@ -159,9 +170,15 @@ __global__ __launch_bounds__(512) void linear_few(LinArgs a) {
 
 // ---------------------------------------------------------------- tiles
 
+// Channel of row r of weight tile j: tiles interleave in fours of rows, four
+// tiles at a time, so that a lane holds sixteen consecutive channels.
+__device__ inline int chan16(int j, int r) { return 64 * (j >> 2) + 16 * (r >> 2) + 4 * (j & 3) + (r & 3); }
+
 // 16-byte piece p of row r of a staged tile (rows of kBK bytes) lies at piece
-// p ^ (r / 4 % 4): the sixteen rows of a fragment read start in different banks
-__device__ inline int swz(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
+// p ^ (r / 4 % 4) for tokens and p ^ (r / 16 % 4) for weights: the sixteen rows
+// of a fragment read start in different banks
+__device__ inline int swz_x(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
+__device__ inline int swz_w(int row, int p) { return row * kBK + ((p ^ ((row >> 4) & 3)) << 4); }
 
 __device__ inline void to_lds(Buffer b, int at, int k, int8_t* lds) {
   typedef __attribute__((address_space(3))) void lds_void;
@@ -193,16 +210,14 @@ __device__ inline Where tile_at(int t, int mt, int nt, int TM, int TN) {
 }
 
 // Tiles of TM tokens and TN channels, 2 x WN waves.  K goes by in steps
-// of kBK bytes through a ring of kRing LDS buffers, filled without registers
-// three steps ahead.  In a step a wave multiplies weight tile by weight tile;
+// of kBK bytes through a ring of R LDS buffers, filled without registers
+// R - 1 steps ahead.  In a step a wave multiplies weight tile by weight tile;
 // once it has read the step's last fragment it meets the others, refills the
 // buffer they have all read and reads the next step's fragments under the
 // rest of the products.  The loop runs over all steps of all the workgroup's
 // tiles, so the next tile's first steps are on their way while one is written.
-constexpr int kRing = 4;
-
-template <int DT, int TM, int TN, int WN>
-__global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int nt) {
+template <int DT, int TM, int TN, int WN, int R>
+__global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, int nt) {
   constexpr int NW = 2 * WN;                              // waves, as 2 x WN
   constexpr int MT = TM / 32, NT = TN / WN / 16;          // 16 x 16 tiles of a wave
   constexpr int UX = TM * kBK / (1024 * NW), U = UX + TN * kBK / (1024 * NW);  // loads of 1 KB a wave makes for a step
@@ -210,7 +225,8 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
   struct Stage {
     int8_t X[TM * kBK], W[TN * kBK];
   };
-  __shared__ __align__(1024) Stage ring[kRing];
+  __shared__ __align__(1024) Stage ring[R];
+  __shared__ __align__(16) float sScale[TM + 2 * TN];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, gq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wr = w / WN * (TM / 2), wc = w % WN * (TN / WN);
   const int tiles = mt * nt, per = (tiles + kXcds - 1) / kXcds;
@@ -225,7 +241,8 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
   // Sixteen rows of four pieces are one load; rows past the end repeat the last.
   int lt = t, lk = 0, off[U];
   Buffer bx, bw;
-  const int prow = lane >> 2, pk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+  static_assert(NW % 4 == 0, "row / 16 of a wave's loads is w modulo 4");
+  const int prow = lane >> 2, pkx = 16 * ((lane & 3) ^ ((lane >> 4) & 3)), pkw = 16 * ((lane & 3) ^ (w & 3));
   const auto aim = [&]() __attribute__((always_inline)) {
     const Where at = tile_at(lt, mt, nt, TM, TN);
     const int rx = min(static_cast<int>(a.m) - at.row, TM), rw = min(static_cast<int>(a.n) - at.col, TN);
@@ -236,12 +253,12 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = ((u < UX ? u : u - UX) * NW + w) * 16 + prow;
-      off[u] = min(row, (u < UX ? rx : rw) - 1) * a.k + pk;
+      off[u] = min(row, (u < UX ? rx : rw) - 1) * a.k + (u < UX ? pkx : pkw);
     }
   };
   const auto load = [&](int u, int8_t* X, int8_t* W) __attribute__((always_inline)) {
     const bool x = u < UX;
-    const bool out = lk + pk >= a.k;  // pieces past the end of K read as zero
+    const bool out = lk + (x ? pkx : pkw) >= a.k;  // pieces past the end of K read as zero
     to_lds(x ? bx : bw, out ? kOutside : off[u], lk, (x ? X : W) + ((x ? u : u - UX) * NW + w) * 1024);
   };
   const auto advance = [&]() __attribute__((always_inline)) {
@@ -255,12 +272,12 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
 
   intx4 acc[NT][MT] = {};
   intx4 fx[MT], fw[NT];
-  const int rx0 = swz(wr + n, gq), rw0 = swz(wc + chan(0, n), gq), rw1 = swz(wc + chan(1, n), gq);
+  const int rx0 = swz_x(wr + n, gq), rw0 = swz_w(wc + chan16(0, n), gq);
   const auto read_x = [&](int i, const int8_t* X) __attribute__((always_inline)) {
     return *reinterpret_cast<const intx4*>(X + rx0 + 16 * i * kBK);  // 16 rows on, the pieces are exchanged alike
   };
   const auto read_w = [&](int j, const int8_t* W) __attribute__((always_inline)) {
-    return *reinterpret_cast<const intx4*>(W + (j & 1 ? rw1 : rw0) + 32 * (j >> 1) * kBK);
+    return *reinterpret_cast<const intx4*>(W + rw0 + (64 * (j >> 2) + 4 * (j & 3)) * kBK);  // and so for these
   };
   // One step, with `more` if there is one to load.  The buffers are restrict
   // arguments: no fragment read has to wait for loads that fill another one.
@@ -274,14 +291,14 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
         for (int q = 2 + (NT - 2) * j / JB; q < 2 + (NT - 2) * (j + 1) / JB; ++q) fw[q] = read_w(q, cW);
       }
       if (j == JB) {
-        if (left > 3)
-          wait_and_meet<2 * U>();
+        if (left >= R)
+          wait_and_meet<(R - 2) * U>();
         else
           wait_and_meet<0>();
       }
       if (j >= JB) {
         constexpr int M = NT - JB;
-        if (left > 4) {
+        if (left > R) {
 #pragma unroll
           for (int u = U * (j - JB) / M; u < U * (j - JB + 1) / M; ++u) load(u, dX, dW);
         }
@@ -296,18 +313,18 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) fx[i] = gx[i];
-    if (left > 4) advance();
+    if (left > R) advance();
   };
 
   aim();
 #pragma unroll 1
-  for (int i = 0; i < min(kRing, left); ++i) {
+  for (int i = 0; i < min(R, left); ++i) {
 #pragma unroll
     for (int u = 0; u < U; ++u) load(u, ring[i].X, ring[i].W);
     advance();
   }
-  if (left > 3)
-    wait_and_meet<3 * U>();
+  if (left >= R)
+    wait_and_meet<(R - 1) * U>();
   else
     wait_and_meet<0>();
 #pragma unroll
@@ -315,31 +332,47 @@ __global__ __launch_bounds__(128 * WN) void linear_tiles(LinArgs a, int mt, int 
   fw[0] = read_w(0, ring[0].W);
   fw[1] = read_w(1, ring[0].W);
 #pragma unroll 1
-  for (int i = 0, k = 0; left > 0; ++i, --left) {
-    Stage &c = ring[i & (kRing - 1)], &nx = ring[(i + 1) & (kRing - 1)];
-    step(left, c.X, c.W, c.W, nx.X, nx.W);
+  for (int i = 0, k = 0; left > 0; --left) {
+    Stage& c = ring[i];
+    i = i + 1 < R ? i + 1 : 0;
+    step(left, c.X, c.W, c.W, ring[i].X, ring[i].W);
     if (++k < steps) continue;
     k = 0;
     const Where at = tile_at(t, mt, nt, TM, TN);
     t += group;
     const int m = static_cast<int>(a.m), row0 = at.row + wr + n;
+    const bool whole = at.row + TM <= m && at.col + TN <= static_cast<int>(a.n);
+    // the tile's scales, through LDS: 16 + 16 + 8 loads a lane from memory would be one or more trips there
+    if (tid < TN) {
+      sScale[TM + tid] = a.sw[min(at.col + tid, static_cast<int>(a.n) - 1)];
+      sScale[TM + TN + tid] = a.bias ? a.bias[min(at.col + tid, static_cast<int>(a.n) - 1)] : 0.0f;
+    } else if (tid < TN + TM) {
+      sScale[tid - TN] = a.sx[min(at.row + tid - TN, m - 1)];
+    }
+    __asm__ volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+    static_assert(NT == 4 && TN + TM <= 128 * WN, "a lane's channels are one run of sixteen, one scale a thread");
+    const int c0 = wc + 16 * gq, count = static_cast<int>(a.n) - at.col - c0;
+    float sw[16], bias[16];
 #pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      const int col = at.col + wc + 16 * j + 8 * gq, count = min(static_cast<int>(a.n) - col, 8);
-      float sw[8], bias[8];
-      channel_scales(a, col, sw, bias);
+    for (int i = 0; i < 16; i += 4) {
+      *reinterpret_cast<float4*>(sw + i) = *reinterpret_cast<const float4*>(sScale + TM + c0 + i);
+      *reinterpret_cast<float4*>(bias + i) = *reinterpret_cast<const float4*>(sScale + TM + TN + c0 + i);
+    }
 #pragma unroll
-      for (int r = 0; r < MT; ++r) {
-        const int row = row0 + 16 * r;
-        if (row < m && count > 0) {
-          const float sx = a.sx[row];
-          const int64_t to = static_cast<int64_t>(row) * a.n + col;
-          if (count == 8)
-            store_whole<DT>(a, to, sx, sw, bias, acc[j][r], acc[j + 1][r]);
-          else
-            store_some<DT>(a, to, sx, sw, bias, acc[j][r], acc[j + 1][r], count);
-        }
-        acc[j][r] = acc[j + 1][r] = intx4{};
+    for (int r = 0; r < MT; ++r) {
+      const int row = row0 + 16 * r;
+      const int64_t to = static_cast<int64_t>(row) * a.n + at.col + c0;
+      const float sx = sScale[wr + 16 * r + n];
+#pragma unroll
+      for (int q = 0; q < 4; q += 2) {
+        if (whole || (row < m && count >= 4 * q + 8))
+          store_whole<DT>(a, to + 4 * q, sx, sw + 4 * q, bias + 4 * q, acc[q][r], acc[q + 1][r]);
+        else if (row < m && count > 4 * q)
+          store_some<DT>(a, to + 4 * q, sx, sw + 4 * q, bias + 4 * q, acc[q][r], acc[q + 1][r], count - 4 * q);
+        acc[q][r] = acc[q + 1][r] = intx4{};
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -355,16 +388,16 @@ void few_launch(const LinArgs& a, int dtype, hipStream_t st) {
     hipLaunchKernelGGL((linear_few<BLLM_BF16, MT>), grid, dim3(512), 0, st, a);
 }
 
-template <int TM, int TN, int WN>
+template <int TM, int TN, int WN, int R>
 void tiles_launch(const LinArgs& a, int dtype, hipStream_t st) {
   const int mt = static_cast<int>(ceil_div(a.m, TM)), nt = static_cast<int>(ceil_div(a.n, TN));
   // as many workgroups as the LDS of all CUs holds at once, each with several tiles
-  const int64_t most = kCus * (160 * 1024 / (kRing * (TM + TN) * kBK));
+  const int64_t most = kCus * (160 * 1024 / (R * (TM + TN) * kBK + 4 * (TM + 2 * TN)));
   const dim3 grid(static_cast<unsigned>(std::min(ceil_div(int64_t(mt) * nt, kXcds) * kXcds, most)));
   if (dtype == BLLM_F32)
-    hipLaunchKernelGGL((linear_tiles<BLLM_F32, TM, TN, WN>), grid, dim3(128 * WN), 0, st, a, mt, nt);
+    hipLaunchKernelGGL((linear_tiles<BLLM_F32, TM, TN, WN, R>), grid, dim3(128 * WN), 0, st, a, mt, nt);
   else
-    hipLaunchKernelGGL((linear_tiles<BLLM_BF16, TM, TN, WN>), grid, dim3(128 * WN), 0, st, a, mt, nt);
+    hipLaunchKernelGGL((linear_tiles<BLLM_BF16, TM, TN, WN, R>), grid, dim3(128 * WN), 0, st, a, mt, nt);
 }
 
 }  // namespace
@@ -384,15 +417,26 @@ extern "C" int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8
   if (m == 0) return BLLM_OK;
   LinArgs a{xq, x_scale, wq, w_scale, bias, y_out, m, n, static_cast<int>(k)};
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (m <= 16)
+  const int64_t col32 = ceil_div(n, 32);
+  // Few tokens: the fewest token tiles a workgroup that do not need more
+  // workgroups than CUs, so that K's waves are spread widest (us by 16, 32, 64
+  // tokens a workgroup: 100 x 1000, K 1024: 4.5, 5.2, 6.9; 300 x 1024, K 4096:
+  // 19.2, 17.6, 14.9).  Up to 64 tokens weights are read once whatever n is.
+  // Else the largest tile that at least half of the CUs (all of them for 128 x
+  // 128) get one of (64 x 128, 128 x 128, 256 x 256: 1024 x 2048, K 2048: 13.8,
+  // 17.3, 28.4; 1000 x 6144, K 1536: 24.0, 20.0, 26.0; 8192 x 1536, K 1536:
+  // 42.4, 33.5, 28.7).
+  if (ceil_div(m, 16) * col32 <= kCus || m <= 16)
     few_launch<1>(a, dtype, st);
-  else if (m <= 32)
+  else if (ceil_div(m, 32) * col32 <= kCus || m <= 32)
     few_launch<2>(a, dtype, st);
-  else if (ceil_div(m, 128) * ceil_div(n, 128) < 64)
+  else if (ceil_div(m, 64) * col32 <= kCus || m <= 64)
     few_launch<4>(a, dtype, st);
-  else if (ceil_div(m, 256) * ceil_div(n, 256) < kCus)
-    tiles_launch<128, 128, 2>(a, dtype, st);
+  else if (ceil_div(m, 256) * ceil_div(n, 256) >= kCus / 2)
+    tiles_launch<256, 256, 4, 4>(a, dtype, st);
+  else if (ceil_div(m, 128) * ceil_div(n, 128) >= kCus)
+    tiles_launch<128, 128, 2, 4>(a, dtype, st);
   else
-    tiles_launch<256, 256, 4>(a, dtype, st);
+    tiles_launch<64, 128, 2, 4>(a, dtype, st);
   return launch_status();
 }
