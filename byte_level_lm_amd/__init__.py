@@ -10,5 +10,5 @@ from .ops import (  # noqa: F401
     topk_select_window, gather_topk, upsample_bins, upsample_plan, upsample_apply,
     rmsnorm, rmsnorm_q8, quant_rows_q8, linear_i8, gated_delta, gated_delta_step,
     route_workspace, compact_workspace, dechunk_workspace, dechunk_ema_backward_workspace,
-    coding_rate_workspace, upsample_workspace, linear_i8_workspace, gated_delta_workspace,
+    coding_rate_workspace, upsample_workspace, gated_delta_workspace,
 )

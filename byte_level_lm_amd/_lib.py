@@ -55,8 +55,7 @@ _SIGS = {
     "bllm_rmsnorm": (C.c_int, [_p, _p, _p, C.c_int, _i64, _i64, C.c_double, _p, _p, _p]),
     "bllm_rmsnorm_q8": (C.c_int, [_p, _p, _p, C.c_int, _i64, _i64, C.c_double, _p, _p, _p, _p]),
     "bllm_quant_rows_q8": (C.c_int, [_p, C.c_int, _i64, _i64, _p, _p, _p]),
-    "bllm_linear_i8_workspace": (C.c_size_t, [_i64, _i64, _i64]),
-    "bllm_linear_i8": (C.c_int, [_p, _p, _p, _p, _p, C.c_int, _i64, _i64, _i64, _p, _p, C.c_size_t, _p]),
+    "bllm_linear_i8": (C.c_int, [_p, _p, _p, _p, _p, C.c_int, _i64, _i64, _i64, _p, _p]),
     "bllm_gated_delta_workspace": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64]),
     "bllm_gated_delta": (C.c_int, [_p, _p, _p, _p, _p, C.c_int, _p, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
                                    _i64, C.c_double, C.c_int, _p, _p, _p, _p, C.c_size_t, _p]),

@@ -405,11 +405,9 @@ void tiles_launch(const LinArgs& a, int dtype, hipStream_t st) {
 
 using namespace bllm;
 
-extern "C" size_t bllm_linear_i8_workspace(int64_t m, int64_t n, int64_t k) { return 0; }
-
 extern "C" int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
                               const float* bias, int dtype, int64_t m, int64_t n, int64_t k, void* y_out,
-                              void* ws, size_t ws_bytes, void* stream) {
+                              void* stream) {
   if (m < 0 || n < 1 || k < 1 || !wq || !w_scale || (m > 0 && (!xq || !x_scale || !y_out))) return BLLM_E_INVAL;
   if (!valid_dtype(dtype) || k % 16 != 0 || k > kMaxK || m > kMaxRows || n > kMaxRows || m * n > kMaxOut ||
       !aligned16(xq) || !aligned16(wq) || !aligned16(y_out))

@@ -6,8 +6,11 @@
 // r divides out of q, so q depends on no sum's order: it is the same whole
 // number whatever the split of the row over threads.
 //
-// One workgroup per row, two passes over it: the sum of squares and the
-// largest |t|, then the outputs.
+// Bound by the bytes: x and the residual are read once, held in registers as
+// they came (a row's 16-byte pieces over the lanes) and the outputs written
+// once.  A group of G lanes has a row, with P pieces each: part of a wave for
+// short rows (several rows a wave keep its loads in flight), a wave, or a
+// workgroup whose waves add up in LDS.  Rows of more than 64 KB are read twice.
 #include "common.h"
 
 namespace bllm {
@@ -29,82 +32,246 @@ struct NormArgs {
   float eps;
 };
 
-// 127 (1 / a) and the row's scale; zeros for rows that are too small to divide by
-__device__ inline void quant_scales(float a, float r, float* inv, float* scale) {
-  const bool some = !(a < kTiny);
-  *inv = some ? 127.0f * (1.0f / a) : 0.0f;
-  *scale = some ? a * r / 127.0f : 0.0f;
+template <int DT>
+__device__ inline void unpack(const uint4& v, float* x) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == BLLM_F32) {
+      x[i] = __uint_as_float(u[i]);
+    } else {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+}
+__device__ inline uint4 piece(const void* p, int64_t i) { return static_cast<const uint4*>(p)[i]; }
+
+// the row's divisor and 8-bit scales from its sum of squares and largest |t|
+struct RowScale {
+  float r, inv, scale;
+};
+__device__ inline RowScale row_scale(const NormArgs& a, float ss, float top) {
+  RowScale s;
+  // a NaN in the row is lost by the maximum but not by the sum: it reaches r, y and the scale
+  s.r = a.w ? 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps) : (ss == ss ? 1.0f : ss);
+  const bool some = !(top < kTiny);
+  s.inv = some ? 127.0f * (1.0f / top) : 0.0f;
+  s.scale = some ? top * s.r / 127.0f : 0.0f;
+  return s;
 }
 
-__device__ inline int quant1(float t, float inv) {
-  const float v = rintf(t * inv);
-  return static_cast<int>(fminf(fmaxf(v, -127.0f), 127.0f));
+// s of one piece: x (+ residual)
+template <int DT, bool RES>
+__device__ inline void sum_piece(const uint4& x, const uint4& res, float* s) {
+  constexpr int N = Vec<DT>::N;
+  unpack<DT>(x, s);
+  if (RES) {
+    float r[N];
+    unpack<DT>(res, r);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += r[i];
+  }
+}
+
+// writes one piece's outputs; i is the piece's number in the arrays
+template <int DT, bool RES, bool Q8>
+__device__ inline void put_piece(const NormArgs& a, int64_t i, float* s, const float* w, const RowScale& rs) {
+  constexpr int N = Vec<DT>::N;
+  if (RES && a.res_out) Vec<DT>::store(a.res_out, i * N, s);
+  if (Q8) {
+    uint32_t q[N / 4];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+      uint32_t u = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = rintf(s[4 * j + e] * w[4 * j + e] * rs.inv);
+        const int c = static_cast<int>(fminf(fmaxf(v, -127.0f), 127.0f));
+        u |= static_cast<uint32_t>(c & 0xFF) << (8 * e);
+      }
+      q[j] = u;
+    }
+    uint32_t* to = reinterpret_cast<uint32_t*>(a.q + i * N);
+    if constexpr (N == 8)
+      *reinterpret_cast<uint2*>(to) = make_uint2(q[0], q[1]);
+    else
+      *to = q[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = s[j] * w[j] * rs.r;
+    Vec<DT>::store(a.y, i * N, s);
+  }
 }
 
 template <int DT>
-__global__ __launch_bounds__(256) void norm_rows(NormArgs a) {
-  constexpr int N = Vec<DT>::N;
-  __shared__ float sSum[4], sMax[4];
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * a.d;
-  float ss = 0.0f, top = 0.0f;
-  for (int c = threadIdx.x * N; c < a.d; c += 256 * N) {
-    float s[N], r[N], w[N];
-    Vec<DT>::load(a.x, base + c, s);
-    if (a.res) Vec<DT>::load(a.res, base + c, r);
-    if (a.w) Vec<DT>::load(a.w, c, w);
+__device__ inline void weights(const NormArgs& a, int64_t c, float* w) {
+  if (a.w) {
+    unpack<DT>(piece(a.w, c), w);
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (a.res) s[i] += r[i];
-      ss += s[i] * s[i];
-      top = fmaxf(top, fabsf(a.w ? s[i] * w[i] : s[i]));
+    for (int i = 0; i < Vec<DT>::N; ++i) w[i] = 1.0f;
+  }
+}
+
+template <int G>
+__device__ inline float group_max(float v) {
+#pragma unroll
+  for (int off = G / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  return v;
+}
+
+// G <= 64: lanes of a wave, rows side by side.  G > 64: G threads, one row a workgroup.
+template <int DT, bool RES, bool Q8, int G, int P>
+__global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
+  constexpr int N = Vec<DT>::N, NT = G > 256 ? G : 256, GW = G < 64 ? G : 64;
+  __shared__ float sSum[16], sMax[16];
+  const int pieces = a.d / N, in = threadIdx.x % G;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (NT / G) + threadIdx.x / G;
+  if (G <= 64 && row >= a.rows) return;
+  const int64_t base = row * pieces;
+  uint4 x[P], r[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int c = in + p * G;
+    x[p] = r[p] = make_uint4(0, 0, 0, 0);
+    if (c < pieces) {
+      x[p] = piece(a.x, base + c);
+      if (RES) r[p] = piece(a.res, base + c);
     }
   }
-  ss = wave_sum(ss);
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  float ss = 0.0f, top = 0.0f;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int c = in + p * G;
+    if (c >= pieces) break;
+    float s[N], w[N];
+    sum_piece<DT, RES>(x[p], r[p], s);
+    if (Q8) weights<DT>(a, c, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      ss = fmaf(s[i], s[i], ss);
+      if (Q8) top = fmaxf(top, fabsf(s[i] * w[i]));
+    }
+  }
+  ss = group_sum<GW>(ss);
+  if (Q8) top = group_max<GW>(top);
+  if (G > 64) {
+    if ((threadIdx.x & 63) == 0) {
+      sSum[threadIdx.x >> 6] = ss;
+      sMax[threadIdx.x >> 6] = top;
+    }
+    __syncthreads();
+    ss = top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < G / 64; ++i) {
+      ss += sSum[i];
+      top = fmaxf(top, sMax[i]);
+    }
+  }
+  const RowScale rs = row_scale(a, ss, top);
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const int c = in + p * G;
+    if (c >= pieces) break;
+    float s[N], w[N];
+    sum_piece<DT, RES>(x[p], r[p], s);
+    weights<DT>(a, c, w);
+    put_piece<DT, RES, Q8>(a, base + c, s, w, rs);
+  }
+  if (Q8 && in == 0) a.scale[row] = rs.scale;
+}
+
+// rows too long for registers: two passes over memory
+template <int DT, bool RES, bool Q8>
+__global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
+  constexpr int N = Vec<DT>::N;
+  __shared__ float sSum[16], sMax[16];
+  const int pieces = a.d / N;
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * pieces;
+  float ss = 0.0f, top = 0.0f;
+  for (int c = threadIdx.x; c < pieces; c += 1024) {
+    float s[N], w[N];
+    sum_piece<DT, RES>(piece(a.x, base + c), RES ? piece(a.res, base + c) : uint4{}, s);
+    weights<DT>(a, c, w);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      ss = fmaf(s[i], s[i], ss);
+      top = fmaxf(top, fabsf(s[i] * w[i]));
+    }
+  }
+  ss = group_sum<64>(ss);
+  top = group_max<64>(top);
   if ((threadIdx.x & 63) == 0) {
     sSum[threadIdx.x >> 6] = ss;
     sMax[threadIdx.x >> 6] = top;
   }
   __syncthreads();
-  ss = sSum[0] + sSum[1] + sSum[2] + sSum[3];
-  top = fmaxf(fmaxf(sMax[0], sMax[1]), fmaxf(sMax[2], sMax[3]));
-  // a NaN in the row is lost by the maximum but not by the sum: it reaches r, y and the scale
-  const float r1 = a.w ? 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps) : (ss == ss ? 1.0f : ss);
-  float inv, scale;
-  quant_scales(top, r1, &inv, &scale);
-  for (int c = threadIdx.x * N; c < a.d; c += 256 * N) {
-    float s[N], r[N], w[N];
-    Vec<DT>::load(a.x, base + c, s);
-    if (a.res) Vec<DT>::load(a.res, base + c, r);
-    if (a.w) Vec<DT>::load(a.w, c, w);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (a.res) s[i] += r[i];
-    if (a.res_out) Vec<DT>::store(a.res_out, base + c, s);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (a.w) s[i] *= w[i];
-    if (a.q) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) a.q[base + c + i] = static_cast<int8_t>(quant1(s[i], inv));
-    }
-    if (a.y) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] *= r1;
-      Vec<DT>::store(a.y, base + c, s);
-    }
+  ss = top = 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    ss += sSum[i];
+    top = fmaxf(top, sMax[i]);
   }
-  if (a.q && threadIdx.x == 0) a.scale[blockIdx.x] = scale;
+  const RowScale rs = row_scale(a, ss, top);
+  for (int c = threadIdx.x; c < pieces; c += 1024) {
+    float s[N], w[N];
+    sum_piece<DT, RES>(piece(a.x, base + c), RES ? piece(a.res, base + c) : uint4{}, s);
+    weights<DT>(a, c, w);
+    put_piece<DT, RES, Q8>(a, base + c, s, w, rs);
+  }
+  if (Q8 && threadIdx.x == 0) a.scale[blockIdx.x] = rs.scale;
+}
+
+constexpr int64_t kFewRows = 4096;
+
+template <int DT, bool RES, bool Q8, int G, int P>
+void rows_launch(const NormArgs& a, hipStream_t st) {
+  constexpr int NT = G > 256 ? G : 256;
+  const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, NT / G)));
+  hipLaunchKernelGGL((norm_rows<DT, RES, Q8, G, P>), grid, dim3(NT), 0, st, a);
+}
+
+// The smallest group whose lanes hold the row in four pieces or fewer: more rows
+// a wave, more loads in flight (262144 x 512 in bf16 with the residual: 174 us).
+// A few rows only wait for their own chain, which a piece a lane makes shortest.
+template <int DT, bool RES, bool Q8>
+void norm_launch_as(const NormArgs& a, hipStream_t st) {
+  const int pieces = a.d / Vec<DT>::N;
+  if (a.rows <= kFewRows && pieces > 16 && pieces <= 64)
+    rows_launch<DT, RES, Q8, 64, 1>(a, st);
+  else if (pieces <= 16)
+    rows_launch<DT, RES, Q8, 16, 1>(a, st);
+  else if (pieces <= 32)
+    rows_launch<DT, RES, Q8, 16, 2>(a, st);
+  else if (pieces <= 64)
+    rows_launch<DT, RES, Q8, 16, 4>(a, st);
+  else if (pieces <= 128)
+    rows_launch<DT, RES, Q8, 64, 2>(a, st);
+  else if (pieces <= 256)
+    rows_launch<DT, RES, Q8, 64, 4>(a, st);
+  else if (pieces <= 1024)
+    rows_launch<DT, RES, Q8, 256, 4>(a, st);
+  else if (pieces <= 4096)
+    rows_launch<DT, RES, Q8, 1024, 4>(a, st);
+  else
+    hipLaunchKernelGGL((norm_long<DT, RES, Q8>), dim3(static_cast<unsigned>(a.rows)), dim3(1024), 0, st, a);
+}
+
+template <int DT>
+void norm_launch_type(const NormArgs& a, hipStream_t st) {
+  if (a.res)
+    a.q ? norm_launch_as<DT, true, true>(a, st) : norm_launch_as<DT, true, false>(a, st);
+  else
+    a.q ? norm_launch_as<DT, false, true>(a, st) : norm_launch_as<DT, false, false>(a, st);
 }
 
 int norm_launch(const NormArgs& a, int dtype, void* stream) {
   if (a.rows == 0) return BLLM_OK;
-  const dim3 grid(static_cast<unsigned>(a.rows));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (dtype == BLLM_F32)
-    hipLaunchKernelGGL(norm_rows<BLLM_F32>, grid, dim3(256), 0, st, a);
+    norm_launch_type<BLLM_F32>(a, st);
   else
-    hipLaunchKernelGGL(norm_rows<BLLM_BF16>, grid, dim3(256), 0, st, a);
+    norm_launch_type<BLLM_BF16>(a, st);
   return launch_status();
 }
 

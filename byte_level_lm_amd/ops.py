@@ -35,7 +35,8 @@ def _ptr(t):
 
 
 def _stream():
-    return torch.cuda.current_stream().cuda_stream
+    # the raw handle of torch.cuda.current_stream(), without building the Stream object
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ws(nbytes: int, ws, device):
@@ -365,61 +366,63 @@ def upsample_bins(g, W, idx, h, nbins: int, *, s_out=None, ws=None):
 
 
 # ------------------------------------------------------------------ mixer block in serving
-
-def linear_i8_workspace(m: int, n: int, k: int) -> int:
-    return int(L.lib().bllm_linear_i8_workspace(m, n, k))
-
+# A step of one byte makes a dozen of these calls, each a few microseconds on
+# the GPU: checks are plain comparisons, and outputs that the caller passes are
+# not allocated.
 
 def gated_delta_workspace(nseq: int, total: int, hv: int, dk: int, dv: int) -> int:
     return int(L.lib().bllm_gated_delta_workspace(nseq, total, hv, dk, dv))
 
 
-def _shape(name, t, shape, dtype=None):
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
-        want = list(shape) if dtype is None else f"{dtype} {list(shape)}"
-        raise ValueError(f"{name} must be {want}, got {t.dtype} {list(t.shape)}")
+def _is(name, t, shape, dtype):
+    """t is a dense GPU tensor of this shape and dtype."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        _dev(t)
+
+
+def _out(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _is(name, t, shape, dtype)
+    return t
 
 
 def _norm_args(x, w, residual, residual_out):
-    _dev(x, w, residual, residual_out)
+    _dev(x)
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
-    _shape("w", w, x.shape[1:], x.dtype)
-    _shape("residual", residual, x.shape, x.dtype)
-    _shape("residual_out", residual_out, x.shape, x.dtype)
-    if residual is None and residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    return torch.empty_like(x) if residual is not None and residual_out is None else residual_out
+    _is("w", w, x.shape[1:], x.dtype)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return None
+    _is("residual", residual, x.shape, x.dtype)
+    return _out("residual_out", residual_out, x.shape, x.dtype, x.device)
 
 
 def rmsnorm(x, w, *, eps: float = 1e-6, residual=None, y_out=None, residual_out=None):
     """RMS norm of the rows of x [rows, d] (plus residual), weighted by w [d]:
     returns (y, x + residual), the second None without a residual."""
     residual_out = _norm_args(x, w, residual, residual_out)
-    _dev(y_out)
-    _shape("y_out", y_out, x.shape, x.dtype)
-    y_out = torch.empty_like(x) if y_out is None else y_out
-    rc = L.lib().bllm_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), x.shape[0], x.shape[1], float(eps),
-                              _ptr(residual_out), y_out.data_ptr(), _stream())
+    rows, d = x.shape
+    y_out = _out("y_out", y_out, x.shape, x.dtype, x.device)
+    rc = L.lib().bllm_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), rows, d, eps, _ptr(residual_out),
+                              y_out.data_ptr(), _stream())
     L.check("bllm_rmsnorm", rc)
     return y_out, residual_out
-
-
-def _q8_outs(x, q_out, scale_out):
-    _dev(q_out, scale_out)
-    _shape("q_out", q_out, x.shape, torch.int8)
-    _shape("scale_out", scale_out, x.shape[:1], torch.float32)
-    return (torch.empty(x.shape, dtype=torch.int8, device=x.device) if q_out is None else q_out,
-            torch.empty(x.shape[0], dtype=torch.float32, device=x.device) if scale_out is None else scale_out)
 
 
 def rmsnorm_q8(x, w, *, eps: float = 1e-6, residual=None, q_out=None, scale_out=None, residual_out=None):
     """``rmsnorm`` with each row in 8 bits: returns (q int8 [rows, d], scale fp32
     [rows], x + residual or None); the row is q * scale."""
     residual_out = _norm_args(x, w, residual, residual_out)
-    q_out, scale_out = _q8_outs(x, q_out, scale_out)
-    rc = L.lib().bllm_rmsnorm_q8(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), x.shape[0], x.shape[1],
-                                 float(eps), _ptr(residual_out), q_out.data_ptr(), scale_out.data_ptr(), _stream())
+    rows, d = x.shape
+    q_out = _out("q_out", q_out, x.shape, torch.int8, x.device)
+    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x.device)
+    rc = L.lib().bllm_rmsnorm_q8(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), rows, d, eps,
+                                 _ptr(residual_out), q_out.data_ptr(), scale_out.data_ptr(), _stream())
     L.check("bllm_rmsnorm_q8", rc)
     return q_out, scale_out, residual_out
 
@@ -429,64 +432,62 @@ def quant_rows_q8(x, *, q_out=None, scale_out=None):
     _dev(x)
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
-    q_out, scale_out = _q8_outs(x, q_out, scale_out)
-    rc = L.lib().bllm_quant_rows_q8(x.data_ptr(), _dt(x), x.shape[0], x.shape[1], q_out.data_ptr(),
-                                    scale_out.data_ptr(), _stream())
+    rows, d = x.shape
+    q_out = _out("q_out", q_out, x.shape, torch.int8, x.device)
+    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x.device)
+    rc = L.lib().bllm_quant_rows_q8(x.data_ptr(), _dt(x), rows, d, q_out.data_ptr(), scale_out.data_ptr(), _stream())
     L.check("bllm_quant_rows_q8", rc)
     return q_out, scale_out
 
 
-def linear_i8(xq, x_scale, wq, w_scale, *, bias=None, out_dtype=torch.bfloat16, y_out=None, ws=None):
+def linear_i8(xq, x_scale, wq, w_scale, *, bias=None, out_dtype=torch.bfloat16, y_out=None):
     """y [m, n] = (xq @ wq.T) * x_scale[:, None] * w_scale + bias for int8 xq [m, k]
-    and wq [n, k], exact integer sums, rounded once to out_dtype."""
-    _dev(xq, x_scale, wq, w_scale, bias, y_out)
-    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
-        raise ValueError("xq must be [m, k] and wq [n, k]")
-    m, k = xq.shape
-    n = wq.shape[0]
+    and wq [n, k], exact integer sums, rounded once to out_dtype (y_out's dtype if given)."""
     if xq.dtype != torch.int8 or wq.dtype != torch.int8:
         raise TypeError("xq and wq must be int8")
-    _shape("x_scale", x_scale, (m,), torch.float32)
-    _shape("w_scale", w_scale, (n,), torch.float32)
-    _shape("bias", bias, (n,), torch.float32)
-    _shape("y_out", y_out, (m, n))
-    y_out = torch.empty((m, n), dtype=out_dtype, device=xq.device) if y_out is None else y_out
-    need = linear_i8_workspace(m, n, k)
-    w = _ws(need, ws, xq.device) if need else ws
+    if xq.dim() != 2 or wq.dim() != 2 or xq.shape[1] != wq.shape[1]:
+        raise ValueError("xq must be [m, k] and wq [n, k]")
+    _dev(xq, wq)
+    m, k = xq.shape
+    n = wq.shape[0]
+    _is("x_scale", x_scale, (m,), torch.float32)
+    _is("w_scale", w_scale, (n,), torch.float32)
+    if bias is not None:
+        _is("bias", bias, (n,), torch.float32)
+    y_out = _out("y_out", y_out, (m, n), out_dtype if y_out is None else y_out.dtype, xq.device)
     rc = L.lib().bllm_linear_i8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), _ptr(bias),
-                                _dt(y_out), m, n, k, y_out.data_ptr(), _ptr(w), 0 if w is None else _nbytes(w),
-                                _stream())
+                                _dt(y_out), m, n, k, y_out.data_ptr(), _stream())
     L.check("bllm_linear_i8", rc)
     return y_out
 
 
-def _token_stride(name, t, heads, width):
+def _token_stride(name, t, total, heads, width):
     """Distance between tokens of t [total, heads, width], whose heads are dense."""
+    if t.shape != (total, heads, width):
+        raise ValueError(f"{name} must be [{total}, {heads}, {width}], got {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU")
-    if t.dim() != 3 or (heads and t.shape[1] != heads) or (width and t.shape[2] != width):
-        raise ValueError(f"{name} must be [tokens, heads, width], got {list(t.shape)}")
-    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    s0, s1, s2 = t.stride()
+    if (width > 1 and s2 != 1) or (heads > 1 and s1 != width):
         raise ValueError(f"the heads of a token of {name} must be dense")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return s0 if total > 1 else heads * width
 
 
 def _delta_args(q, k, v, g, beta, o_out):
-    qs = _token_stride("q", q, 0, 0)
+    if q.dim() != 3 or v.dim() != 3 or q.shape[0] != v.shape[0]:
+        raise ValueError("q, k and v must be [tokens, heads, width] with the same tokens")
     total, hk, dk = q.shape
-    ks, vs = _token_stride("k", k, hk, dk), _token_stride("v", v, 0, 0)
-    hv, dv = v.shape[1:]
-    if k.shape[0] != total or v.shape[0] != total:
-        raise ValueError("q, k and v must hold the same tokens")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    _, hv, dv = v.shape
+    strides = (_token_stride("q", q, total, hk, dk), _token_stride("k", k, total, hk, dk),
+               _token_stride("v", v, total, hv, dv))
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
         raise TypeError("q, k and v must have one dtype")
-    _dev(g, beta, o_out)
-    _shape("g", g, (total, hv), torch.float32)
-    _shape("beta", beta, (total, hv), torch.float32)
-    _shape("o_out", o_out, (total, hv, dv), q.dtype)
-    o_out = torch.empty((total, hv, dv), dtype=q.dtype, device=q.device) if o_out is None else o_out
-    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q)), (total, hk, hv, dk, dv,
-                                                                                              qs, ks, vs), o_out
+    _is("g", g, (total, hv), torch.float32)
+    _is("beta", beta, (total, hv), torch.float32)
+    o_out = _out("o_out", o_out, (total, hv, dv), dt, q.device)
+    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q)),
+            (hk, hv, dk, dv, *strides), o_out)
 
 
 def gated_delta(q, k, v, g, beta, offsets, *, scale=None, unit_qk: bool = True, state_in=None, state_out=None,
@@ -495,21 +496,22 @@ def gated_delta(q, k, v, g, beta, offsets, *, scale=None, unit_qk: bool = True, 
     be strided), g and beta fp32 [total, hv], offsets int64 [nseq + 1].  Returns (o [total, hv, dv],
     state fp32 [nseq, hv, dk, dv] or None); state_out may be state_in (updated in place).  scale
     defaults to dk ** -0.5; unit_qk scales every q and k row to unit length first."""
-    ptrs, (total, hk, hv, dk, dv, *strides), o_out = _delta_args(q, k, v, g, beta, o_out)
-    _dev(offsets, state_in, state_out)
+    ptrs, dims, o_out = _delta_args(q, k, v, g, beta, o_out)
+    hk, hv, dk, dv = dims[:4]
     if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 2:
         raise ValueError("offsets must be int64 [nseq + 1]")
-    nseq = offsets.numel() - 1
+    _dev(offsets)
+    total, nseq = q.shape[0], offsets.shape[0] - 1
     shape = (nseq, hv, dk, dv)
-    _shape("state_in", state_in, shape, torch.float32)
-    _shape("state_out", state_out, shape, torch.float32)
+    if state_in is not None:
+        _is("state_in", state_in, shape, torch.float32)
     if not want_state:
         state_out = None
-    elif state_out is None:
-        state_out = torch.empty(shape, dtype=torch.float32, device=q.device)
+    else:
+        state_out = _out("state_out", state_out, shape, torch.float32, q.device)
     w = _ws(gated_delta_workspace(nseq, total, hv, dk, dv), ws, q.device)
-    rc = L.lib().bllm_gated_delta(*ptrs, offsets.data_ptr(), nseq, total, hk, hv, dk, dv, *strides,
-                                  dk ** -0.5 if scale is None else float(scale), 1 if unit_qk else 0, _ptr(state_in),
+    rc = L.lib().bllm_gated_delta(*ptrs, offsets.data_ptr(), nseq, total, *dims,
+                                  dk ** -0.5 if scale is None else scale, 1 if unit_qk else 0, _ptr(state_in),
                                   _ptr(state_out), o_out.data_ptr(), w.data_ptr(), _nbytes(w), _stream())
     L.check("bllm_gated_delta", rc)
     return o_out, state_out
@@ -520,16 +522,18 @@ def gated_delta_step(q, k, v, g, beta, state, *, state_out=None, slots=None, sca
     """One token of each stream: q, k [nseq, hk, dk], v [nseq, hv, dv], g and beta [nseq, hv].  state
     fp32 [nslots, hv, dk, dv] is updated in place unless state_out is given; stream s has row
     slots[s] (int32, row s without slots).  Returns (o [nseq, hv, dv], the state written)."""
-    ptrs, (nseq, hk, hv, dk, dv, *strides), o_out = _delta_args(q, k, v, g, beta, o_out)
-    state_out = state if state_out is None else state_out
-    _dev(state, state_out, slots)
-    nslots = state.shape[0]
-    _shape("state", state, (nslots, hv, dk, dv), torch.float32)
-    _shape("state_out", state_out, (nslots, hv, dk, dv), torch.float32)
-    _shape("slots", slots, (nseq,), torch.int32)
-    rc = L.lib().bllm_gated_delta_step(*ptrs, nseq, hk, hv, dk, dv, *strides,
-                                       dk ** -0.5 if scale is None else float(scale), 1 if unit_qk else 0,
-                                       state.data_ptr(), state_out.data_ptr(), _ptr(slots), nslots, o_out.data_ptr(),
-                                       _stream())
+    ptrs, dims, o_out = _delta_args(q, k, v, g, beta, o_out)
+    hk, hv, dk, dv = dims[:4]
+    nseq, nslots = q.shape[0], state.shape[0]
+    _is("state", state, (nslots, hv, dk, dv), torch.float32)
+    if state_out is None:
+        state_out = state
+    else:
+        _is("state_out", state_out, state.shape, torch.float32)
+    if slots is not None:
+        _is("slots", slots, (nseq,), torch.int32)
+    rc = L.lib().bllm_gated_delta_step(*ptrs, nseq, *dims, dk ** -0.5 if scale is None else scale,
+                                       1 if unit_qk else 0, state.data_ptr(), state_out.data_ptr(), _ptr(slots),
+                                       nslots, o_out.data_ptr(), _stream())
     L.check("bllm_gated_delta_step", rc)
     return o_out, state_out

@@ -433,17 +433,14 @@ int bllm_quant_rows_q8(const void* x, int dtype, int64_t rows, int64_t d, int8_t
  * xq : int8 [m x k], x_scale : fp32 [m] (each token's scale);
  * wq : int8 [n x k] (one row for each output channel), w_scale : fp32 [n];
  * bias : fp32 [n] or NULL; y_out : [m x n] of dtype.
- * ws : bllm_linear_i8_workspace(m, n, k) bytes (0 for most sizes; then ws
- *      may be NULL).
  * Errors : BLLM_E_INVAL for null pointers (xq, x_scale and y_out may be NULL
  *          when m = 0), m < 0, n < 1, k < 1; BLLM_E_NOTSUP for a bad dtype, k
  *          not a multiple of 16 or above 131056, m or n above 2^31 - 1025, m n
- *          above 2^44, unaligned xq, wq or y_out; BLLM_E_WS.
+ *          above 2^44, unaligned xq, wq or y_out.
  */
-size_t bllm_linear_i8_workspace(int64_t m, int64_t n, int64_t k);
 int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, const float* w_scale,
-                   const float* bias, int dtype, int64_t m, int64_t n, int64_t k, void* y_out, void* ws,
-                   size_t ws_bytes, void* stream);
+                   const float* bias, int dtype, int64_t m, int64_t n, int64_t k, void* y_out,
+                   void* stream);
 
 /*
  * bllm_gated_delta -- the gated delta rule over a ragged batch.  Per sequence

@@ -33,12 +33,11 @@ def test_norm_refusals(L):
 
 def test_linear_refusals(L):
     lin = lambda x=P, sx=P, w=P, sw=P, dt=1, m=4, n=4, k=64, y=P: L.bllm_linear_i8(  # noqa: E731
-        x, sx, w, sw, None, dt, m, n, k, y, None, 0, None)
+        x, sx, w, sw, None, dt, m, n, k, y, None)
     assert lin(x=None) == lin(sx=None) == lin(w=None) == lin(sw=None) == lin(y=None) == lin(m=-1) == lin(n=0) == lin(k=0) == -1
     assert lin(dt=3) == lin(k=24) == lin(k=131072) == lin(x=ODD) == lin(w=ODD) == lin(y=ODD) == lin(m=1 << 31) == -2
     assert lin(n=1 << 31) == -2
     assert lin(m=0, x=None, sx=None, y=None) == 0
-    assert L.bllm_linear_i8_workspace(0, 4, 64) == 0
 
 
 def test_delta_refusals(L):
