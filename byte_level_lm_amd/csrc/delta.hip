@@ -160,15 +160,14 @@ typedef float floatx2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kC = 64;            // tokens of a block
-constexpr int kTFloats = 12 * 256;  // T: 12 tiles of 64 lanes x 4 floats (16 x 16 entries on or below the diagonal)
-constexpr int kPWords = 6 * 512;    // P: 6 fragments of 64 lanes x 8 (16 x 32 entries) in two bf16 terms
-constexpr int kRec = kTFloats + kPWords + 256;  // one block and head in the workspace, in 4-byte words
+// One block and head in the workspace, in 4-byte words: T - I and P, each 6 fragments of 64 lanes x 8
+// (16 x 32 entries on or below the diagonal) in two bf16 terms, then beta and the decays of the tokens
+constexpr int kFrags = 6 * 512;
+constexpr int kRec = 2 * kFrags + 256 + 64;
 constexpr int kLd = 68;           // pitch of a 64 x 64 fp32 tile in LDS
 constexpr float kForget = -1e4f;  // smaller gates decay by e^-10000 = 0 as well, and their sums stay finite
 
-// Fragment f of P belongs to row tile frag_row(f) and inner tokens 32 frag_k(f) .. + 31;
-// the scan's two waves of a pair take the tiles of one parity each and number
-// tiles from their own on, so an odd tile's inner index has its fours swapped.
+// fragment f of T and P: row tile frag_row(f), inner tokens 32 frag_k(f) .. + 31
 __device__ constexpr int frag_row(int f) { return f < 2 ? f : 2 + (f & 1); }
 __device__ constexpr int frag_k(int f) { return f < 4 ? 0 : 1; }
 // token (or row of the state) of row r of tile i: pairs of tiles interleave in fours
@@ -215,33 +214,54 @@ __device__ inline void cut_pair(const floatx4& a, const floatx4& b, bf16x8* f) {
   for (int i = 0; i < N; ++i) f[i] = as_frag(w + 4 * i);
 }
 
+// Barrier for what the waves exchange through LDS: waits for the wave's own LDS
+// operations, not for loads and stores of memory.
+__device__ inline void exchange_barrier() {
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+}
+
 struct Block {
   int64_t first, left;  // its first token; tokens from there to the sequence's end
 };
 
+// the same value in every lane, told to the compiler
+__device__ inline int64_t uniform(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+  const int hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+  return static_cast<int64_t>(hi) << 32 | lo;
+}
+
 // sequence s of the batch, cut at its rows
 __device__ inline void seq_span(const DeltaArgs& a, int s, int64_t* t0, int64_t* t1) {
-  *t0 = min(max(a.offsets[s], int64_t(0)), a.total);
-  *t1 = min(max(a.offsets[s + 1], *t0), a.total);
+  *t0 = uniform(min(max(a.offsets[s], int64_t(0)), a.total));
+  *t1 = uniform(min(max(a.offsets[s + 1], *t0), a.total));
 }
 
 // Block j of the workspace: sequence s has blocks offsets[s] / 64 + s and on,
 // which leaves room for every sequence's last, partial block.
 __device__ inline bool find_block(const DeltaArgs& a, int64_t j, Block* b) {
-  int lo = 0, hi = a.nseq;  // the sequence is in [lo, hi)
-  while (hi - lo > 1) {     // every lane asks about one of 64 places at once
-    const int step = (hi - lo + kWave - 1) / kWave, at = lo + lane_id() * step;
-    const bool before = at < hi && min(max(a.offsets[at], int64_t(0)), a.total) / kC + at <= j;
+  int lo = 0, hi = a.nseq;  // the sequence is in [lo, hi); every lane asks about one of 64 places at once
+  for (;;) {
+    const int step = (hi - lo + kWave - 1) / kWave, at = min(lo + lane_id() * step, a.nseq);
+    const int64_t off = min(max(a.offsets[at], int64_t(0)), a.total);
+    const bool before = lo + lane_id() * step < hi && off / kC + at <= j;
     const int k = max(__popcll(__ballot(before)) - 1, 0);
+    if (step == 1) {
+      const int s = __builtin_amdgcn_readfirstlane(lo + k);
+      const int64_t t0 = __shfl(off, k, kWave);
+      // the next offset is the next lane's, if there is one
+      int64_t t1 = k + 1 < kWave ? __shfl(off, k + 1, kWave) : min(a.offsets[s + 1], a.total);
+      t1 = max(t1, t0);
+      b->first = uniform(t0 + (j - (t0 / kC + s)) * kC);
+      b->left = uniform(t1) - b->first;
+      return b->first >= uniform(t0) && b->left > 0;
+    }
     lo += k * step;
     hi = min(hi, lo + step);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  int64_t t0, t1;
-  seq_span(a, lo, &t0, &t1);
-  b->first = t0 + (j - (t0 / kC + lo)) * kC;
-  b->left = t1 - b->first;
-  return b->first >= t0 && b->left > 0;
 }
 
 // A block's rows of one head as a buffer: pieces past the last row, and pieces
@@ -254,8 +274,9 @@ constexpr int64_t kMaxStride = 1 << 22;
 
 __device__ inline Rows rows_of(const uint16_t* base, int64_t stride, const Block& b, int width) {
   const int n = static_cast<int>(min(b.left, int64_t(kC)));
-  const int bytes = n > 0 ? 2 * ((n - 1) * static_cast<int>(stride) + width) : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + b.first * stride), 0, bytes, 0x00027000);
+  const int bytes = __builtin_amdgcn_readfirstlane(n > 0 ? 2 * ((n - 1) * static_cast<int>(stride) + width) : 0);
+  const int64_t at = uniform(reinterpret_cast<int64_t>(base + b.first * stride));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<uint16_t*>(at), 0, bytes, 0x00027000);
 }
 __device__ inline int piece_at(int row, int64_t stride, int col, int width) {
   return col < width ? 2 * (row * static_cast<int>(stride) + col) : kOutside;
@@ -285,15 +306,54 @@ __device__ inline float square_sum(const uint4& v) {
   return s;
 }
 
-// T, P and the decays of one block and head.  Wave w has rows 16 w .. 16 w + 15
-// of K K^T and Q K^T.  (I + A)^-1: the 16 x 16 blocks on the diagonal by
-// substitution (a lane a column), then two doublings,
-//   [T1 0; -T2 A21 T1 T2],
-// on fp32 MFMA, whose accumulators feed the second product as they are.
-// Gates are summed in fp64, in units of ln 2, so that a difference of two sums
-// is as good as an fp32 gate however far the block has decayed.
+// inclusive sum over the lanes of a wave, in fp64, by row shifts and readlanes
+template <int N>
+__device__ inline double row_shr(double v) {
+  const int64_t u = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), 0x110 + N, 0xF, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), 0x110 + N, 0xF, 0xF, true);
+  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo));
+}
+__device__ inline double lane_value(double v, int lane) {
+  const int64_t u = __double_as_longlong(v);
+  const int lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+  const int hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+  return __longlong_as_double(static_cast<int64_t>(hi) << 32 | static_cast<uint32_t>(lo));
+}
+__device__ inline double wave_sums(double v) {
+  v += row_shr<1>(v);
+  v += row_shr<2>(v);
+  v += row_shr<4>(v);
+  v += row_shr<8>(v);
+  const double t0 = lane_value(v, 15), t1 = lane_value(v, 31) + t0, t2 = lane_value(v, 47) + t1;
+  const int r = lane_id() >> 4;
+  return r == 0 ? v : v + (r == 1 ? t0 : r == 2 ? t1 : t2);
+}
+
+// products of 16 x 16 fp32 blocks on MFMA: inner index 4 (lane / 16) + r at step r,
+// which is how an accumulator already holds it
+__device__ inline floatx4 mfma_f32(const float* a, const floatx4& b, floatx4 c) {
+  const float4 v = *reinterpret_cast<const float4*>(a);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(v.x, b[0], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(v.y, b[1], c, 0, 0, 0);
+  c = __builtin_amdgcn_mfma_f32_16x16x4f32(v.z, b[2], c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(v.w, b[3], c, 0, 0, 0);
+}
+__device__ inline floatx4 column4(const float* t) {  // entries r kLd of a column
+  return floatx4{t[0], t[kLd], t[2 * kLd], t[3 * kLd]};
+}
+
+// T - I, P and the decays of one block and head, T = (I + A)^-1.
+// Waves 0 and 1 form K K^T and from it A in LDS, waves 2 and 3 K Q^T, which
+// gives P in the order of its fragments (a lane a row, its accumulator four
+// consecutive columns).  The inverse: 8 x 8 blocks on the diagonal by
+// substitution, a lane a column, then three doublings [T1 0; -T2 A21 T1 T2] on
+// fp32 MFMA, whose accumulators feed the second product as they are.  Gates
+// are summed in fp64, in units of ln 2, so that a difference of two sums is as
+// good as an fp32 gate however far the block has decayed.  What bounds it is
+// the chain of these steps at four workgroups a CU.
 template <int DKP>
-__global__ __launch_bounds__(256) void delta_prep(DeltaArgs a, float* ws) {
+__global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
   constexpr int NS = DKP / 32;
   constexpr int NP = DKP / 32;     // pieces of K (and of Q) a thread stages
   constexpr int G16 = DKP / 8;     // lanes that hold a row
@@ -320,22 +380,9 @@ __global__ __launch_bounds__(256) void delta_prep(DeltaArgs a, float* ws) {
     pk[i] = piece(K, piece_at(row, a.ks, 8 * p, a.dk));
     pq[i] = piece(Q, piece_at(row, a.qs, 8 * p, a.dk));
   }
+  const int64_t mine = (blk.first + min(static_cast<int64_t>(lane), blk.left - 1)) * a.hv + h;
+  const float g = a.g[mine], be = lane < blk.left ? a.beta[mine] : 0.0f;
   if (tid == 0) sBad = kC;
-  if (w == 0) {
-    double b = 0.0;
-    float be = 0.0f;
-    if (lane < blk.left) {
-      const float g = a.g[(blk.first + lane) * a.hv + h];
-      b = (g < kForget ? kForget : g) * 1.4426950408889634;  // a NaN stays
-      be = a.beta[(blk.first + lane) * a.hv + h];
-    }
-    for (int off = 1; off < kC; off <<= 1) {
-      const double up = __shfl_up(b, off, kWave);
-      if (lane >= off) b += up;
-    }
-    sB[lane] = b;
-    sBeta[lane] = be;
-  }
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int e = i * 256 + tid, row = e / G16, p = e % G16;
@@ -343,73 +390,127 @@ __global__ __launch_bounds__(256) void delta_prep(DeltaArgs a, float* ws) {
     *reinterpret_cast<uint4*>(sQ + swz<DKP>(row, p)) = pq[i];
     const float kk = group_sum<G16>(square_sum(pk[i])), qq = group_sum<G16>(square_sum(pq[i]));
     if (p == 0) {
-      sRk[row] = kk;
-      sRq[row] = qq;
+      sRk[row] = a.unit ? 1.0f / sqrtf(kk + kL2Eps) : 1.0f;
+      sRq[row] = a.unit ? 1.0f / sqrtf(qq + kL2Eps) : 1.0f;
     }
+  }
+  if (w == 0) {
+    const double b = wave_sums(lane < blk.left ? (g < kForget ? kForget : g) * 1.4426950408889634 : 0.0);
+    sB[lane] = b;  // a NaN stays
+    sBeta[lane] = be;
   }
   __syncthreads();
-  floatx4 G[4] = {}, P[4] = {};
+  float* rec = ws + (static_cast<int64_t>(blockIdx.x) * a.hv + h) * kRec;
+  if (w < 2) {
+    // rows 16 i of K K^T: wave 0 has i = 3 and 0, wave 1 has i = 2 and 1
+    const int i0 = 3 - w, i1 = w;
+    floatx4 G0[4] = {}, G1[2] = {};
 #pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    const int at = swz<DKP>(16 * w + n, 4 * s + gq);
-    const bf16x8 fk = as_frag(*reinterpret_cast<const uint4*>(sK + at));
-    const bf16x8 fq = as_frag(*reinterpret_cast<const uint4*>(sQ + at));
+    for (int s = 0; s < NS; ++s) {
+      bf16x8 f[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c > w) continue;
-      const bf16x8 fb = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(16 * c + n, 4 * s + gq)));
-      G[c] = mfma_bf(fk, fb, G[c]);
-      P[c] = mfma_bf(fq, fb, P[c]);
+      for (int c = 0; c < 4; ++c) f[c] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(16 * c + n, 4 * s + gq)));
+      const bf16x8 f0 = w ? f[2] : f[3], f1 = w ? f[1] : f[0];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) G0[c] = mfma_bf(f0, f[c], G0[c]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) G1[c] = mfma_bf(f1, f[c], G1[c]);
     }
-  }
-  if (a.unit && tid < 2 * kC) {
-    float* r = tid < kC ? sRk + tid : sRq + tid - kC;
-    *r = 1.0f / sqrtf(*r + kL2Eps);
-  } else if (tid < 2 * kC) {
-    (tid < kC ? sRk[tid] : sRq[tid - kC]) = 1.0f;
-  }
-  __syncthreads();
-  {
-    double bt[4];
-    float at[4], pt[4];
+    exchange_barrier();  // K and Q have been read
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int t = 16 * w + 4 * gq + r;
-      bt[r] = sB[t];
-      at[r] = sBeta[t] * sRk[t];
-      pt[r] = a.scale * sRq[t];
-      // a token's own gates also reach T through its column, and the state
-      if (!(fabsf(at[r]) < INFINITY && fabs(bt[r]) < INFINITY)) atomicMin(&sBad, t);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      if (c > w) continue;
-      const int i = 16 * c + n;
-      const double bi = sB[i];
-      const float ri = sRk[i];
-      bool lost = false;
+    for (int part = 0; part < 2; ++part) {
+      const int i = part ? i1 : i0;
+      double bt[4];
+      float at[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int t = 16 * w + 4 * gq + r;
-        const float f = __builtin_amdgcn_exp2f(static_cast<float>(bt[r] - bi)) * ri;
-        const float av = i < t ? at[r] * f * G[c][r] : 0.0f;
-        const bool fine = fabsf(av) < INFINITY;
-        lost |= !fine;
-        P[c][r] = i <= t ? pt[r] * f * P[c][r] : 0.0f;
-        G[c][r] = fine ? av : 0.0f;
-        if (__builtin_expect(!fine, 0)) atomicMin(&sBad, t);
+        const int t = 16 * i + 4 * gq + r;
+        bt[r] = sB[t];
+        at[r] = sBeta[t] * sRk[t];
+        // a token's own gates also reach T through its column, and the state
+        if (!(fabsf(at[r]) < INFINITY && fabs(bt[r]) < INFINITY)) atomicMin(&sBad, t);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) sA[(16 * w + 4 * gq + r) * kLd + i] = G[c][r];
+      for (int c = 0; c < (part ? 2 : 4); ++c) {
+        if (c > i) continue;
+        const int u = 16 * c + n;
+        const double bu = sB[u];
+        const float ru = sRk[u];
+        const floatx4 G = part ? G1[c & 1] : G0[c];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * i + 4 * gq + r;
+          const float f = __builtin_amdgcn_exp2f(static_cast<float>(bt[r] - bu)) * ru;
+          float av = u < t ? at[r] * f * G[r] : 0.0f;
+          if (__builtin_expect(!(fabsf(av) < INFINITY), 0)) {
+            atomicMin(&sBad, t);
+            av = 0.0f;
+          }
+          sA[t * kLd + u] = av;
+        }
+      }
+    }
+  } else {
+    // columns of P^T: wave 2 the even row tiles of P, wave 3 the odd ones, each against tiles 0, 1 and then 0 .. 3
+    const int odd = w - 2;
+    floatx4 P[6] = {};
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      bf16x8 fk[4], fq[2];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        fk[c] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(tile_row(c, n), 4 * s + gq)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(2 * i, n) + 4 * odd, 4 * s + gq)));
+      P[0] = mfma_bf(fk[0], fq[0], P[0]);
+      P[1] = mfma_bf(fk[1], fq[0], P[1]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) P[2 + c] = mfma_bf(fk[c], fq[1], P[2 + c]);
+    }
+    exchange_barrier();
+#pragma unroll
+    for (int f = 0; f < 3; ++f) {  // fragments odd, 2 + odd, 4 + odd
+      const int t = tile_row(f ? 2 : 0, n) + 4 * odd, c0 = f == 2 ? 2 : 0;
+      const double bt = sB[t];
+      const float pt = a.scale * sRq[t];
+      uint32_t p[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int u = tile_row(c0 + c, 4 * gq);
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(static_cast<float>(bt - sB[u + r]));
+          v[r] = u + r <= t ? pt * sRk[u + r] * e * P[2 * f + c][r] : 0.0f;
+        }
+        cut<2>(v[0], v[1], p + 2 * c, 4);
+        cut<2>(v[2], v[3], p + 2 * c + 1, 4);
+      }
+      uint4* to = reinterpret_cast<uint4*>(rec + kFrags) + 128 * (2 * f + odd) + lane;
+      to[0] = make_uint4(p[0], p[1], p[2], p[3]);
+      to[64] = make_uint4(p[4], p[5], p[6], p[7]);
+    }
+    if (w == 3) {
+      float* c = rec + 2 * kFrags;
+      const double b = sB[lane], end = sB[kC - 1];
+      const float e = __builtin_amdgcn_exp2f(static_cast<float>(b)), bb = sBeta[lane];
+      c[lane] = bb * e * sRk[lane];
+      c[64 + lane] = e * sRq[lane] * a.scale;
+      c[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - b)) * sRk[lane];
+      c[192 + lane] = bb;
+      if (lane == 0) c[256] = __builtin_amdgcn_exp2f(static_cast<float>(end));
     }
   }
-  __syncthreads();
-  {  // diagonal blocks: column n of the inverse of rows 16 w ..
-    float x[16];
-    const float* A = sA + 16 * w * kLd + 16 * w;
+  exchange_barrier();
+  // rows 16 w .. of the inverse: two 8 x 8 blocks, lane (block, column), zeros between them
+  if (lane < 16) {
+    const int d = 16 * w + (n & 8);
+    const float* A = sA + d * kLd + d;
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == n ? 1.0f : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      float v = i == (n & 7) ? 1.0f : 0.0f;
 #pragma unroll
       for (int m = 0; m < i; m += 4) {
         const float4 r = *reinterpret_cast<const float4*>(A + i * kLd + m);
@@ -420,129 +521,102 @@ __global__ __launch_bounds__(256) void delta_prep(DeltaArgs a, float* ws) {
       }
       x[i] = v;
     }
+    float* T = sT + 16 * w * kLd + 16 * w + n;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (gq == 0) sT[(16 * w + i) * kLd + 16 * w + n] = x[i];
+    for (int i = 0; i < 8; ++i) {
+      T[(i + (n & 8)) * kLd] = x[i];
+      T[(i + 8 - (n & 8)) * kLd] = 0.0f;
+    }
   }
-  __syncthreads();
-  if (w < 2) {  // 32 x 32 blocks: below the diagonal of pair w
+  {  // 16 x 16: the wave's own block, so no barrier; A's entries outside the lower left 8 x 8 are left out
+    float* T = sT + 16 * w * kLd + 16 * w;
+    const float* A = sA + 16 * w * kLd + 16 * w;
+    __builtin_amdgcn_wave_barrier();
+    floatx4 m = {}, o = {};
+    const floatx4 t1 = column4(T + 4 * gq * kLd + n);
+    const float4 ar = *reinterpret_cast<const float4*>(A + n * kLd + 4 * gq);
+    const bool low = n >= 8 && gq < 2;
+    m = __builtin_amdgcn_mfma_f32_16x16x4f32(low ? ar.x : 0.0f, t1[0], m, 0, 0, 0);
+    m = __builtin_amdgcn_mfma_f32_16x16x4f32(low ? ar.y : 0.0f, t1[1], m, 0, 0, 0);
+    m = __builtin_amdgcn_mfma_f32_16x16x4f32(low ? ar.z : 0.0f, t1[2], m, 0, 0, 0);
+    m = __builtin_amdgcn_mfma_f32_16x16x4f32(low ? ar.w : 0.0f, t1[3], m, 0, 0, 0);
+    o = mfma_f32(T + n * kLd + 4 * gq, m, o);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n < 8 && gq >= 2) T[(4 * gq + r) * kLd + n] = -o[r];
+  }
+  exchange_barrier();
+  if (w < 2) {  // 32 x 32: below the diagonal of pair w
     const int lo = 32 * w, up = 32 * w + 16;
     floatx4 m = {}, o = {};
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      m = __builtin_amdgcn_mfma_f32_16x16x4f32(sA[(up + n) * kLd + lo + 4 * gq + r],
-                                               sT[(lo + 4 * gq + r) * kLd + lo + n], m, 0, 0, 0);
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      o = __builtin_amdgcn_mfma_f32_16x16x4f32(sT[(up + n) * kLd + up + 4 * gq + r], m[r], o, 0, 0, 0);
+    m = mfma_f32(sA + (up + n) * kLd + lo + 4 * gq, column4(sT + (lo + 4 * gq) * kLd + lo + n), m);
+    o = mfma_f32(sT + (up + n) * kLd + up + 4 * gq, m, o);
 #pragma unroll
     for (int r = 0; r < 4; ++r) sT[(up + 4 * gq + r) * kLd + lo + n] = -o[r];
   } else {  // and zeros above it
 #pragma unroll
     for (int r = 0; r < 4; ++r) sT[(32 * (w - 2) + 4 * gq + r) * kLd + 32 * (w - 2) + 16 + n] = 0.0f;
   }
-  __syncthreads();
+  exchange_barrier();
   {  // the lower left 32 x 32 block: wave w has rows 16 (w / 2) and columns 16 (w % 2) of it
     const int c = 16 * (w & 1), p = 32 + 16 * (w >> 1);
-    floatx4 m[2] = {}, o = {};
+    const floatx4 t0 = column4(sT + 4 * gq * kLd + c + n), t1 = column4(sT + (16 + 4 * gq) * kLd + c + n);
+    floatx4 m[2] = {}, o[2] = {};
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int k = 16 * (r >> 2) + 4 * gq + (r & 3);
-        m[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(sA[(32 + 16 * j + n) * kLd + k], sT[k * kLd + c + n], m[j], 0, 0, 0);
-      }
-#pragma unroll
-    for (int r = 0; r < 8; ++r)
-      o = __builtin_amdgcn_mfma_f32_16x16x4f32(sT[(p + n) * kLd + 32 + 16 * (r >> 2) + 4 * gq + (r & 3)],
-                                               m[r >> 2][r & 3], o, 0, 0, 0);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sT[(p + 4 * gq + r) * kLd + c + n] = -o[r];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    if (c > w) continue;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) sA[(16 * w + 4 * gq + r) * kLd + 16 * c + n] = P[c][r];
-  }
-  float* rec = ws + (static_cast<int64_t>(blockIdx.x) * a.hv + h) * kRec;
-  const int bad = sBad;
-  // T tile 4 f + .. : rows of tile frag_row(f), columns of tiles 2 frag_k(f) and the other of the
-  // pair, the row tile's own parity first
-  for (int f = w; f < 6; f += 4) {
-    const int t = tile_row(frag_row(f), n);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int k = tile_row(2 * frag_k(f) + ((half ^ frag_row(f)) & 1), 4 * gq);
-      const float4 v = *reinterpret_cast<const float4*>(sT + t * kLd + k);
-      const float4 be = *reinterpret_cast<const float4*>(sBeta + k);
-      float4 o;
-      o.x = k <= t ? (t < bad ? v.x * be.x : NAN) : 0.0f;
-      o.y = k + 1 <= t ? (t < bad ? v.y * be.y : NAN) : 0.0f;
-      o.z = k + 2 <= t ? (t < bad ? v.z * be.z : NAN) : 0.0f;
-      o.w = k + 3 <= t ? (t < bad ? v.w * be.w : NAN) : 0.0f;
-      reinterpret_cast<float4*>(rec)[(2 * f + half) * 64 + lane] = o;
+    for (int j = 0; j < 2; ++j) {
+      m[j] = mfma_f32(sA + (32 + 16 * j + n) * kLd + 4 * gq, t0, m[j]);
+      m[j] = mfma_f32(sA + (32 + 16 * j + n) * kLd + 16 + 4 * gq, t1, m[j]);
     }
-  }
-  __syncthreads();
-  for (int f = w; f < 6; f += 4) {
-    const int t = tile_row(frag_row(f), n), k0 = 32 * frag_k(f) + 8 * gq, own = 4 * (frag_row(f) & 1);
-    float v[8];
-    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(sA + t * kLd + k0 + own);
-    *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(sA + t * kLd + k0 + 4 - own);
-    uint32_t p[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k0 + (j ^ own) <= t ? v[j] : 0.0f;
+    for (int j = 0; j < 2; ++j) o[j] = mfma_f32(sT + (p + n) * kLd + 32 + 16 * j + 4 * gq, m[j], o[j]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cut<2>(v[2 * j], v[2 * j + 1], p + j, 4);
-    uint4* to = reinterpret_cast<uint4*>(rec + kTFloats) + 128 * f + lane;
-    to[0] = make_uint4(p[0], p[1], p[2], p[3]);
-    to[64] = make_uint4(p[4], p[5], p[6], p[7]);
+    for (int r = 0; r < 4; ++r) sT[(p + 4 * gq + r) * kLd + c + n] = -o[0][r] - o[1][r];
   }
-  if (w == 0) {
-    float* c = rec + kTFloats + kPWords;
-    const double b = sB[lane], end = sB[kC - 1];
-    const float e = __builtin_amdgcn_exp2f(static_cast<float>(b));
-    c[lane] = e * sRk[lane];
-    c[64 + lane] = e * sRq[lane] * a.scale;
-    c[128 + lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - b)) * sRk[lane];
-    if (lane == 0) c[192] = __builtin_amdgcn_exp2f(static_cast<float>(end));
+  exchange_barrier();
+  const int bad = sBad;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {  // 12 halves of fragments
+    const int e = 4 * q + w, f = e >> 1, k = 32 * frag_k(f) + 8 * gq + 4 * (e & 1), t = tile_row(frag_row(f), n);
+    const float4 v = *reinterpret_cast<const float4*>(sT + t * kLd + k);
+    float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = k + r < t ? (t < bad ? x[r] : NAN) : 0.0f;
+    // two terms, the second rounded to nearest: below 2^-17 of the entry is lost, and T - I is
+    // what the block's own keys share, a fraction of I
+    uint2 hi, lo;
+    hi.x = high_halves(x[0], x[1]);
+    hi.y = high_halves(x[2], x[3]);
+    const bf16x2 l0 = __builtin_convertvector((floatx2{below_high(x[0]), below_high(x[1])}), bf16x2);
+    const bf16x2 l1 = __builtin_convertvector((floatx2{below_high(x[2]), below_high(x[3])}), bf16x2);
+    __builtin_memcpy(&lo.x, &l0, 4);
+    __builtin_memcpy(&lo.y, &l1, 4);
+    uint2* to = reinterpret_cast<uint2*>(rec) + (2 * f * 64 + lane) * 2 + (e & 1);
+    to[0] = hi;
+    to[128] = lo;
   }
 }
 
-// In the scan, the waves of a pair own the same 16 columns.  Each holds one
-// half of the state's rows and finishes two of the four token tiles: of tiles
-// 2 j and 2 j + 1 the first wave has the even one, the second the odd one.  A
-// wave numbers tiles by position p, its own at p = 0 and 2; the rows of
-// position p are then 32 (p / 2) + 8 (r / 4) + r % 4 + off(p), off = 0 or 4.
-struct Half {
-  int own;  // 0 or 4
-  __device__ inline int off(int p) const { return p & 1 ? 4 - own : own; }
-  __device__ inline int row(int p, int r) const { return 32 * (p >> 1) + 8 * (r >> 2) + (r & 3) + off(p); }
-};
-
 // first token of a lane's column that is not finite, over the lanes of the column; such entries become zero
-__device__ inline int cut_out(floatx4* x, int gq, const Half& hf) {
+__device__ inline int cut_out(floatx4* x, int gq) {
   int at = kC;
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (!(fabsf(x[p][r]) < INFINITY)) {
-        at = min(at, hf.row(p, 4 * gq + r));
-        x[p][r] = 0.0f;
+      if (!(fabsf(x[i][r]) < INFINITY)) {
+        at = min(at, tile_row(i, 4 * gq + r));
+        x[i][r] = 0.0f;
       }
   at = min(at, __shfl_xor(at, 16, kWave));
   return min(at, __shfl_xor(at, 32, kWave));
 }
 __device__ inline bool any_not_finite(const floatx4* x) {
-  float z = 0.0f;
+  floatx4 z = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) z = fmaf(x[i][r], 0.0f, z);
-  return __any(z != 0.0f);  // 0 x infinity and 0 x NaN are NaN
+    for (int r = 0; r < 4; ++r) z[r] = fmaf(x[i][r], 0.0f, z[r]);
+  return __any((z[0] + z[1]) + (z[2] + z[3]) != 0.0f);  // 0 x infinity and 0 x NaN are NaN
 }
 
 __device__ inline uint2 read_tr(const uint16_t* p) {
@@ -558,57 +632,47 @@ __device__ inline void to_lds(Rows r, int at, void* lds) {
   typedef __attribute__((address_space(3))) void lds_void;
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, at, 0, 0, 0);
 }
-// Barrier for what the waves exchange through LDS.  A fence would also wait for
-// the loads into LDS that are on their way, which nothing reads before
-// landed_barrier: the wave's own LDS writes are all that has to be done here.
-__device__ inline void exchange_barrier() {
-  __asm__ volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
-  __asm__ volatile("" ::: "memory");
-}
 // waits for the wave's own loads into LDS, then for the workgroup's
 __device__ inline void landed_barrier() {
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   lds_barrier();
 }
 
-// LDS of the scan for CG column groups of 16
-template <int DKP, int CG>
+// LDS of the scan for W column groups of 16, twice: a block and the next
+template <int DKP, int W>
 struct ScanLds {
-  uint16_t K[2][kC * DKP], Q[2][kC * DKP], V[2][kC * 16 * CG];
-  float C[2][256];
-  float T[kTFloats];
-  uint16_t P[6 * 2 * 512];
-  floatx4 X[2 * CG][4][64], O[2 * CG][2][64];  // what the waves of a pair exchange
+  uint16_t K[kC * DKP], Q[kC * DKP], V[kC * 16 * W];
+  uint16_t T[2 * kFrags], P[2 * kFrags];
+  float C[256];
 };
-static_assert(sizeof(ScanLds<128, 4>) <= 160 * 1024, "LDS of a CU");
+static_assert(2 * sizeof(ScanLds<128, 4>) <= 160 * 1024, "LDS of a CU");
 
-template <int DKP, int CG>
-__global__ __launch_bounds__(128 * CG) void delta_scan(DeltaArgs a, const float* ws) {
-  constexpr int NT = 128 * CG, NW = 2 * CG;
-  constexpr int NS = DKP / 64;         // inner steps of 32 over a wave's half of the state's rows
+template <int DKP, int W>
+__global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* ws, int cols) {
+  constexpr int NS = DKP / 32;         // inner steps of 32 over the state's rows
   constexpr int PR = DKP / 8;          // pieces of a staged row
-  constexpr int NK = kC * PR / NT;     // pieces of K (and of Q) a thread loads
-  constexpr int VP = 2 * CG;           // pieces of a staged row of V
-  constexpr int NR = (768 + NT - 1) / NT;  // 16-byte pieces of T (and of P) a thread carries
-  __shared__ __align__(1024) ScanLds<DKP, CG> L;
+  constexpr int NK = kC * PR / (64 * W);   // pieces of K (and of Q) a thread loads
+  constexpr int VP = 2 * W;            // pieces of a staged row of V
+  constexpr int NV = kC * VP / (64 * W);   // pieces of V a thread loads
+  constexpr int NF = 12 / W;           // 1 KB parts of T (and of P) a wave loads
+  __shared__ __align__(1024) ScanLds<DKP, W> L[2];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, gq = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), cg = w >> 1;
-  const Half hf{4 * (w & 1)};
-  const int d0 = (w & 1) * (DKP / 2);  // first of the wave's rows of the state
-  const int h = blockIdx.y, s = blockIdx.z, kh = h / (a.hv / a.hk);
-  const int wcol = blockIdx.x * 16 * CG, col = wcol + 16 * cg + n;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the column parts of a head follow each other on one XCD, whose L2 then holds its K, Q, T and P once
+  const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
+  if (head >= a.nseq * a.hv) return;
+  const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
+  const int wcol = part * 16 * W, col = wcol + 16 * w + n;
   const bool in = col < a.dv;
   int64_t t0, t1;
   seq_span(a, s, &t0, &t1);
-  const int64_t at = (static_cast<int64_t>(s) * a.hv + h) * a.dk * static_cast<int64_t>(a.dv) + col;
+  const int64_t at = static_cast<int64_t>(head) * a.dk * a.dv + col;
   floatx4 S[2 * NS];
 #pragma unroll
   for (int i = 0; i < 2 * NS; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int d = d0 + tile_row(i, 4 * gq + r);
+      const int d = tile_row(i, 4 * gq + r);
       S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
     }
   const uint16_t* const K0 = a.k + static_cast<int64_t>(kh) * a.dk;
@@ -620,49 +684,60 @@ __global__ __launch_bounds__(128 * CG) void delta_scan(DeltaArgs a, const float*
   Block next{t0, t1 - t0};
   // where this lane's pieces lie in a block: piece e of the LDS image holds piece
   // (e % PR) ^ swap(row) of row e / PR
-  int ak[NK], aq[NK], av;
+  int ak[NK], aq[NK], av[NV];
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    const int row = (i * NT + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
+    const int row = (i * 64 * W + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
     ak[i] = piece_at(row, a.ks, 8 * p, a.dk);
     aq[i] = piece_at(row, a.qs, 8 * p, a.dk);
   }
-  const auto v_at = [&](int row, int p) { return row * 16 * CG + 8 * (p ^ (row & 2)); };
-  {
-    const int row = tid / VP, p = (v_at(row, tid % VP) >> 3) % VP;
-    av = piece_at(row, a.vs, wcol + 8 * p, a.dv);
+  const auto v_at = [&](int row, int p) { return row * 16 * W + 8 * (p ^ (row & 2)); };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int row = (i * 64 * W + tid) / VP, p = (v_at(row, tid % VP) >> 3) % VP;
+    av[i] = piece_at(row, a.vs, wcol + 8 * p, a.dv);
   }
-  static_assert(kC * VP == NT, "one piece of V a thread");
-  uintx4 pt[NR], pp[NR];
-  auto fetch = [&](uint16_t* nK, uint16_t* nQ, uint16_t* nV, float* nC) __attribute__((always_inline)) {
-    const Rows K = rows_of(K0, a.ks, next, a.dk), Q = rows_of(Q0, a.qs, next, a.dk), V = rows_of(V0, a.vs, next, a.dv);
+  // The loads of the next block, in parts that go out between the products: a CU
+  // takes 64 bytes a cycle, so all at once would hold the wave for a thousand.
+  const auto fetch_kq = [&](int k, int parts, uint16_t* nK, uint16_t* nQ) __attribute__((always_inline)) {
+    const Rows K = rows_of(K0, a.ks, next, a.dk), Q = rows_of(Q0, a.qs, next, a.dk);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      to_lds(K, ak[i], nK + (i * NW + w) * 512);
-      to_lds(Q, aq[i], nQ + (i * NW + w) * 512);
+    for (int i = NK * k / parts; i < NK * (k + 1) / parts; ++i) {
+      to_lds(K, ak[i], nK + (i * W + w) * 512);
+      to_lds(Q, aq[i], nQ + (i * W + w) * 512);
     }
-    to_lds(V, av, nV + w * 512);
+  };
+  const auto fetch_v = [&](uint16_t* nV, float* nC) __attribute__((always_inline)) {
+    const Rows V = rows_of(V0, a.vs, next, a.dv);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to_lds(V, av[i], nV + (i * W + w) * 512);
     if (w == 0)
-      to_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec + kTFloats + kPWords), 0, 1024, 0x00027000),
-             16 * lane, nC);
+      to_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000), 8 * kFrags + 16 * lane,
+             nC);
+  };
+  const auto fetch_tp = [&](int k, uint16_t* n) __attribute__((always_inline)) {  // k = 0: T, 1: P
+    const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {  // the last round reads some pieces twice rather than branch
-      const int e = min(i * NT + tid, 767);
-      pt[i] = reinterpret_cast<const uintx4*>(rec)[e];
-      pp[i] = reinterpret_cast<const uintx4*>(rec + kTFloats)[e];
-    }
+    for (int i = 0; i < NF; ++i)
+      to_lds(R, k * 4 * kFrags + (i * W + w) * 1024 + 16 * lane, n + (i * W + w) * 512);
+  };
+  float eNext = 0.0f;
+  const auto advance = [&]() __attribute__((always_inline)) {
+    eNext = rec[2 * kFrags + 256];
     if (next.left > kC) rec += static_cast<int64_t>(a.hv) * kRec;
     next.first += kC;
     next.left -= kC;
   };
+  constexpr int kAllButMemory = 0x38F;  // what may move across a sched_barrier
   const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
-  uint32_t ready[4];  // the outputs of the block before, stored while the next loads are on their way
+  uint32_t ready[8];  // the outputs of the block before, stored while the next loads are on their way
   Block done{t0, 0};
+  const int o_at = in ? 2 * (8 * gq * os + col) : kOutside;  // row tile_row(0, 4 gq)
   const auto store_o = [&]() __attribute__((always_inline)) {
     const Rows to = rows_of(o0, os, done, a.dv);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int to_at = in ? 2 * (hf.row(i & 2, 4 * gq + 2 * (i & 1)) * os + col) : kOutside;
+    for (int i = 0; i < 8; ++i) {
+      const int to_at = o_at + 2 * os * (32 * (i >> 2) + 4 * ((i >> 1) & 1) + 2 * (i & 1));
       __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i]), to, to_at, 0, 0);
       __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i] >> 16), to, to_at + 2 * os, 0, 0);
     }
@@ -671,123 +746,119 @@ __global__ __launch_bounds__(128 * CG) void delta_scan(DeltaArgs a, const float*
   // The buffers are restrict arguments so that no read of one waits for the
   // loads into the other.
   const auto step = [&](bool first, const uint16_t* __restrict__ sK, const uint16_t* __restrict__ sQ,
-                        const uint16_t* __restrict__ sV, const float* __restrict__ sC, uint16_t* __restrict__ nK,
-                        uint16_t* __restrict__ nQ, uint16_t* __restrict__ nV,
-                        float* __restrict__ nC) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-      if ((i + 1) * NT <= 768 || tid < 768 - i * NT) {
-        const int e = i * NT + tid;
-        *reinterpret_cast<uintx4*>(L.T + e * 4) = pt[i];
-        *reinterpret_cast<uintx4*>(L.P + e * 8) = pp[i];
-      }
-    if (!first) store_o();
-    done = next;
-    done.first -= kC;
-    done.left += kC;
-    fetch(nK, nQ, nV, nC);  // after the last block, zeros and that block's T again: no branch around loads
-
-    // the wave's half of K S0 and Q S0
+                        const uint16_t* __restrict__ sV, const uint16_t* __restrict__ sT,
+                        const uint16_t* __restrict__ sP, const float* __restrict__ sC, uint16_t* __restrict__ nK,
+                        uint16_t* __restrict__ nQ, uint16_t* __restrict__ nV, uint16_t* __restrict__ nT,
+                        uint16_t* __restrict__ nP, float* __restrict__ nC) __attribute__((always_inline)) {
+    // after the last block the loads are zeros and that block's T again: no branch around them
+    const float eC = eNext;
+    // K S0 and Q S0
     floatx4 X[4] = {}, O[4] = {};
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
       bf16x8 f[3];
       cut_pair<3>(S[2 * k], S[2 * k + 1], f);
+      fetch_kq(k, NS, nK, nQ);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const int e = swz<DKP>(hf.row(p, n), d0 / 8 + 4 * k + gq);
+      for (int i = 0; i < 4; ++i) {
+        const int e = swz<DKP>(tile_row(i, n), 4 * k + gq);
         const bf16x8 fk = as_frag(*reinterpret_cast<const uint4*>(sK + e));
         const bf16x8 fq = as_frag(*reinterpret_cast<const uint4*>(sQ + e));
-        X[p] = mfma_bf(fk, f[2], X[p]);
-        O[p] = mfma_bf(fq, f[1], O[p]);
-        X[p] = mfma_bf(fk, f[1], X[p]);
-        O[p] = mfma_bf(fq, f[0], O[p]);
-        X[p] = mfma_bf(fk, f[0], X[p]);
+        X[i] = mfma_bf(fk, f[2], X[i]);
+        O[i] = mfma_bf(fq, f[1], O[i]);
+        X[i] = mfma_bf(fk, f[1], X[i]);
+        O[i] = mfma_bf(fq, f[0], O[i]);
+        X[i] = mfma_bf(fk, f[0], X[i]);
       }
+      __builtin_amdgcn_sched_barrier(kAllButMemory);
     }
-    // X is wanted whole by both waves of the pair, O by the one that owns the tile
+    fetch_tp(0, nT);
+    __builtin_amdgcn_sched_barrier(kAllButMemory);
+    // X = diag(beta) (V - diag(e^b) K S0)
 #pragma unroll
-    for (int p = 0; p < 4; ++p) L.X[w][2 * (p >> 1) + (hf.off(p) >> 2)][lane] = X[p];
-    L.O[w][0][lane] = O[1];
-    L.O[w][1][lane] = O[3];
-    exchange_barrier();
-    // X = V - diag(e^b) K S0
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      X[p] += L.X[w ^ 1][2 * (p >> 1) + (hf.off(p) >> 2)][lane];
-      const int t = hf.row(p, 4 * gq);
-      const uint2 v = read_tr(sV + v_at(t + (n >> 2), 2 * cg + ((n >> 1) & 1)) + 4 * (n & 1));
-      const float4 c1 = *reinterpret_cast<const float4*>(sC + t);
-      X[p][0] = __uint_as_float(v.x << 16) - c1.x * X[p][0];
-      X[p][1] = __uint_as_float(v.x & 0xFFFF0000u) - c1.y * X[p][1];
-      X[p][2] = __uint_as_float(v.y << 16) - c1.z * X[p][2];
-      X[p][3] = __uint_as_float(v.y & 0xFFFF0000u) - c1.w * X[p][3];
+    for (int i = 0; i < 4; ++i) {
+      const int t = tile_row(i, 4 * gq);
+      const uint2 v = read_tr(sV + v_at(t + (n >> 2), 2 * w + ((n >> 1) & 1)) + 4 * (n & 1));
+      const float4 c1 = *reinterpret_cast<const float4*>(sC + t), be = *reinterpret_cast<const float4*>(sC + 192 + t);
+      X[i][0] = __uint_as_float(v.x << 16) * be.x - c1.x * X[i][0];
+      X[i][1] = __uint_as_float(v.x & 0xFFFF0000u) * be.y - c1.y * X[i][1];
+      X[i][2] = __uint_as_float(v.y << 16) * be.z - c1.z * X[i][2];
+      X[i][3] = __uint_as_float(v.y & 0xFFFF0000u) * be.w - c1.w * X[i][3];
     }
-    O[0] += L.O[w ^ 1][0][lane];
-    O[2] += L.O[w ^ 1][1][lane];
+    fetch_tp(1, nP);
+    __builtin_amdgcn_sched_barrier(kAllButMemory);
+    // U = X + (T - I) X
+    floatx4 U[4];
+    const auto solve = [&]() __attribute__((always_inline)) {
+      bf16x8 f[2][3];
+      cut_pair<3>(X[0], X[1], f[0]);
+      cut_pair<3>(X[2], X[3], f[1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) U[i] = X[i];
+#pragma unroll
+      for (int b = 0; b < 6; ++b) {
+        const int i = frag_row(b), k = frag_k(b);
+        const bf16x8 th = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + lane) * 8));
+        const bf16x8 tl = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + 64 + lane) * 8));
+        U[i] = mfma_bf(tl, f[k][1], U[i]);
+        U[i] = mfma_bf(th, f[k][2], U[i]);
+        U[i] = mfma_bf(tl, f[k][0], U[i]);
+        U[i] = mfma_bf(th, f[k][1], U[i]);
+        U[i] = mfma_bf(th, f[k][0], U[i]);
+      }
+    };
+    solve();
     int lost = kC;  // first token of this column whose u is not finite
-    if (any_not_finite(X)) lost = cut_out(X, gq, hf);
-    // U = T X on fp32 MFMA, rows of the wave's own tiles: own tile 0 from the tiles of
-    // tokens 0 .. 31, own tile 1 from all four.  (Three bf16 terms of X and of T would be six
-    // products of a sixteenth of the time each, but cutting them costs more on the VALU.)
-    floatx4 U[4] = {};
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-      const int i = b ? 2 : 0, k = b == 2 ? 2 : 0;
-      const floatx4* t = reinterpret_cast<const floatx4*>(L.T) + (2 * b + (hf.own >> 2)) * 128 + lane;
-      const floatx4 ta = t[0], tb = t[64];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) U[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(ta[r], X[k][r], U[i], 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) U[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(tb[r], X[k + 1][r], U[i], 0, 0, 0);
+    if (__builtin_expect(any_not_finite(U), 0)) {
+      lost = cut_out(X, gq);
+      solve();
+      lost = min(lost, cut_out(U, gq));
     }
-    // the pair's other tiles: into the place that only this wave still read
-    L.X[w ^ 1][0][lane] = U[0];
-    L.X[w ^ 1][1][lane] = U[2];
-    exchange_barrier();
-    U[1] = L.X[w][0][lane];
-    U[3] = L.X[w][1][lane];
-    if (any_not_finite(U)) lost = min(lost, cut_out(U, gq, hf));
+    fetch_v(nV, nC);
+    if (!first) store_o();
+    done = next;
+    done.first -= kC;
+    done.left += kC;
+    advance();
+    __builtin_amdgcn_sched_barrier(kAllButMemory);
     // O = diag(e^b) Q S0 + P U (the scale is in both), S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U
     {
       bf16x8 f[2][2];
       cut_pair<2>(U[0], U[1], f[0]);
       cut_pair<2>(U[2], U[3], f[1]);
 #pragma unroll
-      for (int p = 0; p < 4; p += 2) {
-        const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + hf.row(p, 4 * gq));
-        O[p][0] *= c2.x; O[p][1] *= c2.y; O[p][2] *= c2.z; O[p][3] *= c2.w;
+      for (int i = 0; i < 4; ++i) {
+        const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + tile_row(i, 4 * gq));
+        O[i][0] *= c2.x; O[i][1] *= c2.y; O[i][2] *= c2.z; O[i][3] *= c2.w;
       }
 #pragma unroll
-      for (int b = 0; b < 3; ++b) {
-        const int i = b ? 2 : 0, k = b == 2 ? 1 : 0;
-        const uint16_t* frag = L.P + (2 * b + (hf.own >> 2)) * 1024 + lane * 8;
-        const bf16x8 p0 = as_frag(*reinterpret_cast<const uint4*>(frag));
-        const bf16x8 p1 = as_frag(*reinterpret_cast<const uint4*>(frag + 512));
-        O[i] = mfma_bf(p1, f[k][0], O[i]);
-        O[i] = mfma_bf(p0, f[k][1], O[i]);
-        O[i] = mfma_bf(p0, f[k][0], O[i]);
+      for (int b = 0; b < 6; ++b) {
+        const int i = frag_row(b), k = frag_k(b);
+        const bf16x8 ph = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + lane) * 8));
+        const bf16x8 pl = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + 64 + lane) * 8));
+        O[i] = mfma_bf(pl, f[k][0], O[i]);
+        O[i] = mfma_bf(ph, f[k][1], O[i]);
+        O[i] = mfma_bf(ph, f[k][0], O[i]);
       }
     }
     const bool poisoned = __any(lost < kC);
-    if (poisoned) {
+    if (__builtin_expect(poisoned, 0)) {
 #pragma unroll
-      for (int p = 0; p < 4; p += 2)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (hf.row(p, 4 * gq + r) >= lost) O[p][r] = NAN;
+          if (tile_row(i, 4 * gq + r) >= lost) O[i][r] = NAN;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const floatx4 v = O[i & 2];
+    for (int i = 0; i < 8; ++i) {
+      const floatx4 v = O[i >> 1];
       const bf16x2 b = __builtin_convertvector((i & 1 ? floatx2{v[2], v[3]} : floatx2{v[0], v[1]}), bf16x2);
       __builtin_memcpy(&ready[i], &b, 4);
     }
-    const float eC = sC[192];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const float4 c3 = *reinterpret_cast<const float4*>(sC + 128 + hf.row(p, 4 * gq));
-      U[p][0] *= c3.x; U[p][1] *= c3.y; U[p][2] *= c3.z; U[p][3] *= c3.w;
+    for (int i = 0; i < 4; ++i) {
+      const float4 c3 = *reinterpret_cast<const float4*>(sC + 128 + tile_row(i, 4 * gq));
+      U[i][0] *= c3.x; U[i][1] *= c3.y; U[i][2] *= c3.z; U[i][3] *= c3.w;
     }
     bf16x8 f[2][3];
     cut_pair<3>(U[0], U[1], f[0]);
@@ -797,23 +868,32 @@ __global__ __launch_bounds__(128 * CG) void delta_scan(DeltaArgs a, const float*
       S[i] *= eC;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row = 32 * k + 8 * gq + (n >> 2), pc = d0 / 8 + 4 * (i >> 1) + (n & 3);
-        const uint2 lo = read_tr(sK + swz<DKP>(row + hf.own, pc) + 4 * (i & 1));
-        const uint2 hi = read_tr(sK + swz<DKP>(row + 4 - hf.own, pc) + 4 * (i & 1));
+        const int row = 32 * k + 8 * gq + (n >> 2), p = 4 * (i >> 1) + (n & 3);
+        const uint2 lo = read_tr(sK + swz<DKP>(row, p) + 4 * (i & 1));
+        const uint2 hi = read_tr(sK + swz<DKP>(row + 4, p) + 4 * (i & 1));
         const bf16x8 fk = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
         S[i] = mfma_bf(fk, f[k][2], S[i]);
         S[i] = mfma_bf(fk, f[k][1], S[i]);
         S[i] = mfma_bf(fk, f[k][0], S[i]);
       }
-      if (poisoned && lost < kC) S[i] = floatx4{NAN, NAN, NAN, NAN};
+    }
+    if (__builtin_expect(poisoned, 0)) {
+#pragma unroll
+      for (int i = 0; i < 2 * NS; ++i)
+        if (lost < kC) S[i] = floatx4{NAN, NAN, NAN, NAN};
     }
   };
   if (blocks > 0) {
-    fetch(L.K[0], L.Q[0], L.V[0], L.C[0]);
+    fetch_kq(0, 1, L[0].K, L[0].Q);
+    fetch_tp(0, L[0].T);
+    fetch_tp(1, L[0].P);
+    fetch_v(L[0].V, L[0].C);
+    advance();
     for (int c = 0; c < blocks; ++c) {
-      const int b = c & 1;
+      const auto &now = L[c & 1];
+      auto& then = L[(c & 1) ^ 1];
       landed_barrier();
-      step(c == 0, L.K[b], L.Q[b], L.V[b], L.C[b], L.K[b ^ 1], L.Q[b ^ 1], L.V[b ^ 1], L.C[b ^ 1]);
+      step(c == 0, now.K, now.Q, now.V, now.T, now.P, now.C, then.K, then.Q, then.V, then.T, then.P, then.C);
     }
     store_o();
     __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing is on its way into LDS when the workgroup ends
@@ -823,7 +903,7 @@ __global__ __launch_bounds__(128 * CG) void delta_scan(DeltaArgs a, const float*
   for (int i = 0; i < 2 * NS; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int d = d0 + tile_row(i, 4 * gq + r);
+      const int d = tile_row(i, 4 * gq + r);
       if (d < a.dk) a.state_out[at + static_cast<int64_t>(d) * a.dv] = S[i][r];
     }
 }
@@ -834,13 +914,13 @@ int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 constexpr int64_t kFew = 2;
 constexpr int64_t kCus = 256;
 
-template <int DKP, int CG>
+template <int DKP, int W>
 void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
   const dim3 blocks(static_cast<unsigned>(ws_blocks(a.nseq, a.total)), static_cast<unsigned>(a.hv));
   hipLaunchKernelGGL(delta_prep<DKP>, blocks, dim3(256), 0, st, a, ws);
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.dv, 16 * CG)), static_cast<unsigned>(a.hv),
-                  static_cast<unsigned>(a.nseq));
-  hipLaunchKernelGGL((delta_scan<DKP, CG>), grid, dim3(128 * CG), 0, st, a, ws);
+  const int cols = static_cast<int>(ceil_div(a.dv, 16 * W));
+  const dim3 grid(static_cast<unsigned>(ceil_div(int64_t(a.nseq) * a.hv, 8) * 8 * cols));
+  hipLaunchKernelGGL((delta_scan<DKP, W>), grid, dim3(64 * W), 0, st, a, ws, cols);
 }
 
 // sizes, strides and alignment shared by the prompt and the step

@@ -382,9 +382,10 @@ def _is(name, t, shape, dtype):
         _dev(t)
 
 
-def _out(name, t, shape, dtype, device):
+def _out(name, t, shape, dtype, like):
+    """The caller's output, or a new one on the device of ``like``."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     _is(name, t, shape, dtype)
     return t
 
@@ -399,7 +400,7 @@ def _norm_args(x, w, residual, residual_out):
             raise ValueError("residual_out needs a residual")
         return None
     _is("residual", residual, x.shape, x.dtype)
-    return _out("residual_out", residual_out, x.shape, x.dtype, x.device)
+    return _out("residual_out", residual_out, x.shape, x.dtype, x)
 
 
 def rmsnorm(x, w, *, eps: float = 1e-6, residual=None, y_out=None, residual_out=None):
@@ -407,7 +408,7 @@ def rmsnorm(x, w, *, eps: float = 1e-6, residual=None, y_out=None, residual_out=
     returns (y, x + residual), the second None without a residual."""
     residual_out = _norm_args(x, w, residual, residual_out)
     rows, d = x.shape
-    y_out = _out("y_out", y_out, x.shape, x.dtype, x.device)
+    y_out = _out("y_out", y_out, x.shape, x.dtype, x)
     rc = L.lib().bllm_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), rows, d, eps, _ptr(residual_out),
                               y_out.data_ptr(), _stream())
     L.check("bllm_rmsnorm", rc)
@@ -419,8 +420,8 @@ def rmsnorm_q8(x, w, *, eps: float = 1e-6, residual=None, q_out=None, scale_out=
     [rows], x + residual or None); the row is q * scale."""
     residual_out = _norm_args(x, w, residual, residual_out)
     rows, d = x.shape
-    q_out = _out("q_out", q_out, x.shape, torch.int8, x.device)
-    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x.device)
+    q_out = _out("q_out", q_out, x.shape, torch.int8, x)
+    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x)
     rc = L.lib().bllm_rmsnorm_q8(x.data_ptr(), _ptr(residual), w.data_ptr(), _dt(x), rows, d, eps,
                                  _ptr(residual_out), q_out.data_ptr(), scale_out.data_ptr(), _stream())
     L.check("bllm_rmsnorm_q8", rc)
@@ -433,8 +434,8 @@ def quant_rows_q8(x, *, q_out=None, scale_out=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, d]")
     rows, d = x.shape
-    q_out = _out("q_out", q_out, x.shape, torch.int8, x.device)
-    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x.device)
+    q_out = _out("q_out", q_out, x.shape, torch.int8, x)
+    scale_out = _out("scale_out", scale_out, (rows,), torch.float32, x)
     rc = L.lib().bllm_quant_rows_q8(x.data_ptr(), _dt(x), rows, d, q_out.data_ptr(), scale_out.data_ptr(), _stream())
     L.check("bllm_quant_rows_q8", rc)
     return q_out, scale_out
@@ -454,7 +455,7 @@ def linear_i8(xq, x_scale, wq, w_scale, *, bias=None, out_dtype=torch.bfloat16, 
     _is("w_scale", w_scale, (n,), torch.float32)
     if bias is not None:
         _is("bias", bias, (n,), torch.float32)
-    y_out = _out("y_out", y_out, (m, n), out_dtype if y_out is None else y_out.dtype, xq.device)
+    y_out = _out("y_out", y_out, (m, n), out_dtype if y_out is None else y_out.dtype, xq)
     rc = L.lib().bllm_linear_i8(xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(), _ptr(bias),
                                 _dt(y_out), m, n, k, y_out.data_ptr(), _stream())
     L.check("bllm_linear_i8", rc)
@@ -485,7 +486,7 @@ def _delta_args(q, k, v, g, beta, o_out):
         raise TypeError("q, k and v must have one dtype")
     _is("g", g, (total, hv), torch.float32)
     _is("beta", beta, (total, hv), torch.float32)
-    o_out = _out("o_out", o_out, (total, hv, dv), dt, q.device)
+    o_out = _out("o_out", o_out, (total, hv, dv), dt, q)
     return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q)),
             (hk, hv, dk, dv, *strides), o_out)
 
@@ -508,7 +509,7 @@ def gated_delta(q, k, v, g, beta, offsets, *, scale=None, unit_qk: bool = True, 
     if not want_state:
         state_out = None
     else:
-        state_out = _out("state_out", state_out, shape, torch.float32, q.device)
+        state_out = _out("state_out", state_out, shape, torch.float32, q)
     w = _ws(gated_delta_workspace(nseq, total, hv, dk, dv), ws, q.device)
     rc = L.lib().bllm_gated_delta(*ptrs, offsets.data_ptr(), nseq, total, *dims,
                                   dk ** -0.5 if scale is None else scale, 1 if unit_qk else 0, _ptr(state_in),
