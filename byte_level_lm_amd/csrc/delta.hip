@@ -759,17 +759,23 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       bf16x8 f[3];
       cut_pair<3>(S[2 * k], S[2 * k + 1], f);
       fetch_kq(k, NS, nK, nQ);
+      bf16x8 fk[4], fq[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int e = swz<DKP>(tile_row(i, n), 4 * k + gq);
-        const bf16x8 fk = as_frag(*reinterpret_cast<const uint4*>(sK + e));
-        const bf16x8 fq = as_frag(*reinterpret_cast<const uint4*>(sQ + e));
-        X[i] = mfma_bf(fk, f[2], X[i]);
-        O[i] = mfma_bf(fq, f[1], O[i]);
-        X[i] = mfma_bf(fk, f[1], X[i]);
-        O[i] = mfma_bf(fq, f[0], O[i]);
-        X[i] = mfma_bf(fk, f[0], X[i]);
+        fk[i] = as_frag(*reinterpret_cast<const uint4*>(sK + e));
+        fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + e));
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[2], X[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[1], X[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[1], O[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[0], X[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[0], O[i]);
       __builtin_amdgcn_sched_barrier(kAllButMemory);
     }
     fetch_tp(0, nT);
@@ -793,19 +799,28 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       bf16x8 f[2][3];
       cut_pair<3>(X[0], X[1], f[0]);
       cut_pair<3>(X[2], X[3], f[1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) U[i] = X[i];
+      // six chains, the two of a lower tile added at the end
+      bf16x8 th[6], tl[6];
+      floatx4 u[6];
 #pragma unroll
       for (int b = 0; b < 6; ++b) {
-        const int i = frag_row(b), k = frag_k(b);
-        const bf16x8 th = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + lane) * 8));
-        const bf16x8 tl = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + 64 + lane) * 8));
-        U[i] = mfma_bf(tl, f[k][1], U[i]);
-        U[i] = mfma_bf(th, f[k][2], U[i]);
-        U[i] = mfma_bf(tl, f[k][0], U[i]);
-        U[i] = mfma_bf(th, f[k][1], U[i]);
-        U[i] = mfma_bf(th, f[k][0], U[i]);
+        th[b] = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + lane) * 8));
+        tl[b] = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + 64 + lane) * 8));
       }
+#pragma unroll
+      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(tl[b], f[frag_k(b)][1], b < 4 ? X[b] : floatx4{});
+#pragma unroll
+      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][2], u[b]);
+#pragma unroll
+      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(tl[b], f[frag_k(b)][0], u[b]);
+#pragma unroll
+      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][1], u[b]);
+#pragma unroll
+      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][0], u[b]);
+      U[0] = u[0];
+      U[1] = u[1];
+      U[2] = u[2] + u[4];
+      U[3] = u[3] + u[5];
     };
     solve();
     int lost = kC;  // first token of this column whose u is not finite
@@ -831,15 +846,23 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
         const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + tile_row(i, 4 * gq));
         O[i][0] *= c2.x; O[i][1] *= c2.y; O[i][2] *= c2.z; O[i][3] *= c2.w;
       }
+      bf16x8 ph[6], pl[6];
 #pragma unroll
       for (int b = 0; b < 6; ++b) {
-        const int i = frag_row(b), k = frag_k(b);
-        const bf16x8 ph = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + lane) * 8));
-        const bf16x8 pl = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + 64 + lane) * 8));
-        O[i] = mfma_bf(pl, f[k][0], O[i]);
-        O[i] = mfma_bf(ph, f[k][1], O[i]);
-        O[i] = mfma_bf(ph, f[k][0], O[i]);
+        ph[b] = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + lane) * 8));
+        pl[b] = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + 64 + lane) * 8));
       }
+      floatx4 o[6] = {O[0], O[1], O[2], O[3]};
+#pragma unroll
+      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(pl[b], f[frag_k(b)][0], o[b]);
+#pragma unroll
+      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][1], o[b]);
+#pragma unroll
+      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][0], o[b]);
+      O[0] = o[0];
+      O[1] = o[1];
+      O[2] = o[2] + o[4];
+      O[3] = o[3] + o[5];
     }
     const bool poisoned = __any(lost < kC);
     if (__builtin_expect(poisoned, 0)) {
@@ -864,17 +887,23 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
     cut_pair<3>(U[0], U[1], f[0]);
     cut_pair<3>(U[2], U[3], f[1]);
 #pragma unroll
-    for (int i = 0; i < 2 * NS; ++i) {
-      S[i] *= eC;
+    for (int j = 0; j < 2 * NS; j += 4) {  // four tiles of the state at a time
+#pragma unroll
+      for (int i = j; i < j + 4; ++i) S[i] *= eC;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row = 32 * k + 8 * gq + (n >> 2), p = 4 * (i >> 1) + (n & 3);
-        const uint2 lo = read_tr(sK + swz<DKP>(row, p) + 4 * (i & 1));
-        const uint2 hi = read_tr(sK + swz<DKP>(row + 4, p) + 4 * (i & 1));
-        const bf16x8 fk = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
-        S[i] = mfma_bf(fk, f[k][2], S[i]);
-        S[i] = mfma_bf(fk, f[k][1], S[i]);
-        S[i] = mfma_bf(fk, f[k][0], S[i]);
+        bf16x8 fk[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 32 * k + 8 * gq + (n >> 2), p = 4 * ((j + i) >> 1) + (n & 3);
+          const uint2 lo = read_tr(sK + swz<DKP>(row, p) + 4 * (i & 1));
+          const uint2 hi = read_tr(sK + swz<DKP>(row + 4, p) + 4 * (i & 1));
+          fk[i] = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) S[j + i] = mfma_bf(fk[i], f[k][t], S[j + i]);
       }
     }
     if (__builtin_expect(poisoned, 0)) {
