@@ -60,6 +60,24 @@ __device__ inline float column_sum(float x) {
   return x + __shfl_xor(x, 32, kWave);
 }
 
+// R bf16 of a lane's rows as pairs; `left` rows exist (8 of 16 at least)
+template <int R>
+__device__ inline void row_words(const uint16_t* p, int left, uint32_t* w) {
+  if constexpr (R >= 8) {
+#pragma unroll
+    for (int i = 0; i < R; i += 8) {
+      if (i && left < 16) break;
+      const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+      w[i / 2] = v.x; w[i / 2 + 1] = v.y; w[i / 2 + 2] = v.z; w[i / 2 + 3] = v.w;
+    }
+  } else if constexpr (R == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
 // R = ceil(dk / 8) rounded up to 2, 4, 8 or 16 rows for each lane
 template <int R>
 __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
@@ -83,15 +101,38 @@ __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
     if (a.state_in && held && in && r0 + i < a.dk)
       S[i] = *reinterpret_cast<const float4*>(a.state_in + at + static_cast<int64_t>(r0 + i) * a.dv);
   }
+  // the next token's inputs are on their way while this one's are used
+  const int64_t hd = static_cast<int64_t>(kh) * a.dk + r0;
+  const bool rows = r0 < a.dk;  // dk is a multiple of 8: R rows of 8 or 16 are whole or end at 8
+  uint32_t nq[R / 2] = {}, nk[R / 2] = {};
+  uint2 nv = make_uint2(0, 0);
+  float ng = 0.0f, nb = 0.0f;
+  const auto load = [&](int64_t t) __attribute__((always_inline)) {
+    if (rows) {
+      row_words<R>(a.q + t * a.qs + hd, a.dk - r0, nq);
+      row_words<R>(a.k + t * a.ks + hd, a.dk - r0, nk);
+    }
+    if (in) nv = *reinterpret_cast<const uint2*>(a.v + t * a.vs + static_cast<int64_t>(h) * a.dv + col);
+    ng = a.g[t * a.hv + h];
+    nb = a.beta[t * a.hv + h];
+  };
+  if (t0 < t1) load(t0);
   for (int64_t t = t0; t < t1; ++t) {
     float q[R], k[R];
+    const uint2 p = nv;
+    const float al = expf(ng), be = nb;
+#pragma unroll
+    for (int i = 0; i < R; i += 2) {
+      q[i] = __uint_as_float(nq[i / 2] << 16);
+      q[i + 1] = __uint_as_float(nq[i / 2] & 0xFFFF0000u);
+      k[i] = __uint_as_float(nk[i / 2] << 16);
+      k[i + 1] = __uint_as_float(nk[i / 2] & 0xFFFF0000u);
+    }
+    if (t + 1 < t1) load(t + 1);
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
     float4 xk = make_float4(0, 0, 0, 0), xq = make_float4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const bool row = r0 + i < a.dk;
-      q[i] = row ? bf16_to_f32(a.q[t * a.qs + static_cast<int64_t>(kh) * a.dk + r0 + i]) : 0.0f;
-      k[i] = row ? bf16_to_f32(a.k[t * a.ks + static_cast<int64_t>(kh) * a.dk + r0 + i]) : 0.0f;
       kk += k[i] * k[i];
       qq += q[i] * q[i];
       kq += k[i] * q[i];
@@ -106,13 +147,8 @@ __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
     }
     xk.x = column_sum(xk.x); xk.y = column_sum(xk.y); xk.z = column_sum(xk.z); xk.w = column_sum(xk.w);
     xq.x = column_sum(xq.x); xq.y = column_sum(xq.y); xq.z = column_sum(xq.z); xq.w = column_sum(xq.w);
-    const float al = expf(a.g[t * a.hv + h]), be = a.beta[t * a.hv + h];
-    float vv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (in) {
-      const uint2 p = *reinterpret_cast<const uint2*>(a.v + t * a.vs + static_cast<int64_t>(h) * a.dv + col);
-      vv[0] = bf16_to_f32(p.x & 0xFFFFu); vv[1] = bf16_to_f32(p.x >> 16);
-      vv[2] = bf16_to_f32(p.y & 0xFFFFu); vv[3] = bf16_to_f32(p.y >> 16);
-    }
+    const float vv[4] = {__uint_as_float(p.x << 16), __uint_as_float(p.x & 0xFFFF0000u), __uint_as_float(p.y << 16),
+                         __uint_as_float(p.y & 0xFFFF0000u)};
     const float ak = al * rk;
     const float u[4] = {be * (vv[0] - ak * xk.x), be * (vv[1] - ak * xk.y), be * (vv[2] - ak * xk.z),
                         be * (vv[3] - ak * xk.w)};
@@ -124,12 +160,12 @@ __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
     }
     if (in && lane < 8) {
       const float c = a.scale * rq, d = kq * rk;
-      uint2 p;
-      p.x = f32_to_bf16(c * (al * xq.x + d * u[0])) |
+      uint2 y;
+      y.x = f32_to_bf16(c * (al * xq.x + d * u[0])) |
             static_cast<uint32_t>(f32_to_bf16(c * (al * xq.y + d * u[1]))) << 16;
-      p.y = f32_to_bf16(c * (al * xq.z + d * u[2])) |
+      y.y = f32_to_bf16(c * (al * xq.z + d * u[2])) |
             static_cast<uint32_t>(f32_to_bf16(c * (al * xq.w + d * u[3]))) << 16;
-      *reinterpret_cast<uint2*>(a.o + (t * a.hv + h) * a.dv + col) = p;
+      *reinterpret_cast<uint2*>(a.o + (t * a.hv + h) * a.dv + col) = y;
     }
   }
   if (!a.state_out || !held || !in) return;
@@ -161,9 +197,9 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kC = 64;            // tokens of a block
 // One block and head in the workspace, in 4-byte words: T - I and P, each 6 fragments of 64 lanes x 8
-// (16 x 32 entries on or below the diagonal) in two bf16 terms, then beta and the decays of the tokens
-constexpr int kFrags = 6 * 512;
-constexpr int kRec = 2 * kFrags + 256 + 64;
+// (16 x 32 entries on or below the diagonal) in three and two bf16 terms, then beta and the decays of the tokens
+constexpr int kFragsT = 6 * 768, kFragsP = 6 * 512, kFrags = kFragsT + kFragsP;
+constexpr int kRec = kFrags + 256 + 64;
 constexpr int kLd = 68;           // pitch of a 64 x 64 fp32 tile in LDS
 constexpr float kForget = -1e4f;  // smaller gates decay by e^-10000 = 0 as well, and their sums stay finite
 
@@ -272,11 +308,14 @@ typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 constexpr int kOutside = 1 << 30;
 constexpr int64_t kMaxStride = 1 << 22;
 
-__device__ inline Rows rows_of(const uint16_t* base, int64_t stride, const Block& b, int width) {
-  const int n = static_cast<int>(min(b.left, int64_t(kC)));
+__device__ inline Rows rows_at(const uint16_t* base, int64_t stride, int left, int width) {
+  const int n = min(left, kC);
   const int bytes = __builtin_amdgcn_readfirstlane(n > 0 ? 2 * ((n - 1) * static_cast<int>(stride) + width) : 0);
-  const int64_t at = uniform(reinterpret_cast<int64_t>(base + b.first * stride));
+  const int64_t at = uniform(reinterpret_cast<int64_t>(base));
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<uint16_t*>(at), 0, bytes, 0x00027000);
+}
+__device__ inline Rows rows_of(const uint16_t* base, int64_t stride, const Block& b, int width) {
+  return rows_at(base + b.first * stride, stride, static_cast<int>(min(b.left, int64_t(kC))), width);
 }
 __device__ inline int piece_at(int row, int64_t stride, int col, int width) {
   return col < width ? 2 * (row * static_cast<int>(stride) + col) : kOutside;
@@ -286,6 +325,12 @@ __device__ inline uint4 piece(Rows r, int at) {
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 
+// 64 lanes' 16-byte pieces straight into 1 KB of LDS, no register in between
+__device__ inline void to_lds(Rows r, int at, void* lds) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, at, 0, 0, 0);
+}
+
 // LDS image of a block's keys or queries: rows of DKP values in 16-byte pieces,
 // the pieces of a row exchanged so that neither the rows of a tile at one piece
 // nor the 4 x 4 pieces of a transposing read meet in a bank
@@ -293,17 +338,6 @@ template <int DKP>
 __device__ inline int swz(int row, int pc) {
   if (DKP == 128) return row * 128 + ((pc ^ ((row & 3) << 2 | ((row >> 3) & 3))) << 3);
   return row * 64 + ((pc ^ ((row & 2) << 1 | ((row >> 3) & 3))) << 3);
-}
-
-__device__ inline float square_sum(const uint4& v) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-  float s = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(u[i] << 16), hi = __uint_as_float(u[i] & 0xFFFF0000u);
-    s = fmaf(lo, lo, fmaf(hi, hi, s));
-  }
-  return s;
 }
 
 // inclusive sum over the lanes of a wave, in fp64, by row shifts and readlanes
@@ -352,15 +386,20 @@ __device__ inline floatx4 column4(const float* t) {  // entries r kLd of a colum
 // are summed in fp64, in units of ln 2, so that a difference of two sums is as
 // good as an fp32 gate however far the block has decayed.  What bounds it is
 // the chain of these steps at four workgroups a CU.
+//
+// A decay e^(b_t - b_u) is a quotient that must not be formed from its terms
+// (both can underflow).  Between two tiles it is the product of three factors
+// below 1, row to tile start, tile to tile and tile end to column, so that only
+// the tiles on the diagonal take an exponential an entry.
 template <int DKP>
 __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
   constexpr int NS = DKP / 32;
-  constexpr int NP = DKP / 32;     // pieces of K (and of Q) a thread stages
-  constexpr int G16 = DKP / 8;     // lanes that hold a row
-  __shared__ __align__(16) float sA[2 * kC * kLd];  // A and T; before them K and Q
-  __shared__ double sB[kC];
-  __shared__ __align__(16) float sBeta[kC];
-  __shared__ float sRk[kC], sRq[kC];
+  constexpr int PR = DKP / 8;          // pieces of a staged row
+  constexpr int NK = kC * PR / 256;    // pieces of K (and of Q) a thread loads
+  __shared__ __align__(1024) float sA[2 * kC * kLd];  // A and T; before them K and Q
+  __shared__ __align__(16) double sB[kC];
+  // by token: beta, the factors of its decays, the inverse lengths of k and q
+  __shared__ __align__(16) float sBeta[kC], sRow[kC], sCol[kC], sMid[kC], sRk[kC], sRq[kC];
   __shared__ int sBad;
   static_assert(2 * kC * DKP * 2 <= 2 * kC * kLd * 4, "K and Q must fit in the place of A and T");
   float* const sT = sA + kC * kLd;
@@ -373,34 +412,36 @@ __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
   const int h = blockIdx.y, kh = h / (a.hv / a.hk);
   const Rows K = rows_of(a.k + static_cast<int64_t>(kh) * a.dk, a.ks, blk, a.dk);
   const Rows Q = rows_of(a.q + static_cast<int64_t>(kh) * a.dk, a.qs, blk, a.dk);
-  uint4 pk[NP], pq[NP];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int e = i * 256 + tid, row = e / G16, p = e % G16;
-    pk[i] = piece(K, piece_at(row, a.ks, 8 * p, a.dk));
-    pq[i] = piece(Q, piece_at(row, a.qs, 8 * p, a.dk));
-  }
-  const int64_t mine = (blk.first + min(static_cast<int64_t>(lane), blk.left - 1)) * a.hv + h;
-  const float g = a.g[mine], be = lane < blk.left ? a.beta[mine] : 0.0f;
-  if (tid == 0) sBad = kC;
-#pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int e = i * 256 + tid, row = e / G16, p = e % G16;
-    *reinterpret_cast<uint4*>(sK + swz<DKP>(row, p)) = pk[i];
-    *reinterpret_cast<uint4*>(sQ + swz<DKP>(row, p)) = pq[i];
-    const float kk = group_sum<G16>(square_sum(pk[i])), qq = group_sum<G16>(square_sum(pq[i]));
-    if (p == 0) {
-      sRk[row] = a.unit ? 1.0f / sqrtf(kk + kL2Eps) : 1.0f;
-      sRq[row] = a.unit ? 1.0f / sqrtf(qq + kL2Eps) : 1.0f;
-    }
+  for (int i = 0; i < NK; ++i) {
+    const int row = (i * 256 + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
+    to_lds(K, piece_at(row, a.ks, 8 * p, a.dk), sK + (i * 4 + w) * 512);
+    to_lds(Q, piece_at(row, a.qs, 8 * p, a.dk), sQ + (i * 4 + w) * 512);
   }
   if (w == 0) {
+    const int64_t mine = (blk.first + min(static_cast<int64_t>(lane), blk.left - 1)) * a.hv + h;
+    const float g = a.g[mine], be = lane < blk.left ? a.beta[mine] : 0.0f;
+    // a NaN stays
     const double b = wave_sums(lane < blk.left ? (g < kForget ? kForget : g) * 1.4426950408889634 : 0.0);
-    sB[lane] = b;  // a NaN stays
+    const double b15 = lane_value(b, 15), b31 = lane_value(b, 31), b47 = lane_value(b, 47), b63 = lane_value(b, 63);
+    const double start = gq == 0 ? 0.0 : gq == 1 ? b15 : gq == 2 ? b31 : b47;
+    const double end = gq == 0 ? b15 : gq == 1 ? b31 : gq == 2 ? b47 : b63;
+    sB[lane] = b;
     sBeta[lane] = be;
+    sRow[lane] = __builtin_amdgcn_exp2f(static_cast<float>(b - start));
+    sCol[lane] = __builtin_amdgcn_exp2f(static_cast<float>(end - b));
+    sMid[lane] = __builtin_amdgcn_exp2f(static_cast<float>(lane < 32 ? b31 - b : b - b31));
+    if (lane == 0) sBad = kC;
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): K and Q have landed
   __syncthreads();
   float* rec = ws + (static_cast<int64_t>(blockIdx.x) * a.hv + h) * kRec;
+  // 1 / |x| of the rows of a tile from the diagonal of its square, on the lanes that hold it
+  const auto inverse_length = [&](const floatx4& d) {
+    const float v = n & 2 ? (n & 1 ? d[3] : d[2]) : (n & 1 ? d[1] : d[0]);
+    return a.unit ? 1.0f / sqrtf(v + kL2Eps) : 1.0f;
+  };
+  const bool diagonal = gq == n >> 2;
   if (w < 2) {
     // rows 16 i of K K^T: wave 0 has i = 3 and 0, wave 1 has i = 2 and 1
     const int i0 = 3 - w, i1 = w;
@@ -416,44 +457,65 @@ __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) G1[c] = mfma_bf(f1, f[c], G1[c]);
     }
+    if (diagonal) {
+      sRk[16 * i0 + n] = inverse_length(w ? G0[2] : G0[3]);
+      sRk[16 * i1 + n] = inverse_length(w ? G1[1] : G1[0]);
+    }
     exchange_barrier();  // K and Q have been read
+    float z = 0.0f;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
-      const int i = part ? i1 : i0;
-      double bt[4];
-      float at[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * i + 4 * gq + r;
-        bt[r] = sB[t];
-        at[r] = sBeta[t] * sRk[t];
-        // a token's own gates also reach T through its column, and the state
-        if (!(fabsf(at[r]) < INFINITY && fabs(bt[r]) < INFINITY)) atomicMin(&sBad, t);
-      }
+      const int i = part ? i1 : i0, t = 16 * i + 4 * gq;
+      const float4 be = *reinterpret_cast<const float4*>(sBeta + t), rk = *reinterpret_cast<const float4*>(sRk + t);
+      const float4 rw = *reinterpret_cast<const float4*>(sRow + t);
+      const float row[4] = {be.x * rk.x, be.y * rk.y, be.z * rk.z, be.w * rk.w};
+      const float far[4] = {row[0] * rw.x, row[1] * rw.y, row[2] * rw.z, row[3] * rw.w};
 #pragma unroll
       for (int c = 0; c < (part ? 2 : 4); ++c) {
         if (c > i) continue;
         const int u = 16 * c + n;
-        const double bu = sB[u];
-        const float ru = sRk[u];
-        const floatx4 G = part ? G1[c & 1] : G0[c];
+        floatx4& G = part ? G1[c & 1] : G0[c];
+        if (c < i) {
+          const float f = sCol[u] * sRk[u] *
+                          (c + 1 < i ? __builtin_amdgcn_exp2f(static_cast<float>(sB[16 * i - 1] - sB[16 * c + 15])) : 1.0f);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) G[r] *= far[r] * f;
+        } else {
+          const double bu = sB[u];
+          const float ru = sRk[u];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float f = __builtin_amdgcn_exp2f(static_cast<float>(sB[t + r] - bu)) * ru;
+            G[r] = n < 4 * gq + r ? row[r] * f * G[r] : 0.0f;
+          }
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int t = 16 * i + 4 * gq + r;
-          const float f = __builtin_amdgcn_exp2f(static_cast<float>(bt[r] - bu)) * ru;
-          float av = u < t ? at[r] * f * G[r] : 0.0f;
-          if (__builtin_expect(!(fabsf(av) < INFINITY), 0)) {
-            atomicMin(&sBad, t);
-            av = 0.0f;
-          }
-          sA[t * kLd + u] = av;
+          z = fmaf(G[r], 0.0f, z);
+          sA[(t + r) * kLd + u] = G[r];
+        }
+      }
+    }
+    if (__builtin_expect(__any(z != 0.0f), 0)) {  // entries that are not finite: none enters the inverse, rows from the first on are lost
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        const int i = part ? i1 : i0, t = 16 * i + 4 * gq;
+#pragma unroll
+        for (int c = 0; c < (part ? 2 : 4); ++c) {
+          if (c > i) continue;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (!(fabsf(part ? G1[c & 1][r] : G0[c][r]) < INFINITY)) {
+              atomicMin(&sBad, t + r);
+              sA[(t + r) * kLd + 16 * c + n] = 0.0f;
+            }
         }
       }
     }
   } else {
     // columns of P^T: wave 2 the even row tiles of P, wave 3 the odd ones, each against tiles 0, 1 and then 0 .. 3
     const int odd = w - 2;
-    floatx4 P[6] = {};
+    floatx4 P[6] = {}, qq[2] = {};
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       bf16x8 fk[4], fq[2];
@@ -461,38 +523,47 @@ __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
       for (int c = 0; c < 4; ++c)
         fk[c] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(tile_row(c, n), 4 * s + gq)));
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
         fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(2 * i, n) + 4 * odd, 4 * s + gq)));
+        qq[i] = mfma_bf(fq[i], fq[i], qq[i]);
+      }
       P[0] = mfma_bf(fk[0], fq[0], P[0]);
       P[1] = mfma_bf(fk[1], fq[0], P[1]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) P[2 + c] = mfma_bf(fk[c], fq[1], P[2 + c]);
+    }
+    if (diagonal) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) sRq[tile_row(2 * i, n) + 4 * odd] = inverse_length(qq[i]);
     }
     exchange_barrier();
 #pragma unroll
     for (int f = 0; f < 3; ++f) {  // fragments odd, 2 + odd, 4 + odd
       const int t = tile_row(f ? 2 : 0, n) + 4 * odd, c0 = f == 2 ? 2 : 0;
       const double bt = sB[t];
-      const float pt = a.scale * sRq[t];
+      const float pt = a.scale * sRq[t] * (f == 1 ? sMid[t] : 1.0f);
       uint32_t p[8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int u = tile_row(c0 + c, 4 * gq);
+        const float4 rk = *reinterpret_cast<const float4*>(sRk + u), mid = *reinterpret_cast<const float4*>(sMid + u);
+        const float k[4] = {rk.x, rk.y, rk.z, rk.w}, m[4] = {mid.x, mid.y, mid.z, mid.w};
         float v[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float e = __builtin_amdgcn_exp2f(static_cast<float>(bt - sB[u + r]));
-          v[r] = u + r <= t ? pt * sRk[u + r] * e * P[2 * f + c][r] : 0.0f;
+          const float e = f == 1 ? m[r] : __builtin_amdgcn_exp2f(static_cast<float>(bt - sB[u + r]));
+          v[r] = pt * (k[r] * e) * P[2 * f + c][r];
+          if (f != 1) v[r] = u + r <= t ? v[r] : 0.0f;
         }
         cut<2>(v[0], v[1], p + 2 * c, 4);
         cut<2>(v[2], v[3], p + 2 * c + 1, 4);
       }
-      uint4* to = reinterpret_cast<uint4*>(rec + kFrags) + 128 * (2 * f + odd) + lane;
+      uint4* to = reinterpret_cast<uint4*>(rec + kFragsT) + 128 * (2 * f + odd) + lane;
       to[0] = make_uint4(p[0], p[1], p[2], p[3]);
       to[64] = make_uint4(p[4], p[5], p[6], p[7]);
     }
     if (w == 3) {
-      float* c = rec + 2 * kFrags;
+      float* c = rec + kFrags;
       const double b = sB[lane], end = sB[kC - 1];
       const float e = __builtin_amdgcn_exp2f(static_cast<float>(b)), bb = sBeta[lane];
       c[lane] = bb * e * sRk[lane];
@@ -581,18 +652,12 @@ __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
     float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int r = 0; r < 4; ++r) x[r] = k + r < t ? (t < bad ? x[r] : NAN) : 0.0f;
-    // two terms, the second rounded to nearest: below 2^-17 of the entry is lost, and T - I is
-    // what the block's own keys share, a fraction of I
-    uint2 hi, lo;
-    hi.x = high_halves(x[0], x[1]);
-    hi.y = high_halves(x[2], x[3]);
-    const bf16x2 l0 = __builtin_convertvector((floatx2{below_high(x[0]), below_high(x[1])}), bf16x2);
-    const bf16x2 l1 = __builtin_convertvector((floatx2{below_high(x[2]), below_high(x[3])}), bf16x2);
-    __builtin_memcpy(&lo.x, &l0, 4);
-    __builtin_memcpy(&lo.y, &l1, 4);
-    uint2* to = reinterpret_cast<uint2*>(rec) + (2 * f * 64 + lane) * 2 + (e & 1);
-    to[0] = hi;
-    to[128] = lo;
+    uint32_t terms[6];
+    cut<3>(x[0], x[1], terms, 2);
+    cut<3>(x[2], x[3], terms + 1, 2);
+    uint2* to = reinterpret_cast<uint2*>(rec) + (3 * f * 64 + lane) * 2 + (e & 1);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) to[128 * i] = make_uint2(terms[2 * i], terms[2 * i + 1]);
   }
 }
 
@@ -627,11 +692,6 @@ __device__ inline uint2 read_tr(const uint16_t* p) {
   return r;
 }
 
-// 64 lanes' 16-byte pieces straight into 1 KB of LDS, no register in between
-__device__ inline void to_lds(Rows r, int at, void* lds) {
-  typedef __attribute__((address_space(3))) void lds_void;
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)lds, 16, at, 0, 0, 0);
-}
 // waits for the wave's own loads into LDS, then for the workgroup's
 __device__ inline void landed_barrier() {
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
@@ -642,10 +702,10 @@ __device__ inline void landed_barrier() {
 template <int DKP, int W>
 struct ScanLds {
   uint16_t K[kC * DKP], Q[kC * DKP], V[kC * 16 * W];
-  uint16_t T[2 * kFrags], P[2 * kFrags];
+  uint16_t T[2 * kFragsT], P[2 * kFragsP];
   float C[256];
 };
-static_assert(2 * sizeof(ScanLds<128, 4>) <= 160 * 1024, "LDS of a CU");
+static_assert(2 * sizeof(ScanLds<128, 8>) <= 160 * 1024, "LDS of a CU");
 
 template <int DKP, int W>
 __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* ws, int cols) {
@@ -654,7 +714,6 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
   constexpr int NK = kC * PR / (64 * W);   // pieces of K (and of Q) a thread loads
   constexpr int VP = 2 * W;            // pieces of a staged row of V
   constexpr int NV = kC * VP / (64 * W);   // pieces of V a thread loads
-  constexpr int NF = 12 / W;           // 1 KB parts of T (and of P) a wave loads
   __shared__ __align__(1024) ScanLds<DKP, W> L[2];
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, gq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -675,13 +734,15 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       const int d = tile_row(i, 4 * gq + r);
       S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
     }
-  const uint16_t* const K0 = a.k + static_cast<int64_t>(kh) * a.dk;
-  const uint16_t* const Q0 = a.q + static_cast<int64_t>(kh) * a.dk;
-  const uint16_t* const V0 = a.v + static_cast<int64_t>(h) * a.dv;
-  uint16_t* const o0 = a.o + static_cast<int64_t>(h) * a.dv;
   const int os = a.hv * a.dv;
-  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;  // of the block to load next
-  Block next{t0, t1 - t0};
+  // the block to load next: its rows, its record and the tokens from it to the sequence's end (below
+  // 2^31, as the batch); the block whose outputs are to be stored
+  const uint16_t* pk = a.k + static_cast<int64_t>(kh) * a.dk + t0 * a.ks;
+  const uint16_t* pq = a.q + static_cast<int64_t>(kh) * a.dk + t0 * a.qs;
+  const uint16_t* pv = a.v + static_cast<int64_t>(h) * a.dv + t0 * a.vs;
+  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
+  int left = static_cast<int>(t1 - t0), done = 0;
+  uint16_t* po = a.o + (t0 * a.hv + h) * a.dv - static_cast<int64_t>(kC) * os;
   // where this lane's pieces lie in a block: piece e of the LDS image holds piece
   // (e % PR) ^ swap(row) of row e / PR
   int ak[NK], aq[NK], av[NV];
@@ -700,7 +761,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
   // The loads of the next block, in parts that go out between the products: a CU
   // takes 64 bytes a cycle, so all at once would hold the wave for a thousand.
   const auto fetch_kq = [&](int k, int parts, uint16_t* nK, uint16_t* nQ) __attribute__((always_inline)) {
-    const Rows K = rows_of(K0, a.ks, next, a.dk), Q = rows_of(Q0, a.qs, next, a.dk);
+    const Rows K = rows_at(pk, a.ks, left, a.dk), Q = rows_at(pq, a.qs, left, a.dk);
 #pragma unroll
     for (int i = NK * k / parts; i < NK * (k + 1) / parts; ++i) {
       to_lds(K, ak[i], nK + (i * W + w) * 512);
@@ -708,33 +769,35 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
     }
   };
   const auto fetch_v = [&](uint16_t* nV, float* nC) __attribute__((always_inline)) {
-    const Rows V = rows_of(V0, a.vs, next, a.dv);
+    const Rows V = rows_at(pv, a.vs, left, a.dv);
 #pragma unroll
     for (int i = 0; i < NV; ++i) to_lds(V, av[i], nV + (i * W + w) * 512);
     if (w == 0)
-      to_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000), 8 * kFrags + 16 * lane,
+      to_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000), 4 * kFrags + 16 * lane,
              nC);
   };
-  const auto fetch_tp = [&](int k, uint16_t* n) __attribute__((always_inline)) {  // k = 0: T, 1: P
+  const auto fetch_part = [&](int from, int kb, uint16_t* n) __attribute__((always_inline)) {  // kb KB of the record
     const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < NF; ++i)
-      to_lds(R, k * 4 * kFrags + (i * W + w) * 1024 + 16 * lane, n + (i * W + w) * 512);
+    for (int i = 0; i < (kb + W - 1) / W; ++i)
+      if ((i + 1) * W <= kb || i * W + w < kb)
+        to_lds(R, 4 * from + (i * W + w) * 1024 + 16 * lane, n + (i * W + w) * 512);
   };
   float eNext = 0.0f;
   const auto advance = [&]() __attribute__((always_inline)) {
-    eNext = rec[2 * kFrags + 256];
-    if (next.left > kC) rec += static_cast<int64_t>(a.hv) * kRec;
-    next.first += kC;
-    next.left -= kC;
+    eNext = rec[kFrags + 256];
+    if (left > kC) rec += static_cast<int64_t>(a.hv) * kRec;
+    pk += kC * a.ks;
+    pq += kC * a.qs;
+    pv += kC * a.vs;
+    left -= kC;
   };
   constexpr int kAllButMemory = 0x38F;  // what may move across a sched_barrier
   const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
   uint32_t ready[8];  // the outputs of the block before, stored while the next loads are on their way
-  Block done{t0, 0};
   const int o_at = in ? 2 * (8 * gq * os + col) : kOutside;  // row tile_row(0, 4 gq)
   const auto store_o = [&]() __attribute__((always_inline)) {
-    const Rows to = rows_of(o0, os, done, a.dv);
+    const Rows to = rows_at(po, os, done, a.dv);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int to_at = o_at + 2 * os * (32 * (i >> 2) + 4 * ((i >> 1) & 1) + 2 * (i & 1));
@@ -778,7 +841,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[0], O[i]);
       __builtin_amdgcn_sched_barrier(kAllButMemory);
     }
-    fetch_tp(0, nT);
+    fetch_part(0, 18, nT);
     __builtin_amdgcn_sched_barrier(kAllButMemory);
     // X = diag(beta) (V - diag(e^b) K S0)
 #pragma unroll
@@ -791,7 +854,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       X[i][2] = __uint_as_float(v.y << 16) * be.z - c1.z * X[i][2];
       X[i][3] = __uint_as_float(v.y & 0xFFFF0000u) * be.w - c1.w * X[i][3];
     }
-    fetch_tp(1, nP);
+    fetch_part(kFragsT, 12, nP);
     __builtin_amdgcn_sched_barrier(kAllButMemory);
     // U = X + (T - I) X
     floatx4 U[4];
@@ -800,23 +863,19 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
       cut_pair<3>(X[0], X[1], f[0]);
       cut_pair<3>(X[2], X[3], f[1]);
       // six chains, the two of a lower tile added at the end
-      bf16x8 th[6], tl[6];
       floatx4 u[6];
 #pragma unroll
-      for (int b = 0; b < 6; ++b) {
-        th[b] = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + lane) * 8));
-        tl[b] = as_frag(*reinterpret_cast<const uint4*>(sT + (b * 128 + 64 + lane) * 8));
+      for (int b = 0; b < 6; ++b) u[b] = b < 4 ? X[b] : floatx4{};
+#pragma unroll
+      for (int j = 2; j >= 0; --j) {  // term j of T with terms 2 - j .. 0 of X, the smallest products first
+        bf16x8 t[6];
+#pragma unroll
+        for (int b = 0; b < 6; ++b) t[b] = as_frag(*reinterpret_cast<const uint4*>(sT + ((b * 3 + j) * 64 + lane) * 8));
+#pragma unroll
+        for (int i = 2 - j; i >= 0; --i)
+#pragma unroll
+          for (int b = 0; b < 6; ++b) u[b] = mfma_bf(t[b], f[frag_k(b)][i], u[b]);
       }
-#pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(tl[b], f[frag_k(b)][1], b < 4 ? X[b] : floatx4{});
-#pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][2], u[b]);
-#pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(tl[b], f[frag_k(b)][0], u[b]);
-#pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][1], u[b]);
-#pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = mfma_bf(th[b], f[frag_k(b)][0], u[b]);
       U[0] = u[0];
       U[1] = u[1];
       U[2] = u[2] + u[4];
@@ -831,9 +890,8 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
     }
     fetch_v(nV, nC);
     if (!first) store_o();
-    done = next;
-    done.first -= kC;
-    done.left += kC;
+    po += static_cast<int64_t>(kC) * os;
+    done = left + kC;
     advance();
     __builtin_amdgcn_sched_barrier(kAllButMemory);
     // O = diag(e^b) Q S0 + P U (the scale is in both), S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U
@@ -914,8 +972,8 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
   };
   if (blocks > 0) {
     fetch_kq(0, 1, L[0].K, L[0].Q);
-    fetch_tp(0, L[0].T);
-    fetch_tp(1, L[0].P);
+    fetch_part(0, 18, L[0].T);
+    fetch_part(kFragsT, 12, L[0].P);
     fetch_v(L[0].V, L[0].C);
     advance();
     for (int c = 0; c < blocks; ++c) {
@@ -939,8 +997,9 @@ __global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* w
 
 int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 
-// Prompts of at most kFew tokens on average go token by token.
-constexpr int64_t kFew = 2;
+// Prompts of at most kFew tokens on average go token by token, 1.7 us a token after the first (4 heads of
+// 128 x 128, 1 and 64 streams: 4 tokens 11.9 and 14.4 us against 17.4 and 25.8 in a block; 8 tokens 18.7 and 21.3).
+constexpr int64_t kFew = 6;
 constexpr int64_t kCus = 256;
 
 template <int DKP, int W>
@@ -989,17 +1048,19 @@ extern "C" int bllm_gated_delta(const void* q, const void* k, const void* v, con
   if (rc != BLLM_OK) return rc;
   if (!ws || ws_bytes < bllm_gated_delta_workspace(nseq, total, hv, dk, dv) || !aligned16(ws)) return BLLM_E_WS;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  // 64 columns a workgroup where that fills the CUs, else 32: the LDS holds one
-  // workgroup a CU either way, and half the columns are a third faster a block.
-  // 128 heads x 128 columns (256 workgroups of 64): 0.58 ms against 0.88; 4 heads: 0.48 against 0.38.
-  const bool wide = nseq * hv * ceil_div(dv, 64) >= kCus;
   float* w = static_cast<float*>(ws);
+  // The LDS holds one workgroup a CU whatever its columns: the most columns of
+  // 128, 64 and 32 that still give every CU one (us: 512 heads of 128 columns,
+  // 2048 tokens, 638, 735, 1028; 128 heads, 8192 tokens, 813, 726, 989; 4 heads 577, 425, 401).
+  const int64_t heads = nseq * hv;
   if (total <= kFew * nseq)
     recurrent_launch(a, st);
-  else if (dk <= 64)
-    wide ? blocked_launch<64, 4>(a, w, st) : blocked_launch<64, 2>(a, w, st);
+  else if (dv > 64 && heads * ceil_div(dv, 128) >= kCus)
+    dk <= 64 ? blocked_launch<64, 8>(a, w, st) : blocked_launch<128, 8>(a, w, st);
+  else if (dv > 32 && heads * ceil_div(dv, 64) >= kCus)
+    dk <= 64 ? blocked_launch<64, 4>(a, w, st) : blocked_launch<128, 4>(a, w, st);
   else
-    wide ? blocked_launch<128, 4>(a, w, st) : blocked_launch<128, 2>(a, w, st);
+    dk <= 64 ? blocked_launch<64, 2>(a, w, st) : blocked_launch<128, 2>(a, w, st);
   return launch_status();
 }
 
