@@ -128,7 +128,9 @@ def test_norm_in_place_no_rows_and_another_stream(B):
 
 LIN = [(1, 1, 16), (1, 512, 512), (3, 17, 48), (16, 1536, 512), (17, 96, 1040), (33, 130, 80), (64, 64, 64),
        (100, 777, 4096), (129, 257, 768), (300, 40, 131056), (257, 512, 192), (1000, 1551, 336), (2, 8192, 128),
-       (513, 1024, 2048)]
+       (513, 1024, 2048),
+       # tiles of 128 x 128 and of 256 x 256, several of those a workgroup, K shorter than a step or ending inside one
+       (2048, 2100, 80), (4000, 2200, 144), (9000, 2200, 48), (4100, 2060, 336)]
 
 
 @pytest.mark.parametrize("m,n,k", LIN)
@@ -210,7 +212,10 @@ DELTA = [
     ([200], 2, 6, 32, 40), ([77, 128], 3, 3, 40, 24), ([300, 17], 1, 1, 128, 256), ([129], 2, 2, 96, 72),
     ([7] * 40, 1, 4, 64, 32), ([520], 1, 1, 72, 136), ([1000, 0, 10], 1, 1, 64, 128),
     # enough heads and columns that a workgroup takes 64 columns
-    ([70, 0, 9, 64] * 8, 2, 8, 128, 72), ([65, 3] * 20, 1, 8, 24, 40),
+    ([70, 0, 9, 64] * 8, 2, 8, 128, 72), ([65, 3] * 20, 1, 8, 24, 40), ([33, 66] * 16, 8, 8, 128, 64),
+    ([80, 1] * 16, 1, 8, 64, 128),
+    # few tokens a sequence on average, one of them long
+    ([1, 0, 2] * 10 + [90], 2, 4, 64, 40), ([3, 5], 1, 2, 104, 136),
 ]
 
 
@@ -333,6 +338,61 @@ def test_gated_delta_step(B, nseq, hk, hv, dk, dv, unit):
     rest = np.setdiff1d(np.arange(nseq + 3), slots[kept])
     assert np.array_equal(got[rest], pool[rest])
     _check_delta(o, S, o_o, want)
+
+
+@pytest.mark.parametrize("beta", [1.0, 2.0])
+def test_gated_delta_equal_keys(B, beta):
+    """One key for all tokens: the state holds the last values only (strength 1) or reflects (2)."""
+    rng = np.random.default_rng(14)
+    off, q, k, v, g, b = _delta_inputs(rng, [150], 1, 1, 64, 64)
+    k[:] = k[0]
+    g[:] = 0.0
+    b[:] = beta
+    o_o, S_o = oracle.gated_delta(q, k, v, g, b, off, scale=0.125, unit_qk=True)
+    o, S = B.gated_delta(*_strided(q, k, v), to_dev(g), to_dev(b), to_dev(off))
+    _check_delta(o, S, o_o, S_o)
+
+
+def test_offsets_past_32_bits(B):
+    """Rows, outputs and pool slots whose element numbers pass 2^31 and 2^32."""
+    import torch
+    rng = np.random.default_rng(15)
+    n, d = 1_100_000, 2048
+    x = torch.zeros(n, d, dtype=torch.bfloat16, device="cuda")
+    last = _rows(rng, (3, d), "bf16")
+    x[-3:] = to_dev(last, torch.bfloat16)
+    q, scale, _ = B.rmsnorm_q8(x, torch.ones(d, dtype=torch.bfloat16, device="cuda"))
+    q_o, _, _ = oracle.rmsnorm_q8(last, np.ones(d, np.float32), 1e-6)
+    assert np.array_equal(to_np(q[-3:]), q_o) and not q[0].any()
+    del x, q
+    m, n, k = 70_000, 32_768, 16
+    a, b = rng.integers(-128, 128, (m, k), dtype=np.int8), rng.integers(-128, 128, (n, k), dtype=np.int8)
+    y = B.linear_i8(to_dev(a), to_dev(np.ones(m, np.float32)), to_dev(b), to_dev(np.ones(n, np.float32)),
+                    out_dtype=torch.float32)
+    assert np.array_equal(to_np(y[-300:, -300:]), oracle.linear_i8(a[-300:], np.ones(300), b[-300:], np.ones(300)))
+    del y
+    slots, hv, dk = 70_000, 4, 128
+    pool = torch.empty(slots, hv, dk, dk, device="cuda")
+    off, q, k, v, g, beta = _delta_inputs(rng, [1] * 3, 2, hv, dk, dk)
+    at = np.array([slots - 1, 0, 33_000], np.int32)
+    S0 = rng.standard_normal((3, hv, dk, dk)).astype(np.float32)
+    pool[torch.from_numpy(at.astype(np.int64)).cuda()] = to_dev(S0)
+    o_o, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=dk ** -0.5, unit_qk=True, state=S0)
+    o, _ = B.gated_delta_step(*_strided(q, k, v), to_dev(g), to_dev(beta), pool, slots=to_dev(at))
+    _check_delta(o, pool[torch.from_numpy(at.astype(np.int64)).cuda()], o_o, S_o)
+    del pool
+    # one long sequence before a short one: the short one's rows lie past 2^31 elements of v and o
+    long, short, hv, dv = 700_000, 100, 32, 128
+    off, q, k, v, g, beta = _delta_inputs(rng, [short], 1, hv, 8, dv)
+    dv_ = torch.zeros(long + short, hv, dv, dtype=torch.bfloat16, device="cuda")
+    dq, dk_ = (torch.zeros(long + short, 1, 8, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dg, db = (torch.zeros(long + short, hv, device="cuda") for _ in range(2))
+    for t, a in ((dv_, v), (dq, q), (dk_, k), (dg, g), (db, beta)):
+        t[long:] = to_dev(a, t.dtype)
+    o, S = B.gated_delta(dq, dk_, dv_, dg, db, to_dev(np.array([0, long, long + short])))
+    o_o, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=8 ** -0.5, unit_qk=True)
+    _check_delta(o[long:], S[1:], o_o, S_o)
+    assert not S[0].any() and not o[:64].any()
 
 
 def test_operators_inside_a_captured_graph(B):
