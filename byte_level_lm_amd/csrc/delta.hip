@@ -11,9 +11,12 @@
 //   S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U,
 // so the state is read and rounded once a block.  delta_prep, one workgroup for
 // each block and head, forms T = (I + A)^-1 diag(beta), P and the decays, all
-// blocks at once; delta_scan walks the blocks of a sequence with the state in
-// registers.  A wave there owns 16 columns and every row, so the waves of a
-// workgroup share K, Q, T and P through LDS and never exchange results: a
+// blocks at once; a scan walks the blocks of a sequence with the state in
+// registers.  That chain is what bounds it: one wave issues an instruction every
+// four or five cycles, so the scans leave to a wave on the way from state to state
+// what only it can do and give outputs and loads to others.  delta_scan, for many
+// heads, has 16 columns and every row on a wave; delta_scan_quarters, for few, a
+// quarter of the rows.  What one product makes the next takes as it lies: a
 // 16 x 16 accumulator has a lane's four rows where the next product wants its
 // inner index, once the tiles' rows are numbered 8 (r / 4) + r % 4 (+ 4 for the
 // second tile of a pair), which costs nothing.
@@ -692,307 +695,684 @@ __device__ inline uint2 read_tr(const uint16_t* p) {
   return r;
 }
 
-// waits for the wave's own loads into LDS, then for the workgroup's
+// waits for all but the wave's N latest loads and stores, then for the workgroup's
+template <int N>
 __device__ inline void landed_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
-  lds_barrier();
+  static_assert(N < 64);
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);  // vmcnt(N)
+  exchange_barrier();
 }
 
-// LDS of the scan for W column groups of 16, twice: a block and the next
-template <int DKP, int W>
+// The scan with 64 columns on eight waves.  Wave i < 4 holds 16 columns of the
+// state, every row, on the way from state to state; wave 4 + i takes the outputs
+// of these columns, half a block behind, and the loads.  It gets S and U through
+// LDS, cut into the two terms that the outputs take.
+constexpr int kGroups = 4, kCols = 16 * kGroups;
+template <int DKP>
 struct ScanLds {
-  uint16_t K[kC * DKP], Q[kC * DKP], V[kC * 16 * W];
-  uint16_t T[2 * kFragsT], P[2 * kFragsP];
-  float C[256];
+  uint16_t K[2][kC * DKP], T[2][2 * kFragsT];
+  float C[2][256];                         // a block's and the next's
+  uint16_t V[kC * kCols], Q[kC * DKP], P[2 * kFragsP];
+  uint32_t S[kGroups][2 * DKP / 32 * 256], U[kGroups][4 * 256];  // fragments: 64 lanes x 8 terms, 1 KB each
+  int lost[kCols];                         // first token of the column whose u is not finite
 };
-static_assert(2 * sizeof(ScanLds<128, 8>) <= 160 * 1024, "LDS of a CU");
+static_assert(sizeof(ScanLds<128>) <= 160 * 1024, "LDS of a CU");
 
-template <int DKP, int W>
-__global__ __launch_bounds__(64 * W) void delta_scan(DeltaArgs a, const float* ws, int cols) {
+template <int DKP>
+__global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, int cols) {
   constexpr int NS = DKP / 32;         // inner steps of 32 over the state's rows
   constexpr int PR = DKP / 8;          // pieces of a staged row
-  constexpr int NK = kC * PR / (64 * W);   // pieces of K (and of Q) a thread loads
-  constexpr int VP = 2 * W;            // pieces of a staged row of V
-  constexpr int NV = kC * VP / (64 * W);   // pieces of V a thread loads
-  __shared__ __align__(1024) ScanLds<DKP, W> L[2];
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, gq = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int NK = PR / 4;           // pieces of K (and of Q) a thread loads
+  __shared__ __align__(1024) ScanLds<DKP> L;
+  const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, tid = 64 * w + lane;
   // the column parts of a head follow each other on one XCD, whose L2 then holds its K, Q, T and P once
   const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
   if (head >= a.nseq * a.hv) return;
   const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
-  const int wcol = part * 16 * W, col = wcol + 16 * w + n;
+  const int wcol = part * kCols, col = wcol + 16 * w + n;
   const bool in = col < a.dv;
   int64_t t0, t1;
   seq_span(a, s, &t0, &t1);
-  const int64_t at = static_cast<int64_t>(head) * a.dk * a.dv + col;
-  floatx4 S[2 * NS];
+  const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
+  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
+  const int64_t next_rec = static_cast<int64_t>(a.hv) * kRec;
+  const auto v_at = [](int row, int p) { return row * kCols + 8 * (p ^ (row & 2)); };
+  const auto frag = [&](const void* f, int i) __attribute__((always_inline)) {
+    return as_frag(*(reinterpret_cast<const uint4*>(f) + i * 64 + lane));
+  };
+  if (wave < kGroups) {
+    const int64_t at = static_cast<int64_t>(head) * a.dk * a.dv + col;
+    floatx4 S[2 * NS];
 #pragma unroll
-  for (int i = 0; i < 2 * NS; ++i)
+    for (int i = 0; i < 2 * NS; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = tile_row(i, 4 * gq + r);
-      S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+      for (int r = 0; r < 4; ++r) {
+        const int d = tile_row(i, 4 * gq + r);
+        S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+      }
+    const auto step = [&](const uint16_t* sK, const uint16_t* sT, const float* sC, float eC) __attribute__((always_inline)) {
+      // K S0
+      floatx4 X[4] = {};
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        bf16x8 fk[4], f[3];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fk[i] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(tile_row(i, n), 4 * k + gq)));
+        cut_pair<3>(S[2 * k], S[2 * k + 1], f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) *reinterpret_cast<bf16x8*>(L.S[w] + ((2 * k + t) * 64 + lane) * 4) = f[t];
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[t], X[i]);
+      }
+      // X = diag(beta) (V - diag(e^b) K S0)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = tile_row(i, 4 * gq);
+        const uint2 v = read_tr(L.V + v_at(t + (n >> 2), 2 * w + ((n >> 1) & 1)) + 4 * (n & 1));
+        const float4 c1 = *reinterpret_cast<const float4*>(sC + t), be = *reinterpret_cast<const float4*>(sC + 192 + t);
+        X[i][0] = __uint_as_float(v.x << 16) * be.x - c1.x * X[i][0];
+        X[i][1] = __uint_as_float(v.x & 0xFFFF0000u) * be.y - c1.y * X[i][1];
+        X[i][2] = __uint_as_float(v.y << 16) * be.z - c1.z * X[i][2];
+        X[i][3] = __uint_as_float(v.y & 0xFFFF0000u) * be.w - c1.w * X[i][3];
+      }
+      // U = X + (T - I) X
+      floatx4 U[4];
+      const auto solve = [&]() __attribute__((always_inline)) {
+        bf16x8 f[2][3];
+        cut_pair<3>(X[0], X[1], f[0]);
+        cut_pair<3>(X[2], X[3], f[1]);
+        // six chains, the two of a lower tile added at the end
+        floatx4 u[6];
+#pragma unroll
+        for (int b = 0; b < 6; ++b) u[b] = b < 4 ? X[b] : floatx4{};
+#pragma unroll
+        for (int j = 2; j >= 0; --j) {  // term j of T with terms 2 - j .. 0 of X, the smallest products first
+          bf16x8 t[6];
+#pragma unroll
+          for (int b = 0; b < 6; ++b) t[b] = frag(sT, b * 3 + j);
+#pragma unroll
+          for (int i = 2 - j; i >= 0; --i)
+#pragma unroll
+            for (int b = 0; b < 6; ++b) u[b] = mfma_bf(t[b], f[frag_k(b)][i], u[b]);
+        }
+        U[0] = u[0];
+        U[1] = u[1];
+        U[2] = u[2] + u[4];
+        U[3] = u[3] + u[5];
+      };
+      solve();
+      int lost = kC;  // first token of this column whose u is not finite
+      if (__builtin_expect(any_not_finite(U), 0)) {
+        lost = cut_out(X, gq);
+        solve();
+        lost = min(lost, cut_out(U, gq));
+      }
+      float4 c3[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c3[i] = *reinterpret_cast<const float4*>(sC + 128 + tile_row(i, 4 * gq));
+      exchange_barrier();  // the outputs of the block before are made
+      if (gq == 0) L.lost[16 * w + n] = lost;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        bf16x8 f[2];
+        cut_pair<2>(U[2 * k], U[2 * k + 1], f);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) *reinterpret_cast<bf16x8*>(L.U[w] + ((2 * k + t) * 64 + lane) * 4) = f[t];
+      }
+      // S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        U[i][0] *= c3[i].x; U[i][1] *= c3[i].y; U[i][2] *= c3[i].z; U[i][3] *= c3[i].w;
+      }
+      bf16x8 f[2][3];
+      cut_pair<3>(U[0], U[1], f[0]);
+      cut_pair<3>(U[2], U[3], f[1]);
+#pragma unroll
+      for (int j = 0; j < 2 * NS; j += 4) {  // four tiles of the state at a time
+#pragma unroll
+        for (int i = j; i < j + 4; ++i) S[i] *= eC;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          bf16x8 fk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 32 * k + 8 * gq + (n >> 2), p = 4 * ((j + i) >> 1) + (n & 3);
+            const uint2 lo = read_tr(sK + swz<DKP>(row, p) + 4 * (i & 1));
+            const uint2 hi = read_tr(sK + swz<DKP>(row + 4, p) + 4 * (i & 1));
+            fk[i] = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
+          }
+#pragma unroll
+          for (int t = 2; t >= 0; --t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) S[j + i] = mfma_bf(fk[i], f[k][t], S[j + i]);
+        }
+      }
+      if (__builtin_expect(__any(lost < kC), 0)) {
+#pragma unroll
+        for (int i = 0; i < 2 * NS; ++i)
+          if (lost < kC) S[i] = floatx4{NAN, NAN, NAN, NAN};
+      }
+    };
+    if (blocks > 0) {
+      float eC = rec[kFrags + 256];
+      for (int c = 0; c < blocks; ++c) {
+        if (c + 1 < blocks) rec += next_rec;
+        exchange_barrier();  // this block is in LDS, the outputs of the one before have taken S
+        const float e = eC;
+        eC = rec[kFrags + 256];
+        step(L.K[c & 1], L.T[c & 1], L.C[c & 1], e);
+      }
+      exchange_barrier();
     }
+    if (!a.state_out || !in) return;
+#pragma unroll
+    for (int i = 0; i < 2 * NS; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = tile_row(i, 4 * gq + r);
+        if (d < a.dk) a.state_out[at + static_cast<int64_t>(d) * a.dv] = S[i][r];
+      }
+    return;
+  }
   const int os = a.hv * a.dv;
-  // the block to load next: its rows, its record and the tokens from it to the sequence's end (below
-  // 2^31, as the batch); the block whose outputs are to be stored
+  // the block whose K, T and decays are loaded next, and its V; the block whose Q and P are; the outputs to store
   const uint16_t* pk = a.k + static_cast<int64_t>(kh) * a.dk + t0 * a.ks;
   const uint16_t* pq = a.q + static_cast<int64_t>(kh) * a.dk + t0 * a.qs;
   const uint16_t* pv = a.v + static_cast<int64_t>(h) * a.dv + t0 * a.vs;
-  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
-  int left = static_cast<int>(t1 - t0), done = 0;
+  const float* recp = rec;
+  int left = static_cast<int>(t1 - t0), done = 0;  // tokens from the former block to the sequence's end; from the latter
   uint16_t* po = a.o + (t0 * a.hv + h) * a.dv - static_cast<int64_t>(kC) * os;
   // where this lane's pieces lie in a block: piece e of the LDS image holds piece
   // (e % PR) ^ swap(row) of row e / PR
-  int ak[NK], aq[NK], av[NV];
+  int ak[NK], aq[NK], av[2];
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    const int row = (i * 64 * W + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
+    const int row = (i * 256 + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
     ak[i] = piece_at(row, a.ks, 8 * p, a.dk);
     aq[i] = piece_at(row, a.qs, 8 * p, a.dk);
   }
-  const auto v_at = [&](int row, int p) { return row * 16 * W + 8 * (p ^ (row & 2)); };
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int row = (i * 64 * W + tid) / VP, p = (v_at(row, tid % VP) >> 3) % VP;
+  for (int i = 0; i < 2; ++i) {
+    const int row = (i * 256 + tid) / 8, p = (v_at(row, tid % 8) >> 3) % 8;
     av[i] = piece_at(row, a.vs, wcol + 8 * p, a.dv);
   }
-  // The loads of the next block, in parts that go out between the products: a CU
-  // takes 64 bytes a cycle, so all at once would hold the wave for a thousand.
-  const auto fetch_kq = [&](int k, int parts, uint16_t* nK, uint16_t* nQ) __attribute__((always_inline)) {
-    const Rows K = rows_at(pk, a.ks, left, a.dk), Q = rows_at(pq, a.qs, left, a.dk);
-#pragma unroll
-    for (int i = NK * k / parts; i < NK * (k + 1) / parts; ++i) {
-      to_lds(K, ak[i], nK + (i * W + w) * 512);
-      to_lds(Q, aq[i], nQ + (i * W + w) * 512);
-    }
-  };
-  const auto fetch_v = [&](uint16_t* nV, float* nC) __attribute__((always_inline)) {
-    const Rows V = rows_at(pv, a.vs, left, a.dv);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) to_lds(V, av[i], nV + (i * W + w) * 512);
-    if (w == 0)
-      to_lds(__builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000), 4 * kFrags + 16 * lane,
-             nC);
-  };
-  const auto fetch_part = [&](int from, int kb, uint16_t* n) __attribute__((always_inline)) {  // kb KB of the record
+  const auto fetch_ktc = [&](uint16_t* nK, uint16_t* nT, float* nC) __attribute__((always_inline)) {
+    const Rows K = rows_at(pk, a.ks, left, a.dk);
     const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < (kb + W - 1) / W; ++i)
-      if ((i + 1) * W <= kb || i * W + w < kb)
-        to_lds(R, 4 * from + (i * W + w) * 1024 + 16 * lane, n + (i * W + w) * 512);
+    for (int i = 0; i < NK; ++i) to_lds(K, ak[i], nK + (i * 4 + w) * 512);
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {  // 18 KB of T, then the decays, twice to keep the waves' loads alike
+      const bool t = i < 4 || w < 2;
+      to_lds(R, (t ? (4 * i + w) * 1024 : 4 * kFrags) + 16 * lane,
+             t ? static_cast<void*>(nT + (4 * i + w) * 512) : static_cast<void*>(nC));
+    }
+    pk += kC * a.ks;
+    if (left > kC) rec += next_rec;
   };
-  float eNext = 0.0f;
-  const auto advance = [&]() __attribute__((always_inline)) {
-    eNext = rec[kFrags + 256];
-    if (left > kC) rec += static_cast<int64_t>(a.hv) * kRec;
+  const auto fetch_v = [&](uint16_t* nV) __attribute__((always_inline)) {
+    const Rows V = rows_at(pv, a.vs, left, a.dv);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) to_lds(V, av[i], nV + (i * 4 + w) * 512);
+    pv += kC * a.vs;
+    left -= kC;
+  };
+  const int o_at = in ? 2 * (8 * gq * os + col) : kOutside;  // row tile_row(0, 4 gq)
+  floatx4 O[4] = {};
+  // P U and the stores of the block before, from the s buffers
+  const auto finish = [&](const uint16_t* __restrict__ sP, const uint32_t* __restrict__ sU,
+                          const int* __restrict__ sLost) __attribute__((always_inline)) {
+    bf16x8 f[2][2], ph[6], pl[6];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) f[k][t] = frag(sU, 2 * k + t);
+#pragma unroll
+    for (int b = 0; b < 6; ++b) {
+      pl[b] = frag(sP, 2 * b + 1);
+      ph[b] = frag(sP, 2 * b);
+    }
+    const int lost = sLost[16 * w + n];
+    floatx4 o[6] = {O[0], O[1], O[2], O[3]};
+#pragma unroll
+    for (int b = 0; b < 6; ++b) o[b] = mfma_bf(pl[b], f[frag_k(b)][0], o[b]);
+#pragma unroll
+    for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][1], o[b]);
+#pragma unroll
+    for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][0], o[b]);
+    o[2] += o[4];
+    o[3] += o[5];
+    if (__builtin_expect(__any(lost < kC), 0)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (tile_row(i, 4 * gq + r) >= lost) o[i][r] = NAN;
+    }
+    const Rows to = rows_at(po, os, done, a.dv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const floatx4 v = o[i >> 1];
+      const bf16x2 b = __builtin_convertvector((i & 1 ? floatx2{v[2], v[3]} : floatx2{v[0], v[1]}), bf16x2);
+      uint32_t two;
+      __builtin_memcpy(&two, &b, 4);
+      const int to_at = o_at + 2 * os * (32 * (i >> 2) + 4 * ((i >> 1) & 1) + 2 * (i & 1));
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(two), to, to_at, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(two >> 16), to, to_at + 2 * os, 0, 0);
+    }
+  };
+  constexpr int kStores = 16;
+  // The loads into the n buffers go out beside the products from the s buffers;
+  // restrict arguments keep the reads from waiting for the loads.
+  const auto first_half = [&](uint16_t* __restrict__ nQ, uint16_t* __restrict__ nK, uint16_t* __restrict__ nT,
+                              float* __restrict__ nC, const uint16_t* __restrict__ sP, const uint32_t* __restrict__ sU,
+                              const int* __restrict__ sLost) __attribute__((always_inline)) {
+    const int tokens = left + kC;
+    const Rows Q = rows_at(pq, a.qs, tokens, a.dk);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * 4 + w) * 512);
+    pq += kC * a.qs;
+    __asm__ volatile("" ::: "memory");  // Q before the others: they are counted
+    fetch_ktc(nK, nT, nC);  // after the last block zeros and that block's T again: no branch around it
+    finish(sP, sU, sLost);  // before the first block nothing is stored
+    po += static_cast<int64_t>(kC) * os;
+    done = tokens;
+  };
+  const auto second_half = [&](uint16_t* __restrict__ nP, uint16_t* __restrict__ nV, const uint16_t* __restrict__ sQ,
+                               const uint32_t* __restrict__ sS, const float* __restrict__ sC) __attribute__((always_inline)) {
+    const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(recp), 0, 4 * kRec, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) to_lds(R, 4 * kFragsT + (4 * i + w) * 1024 + 16 * lane, nP + (4 * i + w) * 512);
+    recp += next_rec;
+    fetch_v(nV);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) O[i] = floatx4{};
+#pragma unroll
+    for (int k = 0; k < NS; ++k) {
+      bf16x8 fq[4], f[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) f[t] = frag(sS, 2 * k + t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(i, n), 4 * k + gq)));
+#pragma unroll
+      for (int t = 1; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[t], O[i]);
+    }
+    // O = diag(e^b) Q S0 (+ P U; the scale is in both)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + tile_row(i, 4 * gq));
+      O[i][0] *= c2.x; O[i][1] *= c2.y; O[i][2] *= c2.z; O[i][3] *= c2.w;
+    }
+  };
+  if (blocks > 0) {
+    fetch_ktc(L.K[0], L.T[0], L.C[0]);
+    fetch_v(L.V);
+    for (int c = 0; c < blocks; ++c) {
+      const int i = c & 1;
+      landed_barrier<0>();
+      first_half(L.Q, L.K[i ^ 1], L.T[i ^ 1], L.C[i ^ 1], L.P, L.U[w], L.lost);
+      landed_barrier<NK + 5 + kStores>();  // Q
+      second_half(L.P, L.V, L.Q, L.S[w], L.C[i]);
+    }
+    landed_barrier<0>();  // nothing is on its way into LDS when the workgroup ends
+    finish(L.P, L.U[w], L.lost);
+  }
+}
+
+// Brings a block's lines into L2, a quarter of a kilobyte of LDS taking what nobody reads:
+// the way from memory is about as long as a block takes, so the loads into LDS alone,
+// a block ahead, come late (8 heads of 64 x 64, 16 ragged prompts: 390 us without, 333 with).
+// NV lines of 64 columns of v; every wave of NW issues kLoads.
+template <int DKP, int NV, int NW>
+struct Ahead {
+  static constexpr int kRows = DKP / 64, kUnits = 4 + 2 * kRows + NV, kLoads = (kUnits + NW - 1) / NW;
+  static_assert(kLoads <= 15, "counted by vmcnt's low bits");
+  static __device__ inline void touch(int w, const float* rec, const uint16_t* k, const uint16_t* q, const uint16_t* v,
+                                      int ks, int qs, int vs, int rows, int dk, int dv, void* unused) {
+    typedef __attribute__((address_space(3))) void lds_void;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int u = w + j * NW, m = u - 4;  // uniform
+      int64_t base = reinterpret_cast<int64_t>(rec);
+      int stride = 64, line = 8192 * u, width = 0, bytes = 4 * kRec;
+      if (m >= 0) {
+        base = m < kRows ? reinterpret_cast<int64_t>(k) : m < 2 * kRows ? reinterpret_cast<int64_t>(q) : reinterpret_cast<int64_t>(v);
+        stride = m < kRows ? +ks : m < 2 * kRows ? +qs : +vs;
+        width = m < 2 * kRows ? +dk : +dv;
+        line = 128 * (m < kRows ? m : m < 2 * kRows ? m - kRows : m - 2 * kRows);
+        bytes = rows > 0 && u < kUnits ? 2 * ((min(rows, kC) - 1) * stride + width) : 0;
+      }
+      const Rows r = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0,
+                                                       __builtin_amdgcn_readfirstlane(bytes), 0x00027000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)unused, 4, 2 * lane_id() * stride + line, 0, 0, 0);
+    }
+  }
+};
+
+// The scan with 16 columns on eight waves.  Wave i < 4 holds a quarter of the
+// state's rows and takes tile i of the block's tokens (16 of them) on the way from
+// state to state; wave 4 + i takes that tile's outputs, which nothing waits for,
+// and the loads.  What a product needs of other waves (S, X and U, cut into terms
+// by the wave that made them) goes through LDS, with three barriers a block.
+template <int DKP>
+struct QuarterLds {
+  struct {
+    uint16_t K[kC * DKP], Q[kC * DKP], V[kC * 16], T[2 * kFragsT], P[2 * kFragsP];
+    float C[256];
+  } in[2];                             // a block and the next
+  uint32_t S[3 * DKP / 32 * 256], X[6 * 256], U[10 * 256];   // fragments: 64 lanes x 8 terms, 1 KB each
+  int lost[64];                        // [column][wave]: first token whose u is not finite
+  uint32_t unused[64];                 // what the loads that only bring lines into L2 leave behind
+};
+static_assert(sizeof(QuarterLds<128>) <= 160 * 1024, "LDS of a CU");
+
+__device__ inline bool tile_not_finite(const floatx4& x) {
+  const float z = fmaf(x[0], 0.0f, x[1] * 0.0f) + fmaf(x[2], 0.0f, x[3] * 0.0f);
+  return __any(z != 0.0f);  // 0 x infinity and 0 x NaN are NaN
+}
+__device__ inline int cut_out_tile(floatx4* x, int t) {  // t: token of (*x)[0]
+  int at = kC;
+#pragma unroll
+  for (int r = 3; r >= 0; --r)
+    if (!(fabsf((*x)[r]) < INFINITY)) {
+      at = t + r;
+      (*x)[r] = 0.0f;
+    }
+  at = min(at, __shfl_xor(at, 16, kWave));
+  return min(at, __shfl_xor(at, 32, kWave));
+}
+// tile i of an operand's rows, cut into N terms, into its half of the fragments at f (of 32 rows: N of them)
+template <int N>
+__device__ inline void put_tile(uint32_t* f, int i, int lane, const floatx4& x) {
+  uint32_t w[2 * N];
+  cut<N>(x[0], x[1], w, 2);
+  cut<N>(x[2], x[3], w + 1, 2);
+#pragma unroll
+  for (int t = 0; t < N; ++t)
+    *reinterpret_cast<uint2*>(f + (((i >> 1) * N + t) * 64 + lane) * 4 + 2 * (i & 1)) = make_uint2(w[2 * t], w[2 * t + 1]);
+}
+
+template <int DKP>
+__global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const float* ws, int cols) {
+  constexpr int NS = DKP / 32, PR = DKP / 8, NK = PR / 4, TS = DKP / 64;  // TS: tiles of the state a wave holds
+  __shared__ __align__(1024) QuarterLds<DKP> L;
+  const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, tid = 64 * w + lane;
+  const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
+  if (head >= a.nseq * a.hv) return;
+  const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
+  const int wcol = part * 16, col = wcol + n;
+  const bool in = col < a.dv;
+  int64_t t0, t1;
+  seq_span(a, s, &t0, &t1);
+  const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
+  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
+  const int64_t next_rec = static_cast<int64_t>(a.hv) * kRec;
+  const int t4 = tile_row(w, 4 * gq);  // the lane's tokens: t4 .. t4 + 3
+  const auto frag = [&](const void* f, int i) __attribute__((always_inline)) {
+    return as_frag(*(reinterpret_cast<const uint4*>(f) + i * 64 + lane));
+  };
+  if (wave < 4) {
+    const int64_t at = static_cast<int64_t>(head) * a.dk * a.dv + col;
+    floatx4 S[TS];
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = tile_row(TS * w + i, 4 * gq + r);
+        S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+      }
+    const auto put_state = [&]() __attribute__((always_inline)) {
+      if constexpr (TS == 2) {
+        bf16x8 f[3];
+        cut_pair<3>(S[0], S[1], f);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<bf16x8*>(L.S + ((w * 3 + t) * 64 + lane) * 4) = f[t];
+      } else {
+        put_tile<3>(L.S, w, lane, S[0]);
+      }
+    };
+    const auto step = [&](const auto& in, float eC) __attribute__((always_inline)) {
+      // K S0 of the wave's tokens, a chain for each term of S0
+      floatx4 x[3] = {};
+      bf16x8 fk[NS], fs[NS][3];
+#pragma unroll
+      for (int k = 0; k < NS; ++k) {
+        fk[k] = as_frag(*reinterpret_cast<const uint4*>(in.K + swz<DKP>(tile_row(w, n), 4 * k + gq)));
+#pragma unroll
+        for (int t = 0; t < 3; ++t) fs[k][t] = frag(L.S, 3 * k + t);
+      }
+      const uint2 v = read_tr(in.V + (t4 + (n >> 2)) * 16 + 4 * (n & 3));
+      const float4 c1 = *reinterpret_cast<const float4*>(in.C + t4), c3 = *reinterpret_cast<const float4*>(in.C + 128 + t4),
+                   be = *reinterpret_cast<const float4*>(in.C + 192 + t4);
+      bf16x8 ft[2][3];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        ft[0][t] = frag(in.T, 3 * w + t);
+        if (w >= 2) ft[1][t] = frag(in.T, 3 * (w + 2) + t);
+      }
+#pragma unroll
+      for (int k = 0; k < NS; ++k)
+#pragma unroll
+        for (int t = 2; t >= 0; --t) x[t] = mfma_bf(fk[k], fs[k][t], x[t]);
+      floatx4 X = (x[2] + x[1]) + x[0];
+      X[0] = __uint_as_float(v.x << 16) * be.x - c1.x * X[0];
+      X[1] = __uint_as_float(v.x & 0xFFFF0000u) * be.y - c1.y * X[1];
+      X[2] = __uint_as_float(v.y << 16) * be.z - c1.z * X[2];
+      X[3] = __uint_as_float(v.y & 0xFFFF0000u) * be.w - c1.w * X[3];
+      int lost = kC;
+      if (__builtin_expect(tile_not_finite(X), 0)) lost = cut_out_tile(&X, t4);
+      put_tile<3>(L.X, w, lane, X);
+      exchange_barrier();
+      // U = X + (T - I) X
+      floatx4 u[6] = {X};
+      bf16x8 fx[3];
+#pragma unroll
+      for (int t = 0; t < 3; ++t) fx[t] = frag(L.X, t);
+      const auto solve = [&](const bf16x8* ft, floatx4* u) __attribute__((always_inline)) {
+        u[2] = mfma_bf(ft[2], fx[0], u[2]);
+        u[1] = mfma_bf(ft[1], fx[0], u[1]);
+        u[0] = mfma_bf(ft[0], fx[0], u[0]);
+        u[2] = mfma_bf(ft[1], fx[1], u[2]);
+        u[1] = mfma_bf(ft[0], fx[1], u[1]);
+        u[2] = mfma_bf(ft[0], fx[2], u[2]);
+      };
+      bf16x8 fkt[TS][2];
+#pragma unroll
+      for (int i = 0; i < TS; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int ti = TS * w + i, row = 32 * k + 8 * gq + (n >> 2), p = 4 * (ti >> 1) + (n & 3);
+          const uint2 lo = read_tr(in.K + swz<DKP>(row, p) + 4 * (ti & 1));
+          const uint2 hi = read_tr(in.K + swz<DKP>(row + 4, p) + 4 * (ti & 1));
+          fkt[i][k] = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
+      solve(ft[0], u);
+      if (w >= 2) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t) fx[t] = frag(L.X, 3 + t);
+        solve(ft[1], u + 3);
+      }
+      floatx4 U = ((u[2] + u[5]) + (u[1] + u[4])) + (u[0] + u[3]);
+      if (__builtin_expect(tile_not_finite(U), 0)) lost = min(lost, cut_out_tile(&U, t4));
+      if (gq == 0) L.lost[4 * n + w] = lost;
+      put_tile<2>(L.U, w, lane, U);
+      U[0] *= c3.x; U[1] *= c3.y; U[2] *= c3.z; U[3] *= c3.w;
+      put_tile<3>(L.U + 4 * 256, w, lane, U);
+      exchange_barrier();
+      // S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U
+      floatx4 z[TS] = {};
+      bf16x8 f[2][3];
+#pragma unroll
+      for (int t = 2; t >= 0; --t)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) f[k][t] = frag(L.U, 4 + 3 * k + t);
+      const int4 all = *reinterpret_cast<const int4*>(L.lost + 4 * n);
+#pragma unroll
+      for (int i = 0; i < TS; ++i) S[i] *= eC;
+#pragma unroll
+      for (int t = 2; t >= 0; --t)
+#pragma unroll
+        for (int i = 0; i < TS; ++i) {
+          z[i] = mfma_bf(fkt[i][1], f[1][t], z[i]);
+          S[i] = mfma_bf(fkt[i][0], f[0][t], S[i]);
+        }
+#pragma unroll
+      for (int i = 0; i < TS; ++i) S[i] += z[i];
+      lost = min(min(all.x, all.y), min(all.z, all.w));
+      if (__builtin_expect(__any(lost < kC), 0)) {
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+          if (lost < kC) S[i] = floatx4{NAN, NAN, NAN, NAN};
+      }
+      put_state();
+    };
+    if (blocks > 0) {
+      put_state();
+      float eC = rec[kFrags + 256];
+      for (int c = 0; c < blocks; ++c) {
+        if (c + 1 < blocks) rec += next_rec;
+        exchange_barrier();  // the other waves' loads of this block have landed
+        const float e = eC;
+        eC = rec[kFrags + 256];
+        step(L.in[c & 1], e);
+      }
+    }
+    if (!a.state_out || !in) return;
+#pragma unroll
+    for (int i = 0; i < TS; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = tile_row(TS * w + i, 4 * gq + r);
+        if (d < a.dk) a.state_out[at + static_cast<int64_t>(d) * a.dv] = S[i][r];
+      }
+    return;
+  }
+  const int os = a.hv * a.dv;
+  const uint16_t* pk = a.k + static_cast<int64_t>(kh) * a.dk + t0 * a.ks;
+  const uint16_t* pq = a.q + static_cast<int64_t>(kh) * a.dk + t0 * a.qs;
+  const uint16_t* pv = a.v + static_cast<int64_t>(h) * a.dv + t0 * a.vs;
+  int left = static_cast<int>(t1 - t0), done = 0;
+  uint16_t* po = a.o + (t0 * a.hv + h) * a.dv - static_cast<int64_t>(kC) * os;
+  int ak[NK], aq[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int row = (i * 256 + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
+    ak[i] = piece_at(row, a.ks, 8 * p, a.dk);
+    aq[i] = piece_at(row, a.qs, 8 * p, a.dk);
+  }
+  const int av = piece_at((tid & 127) >> 1, a.vs, wcol + 8 * (tid & 1), a.dv);
+  const auto fetch = [&](uint16_t* nK, uint16_t* nQ, uint16_t* nV, uint16_t* nT, uint16_t* nP,
+                         float* nC) __attribute__((always_inline)) {
+    const Rows K = rows_at(pk, a.ks, left, a.dk), Q = rows_at(pq, a.qs, left, a.dk);
+    const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) to_lds(K, ak[i], nK + (i * 4 + w) * 512);
+    if (w < 2) to_lds(rows_at(pv, a.vs, left, a.dv), av, nV + w * 512);
+    if (w == 3) to_lds(R, 4 * kFrags + 16 * lane, nC);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (i < 4 || w < 2) to_lds(R, (4 * i + w) * 1024 + 16 * lane, nT + (4 * i + w) * 512);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * 4 + w) * 512);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) to_lds(R, 4 * kFragsT + (4 * i + w) * 1024 + 16 * lane, nP + (4 * i + w) * 512);
+    if (left > kC) rec += next_rec;
     pk += kC * a.ks;
     pq += kC * a.qs;
     pv += kC * a.vs;
     left -= kC;
   };
-  constexpr int kAllButMemory = 0x38F;  // what may move across a sched_barrier
-  const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
-  uint32_t ready[8];  // the outputs of the block before, stored while the next loads are on their way
-  const int o_at = in ? 2 * (8 * gq * os + col) : kOutside;  // row tile_row(0, 4 gq)
+  typedef Ahead<DKP, 1, 4> Next;  // the block after the next
+  uint32_t ready[2];  // the outputs of the block before
+  const int o_at = in ? 2 * (t4 * os + col) : kOutside;
   const auto store_o = [&]() __attribute__((always_inline)) {
     const Rows to = rows_at(po, os, done, a.dv);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int to_at = o_at + 2 * os * (32 * (i >> 2) + 4 * ((i >> 1) & 1) + 2 * (i & 1));
-      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i]), to, to_at, 0, 0);
-      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i] >> 16), to, to_at + 2 * os, 0, 0);
+    for (int i = 0; i < 2; ++i) {
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i]), to, o_at + 4 * os * i, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(ready[i] >> 16), to, o_at + 4 * os * i + 2 * os, 0, 0);
     }
   };
   // One block, from the s buffers, with the next on its way into the n buffers.
   // The buffers are restrict arguments so that no read of one waits for the
   // loads into the other.
-  const auto step = [&](bool first, const uint16_t* __restrict__ sK, const uint16_t* __restrict__ sQ,
-                        const uint16_t* __restrict__ sV, const uint16_t* __restrict__ sT,
-                        const uint16_t* __restrict__ sP, const float* __restrict__ sC, uint16_t* __restrict__ nK,
-                        uint16_t* __restrict__ nQ, uint16_t* __restrict__ nV, uint16_t* __restrict__ nT,
-                        uint16_t* __restrict__ nP, float* __restrict__ nC) __attribute__((always_inline)) {
-    // after the last block the loads are zeros and that block's T again: no branch around them
-    const float eC = eNext;
-    // K S0 and Q S0
-    floatx4 X[4] = {}, O[4] = {};
+  const auto step = [&](bool first, const uint16_t* __restrict__ sQ, const uint16_t* __restrict__ sP,
+                        const float* __restrict__ sC, uint16_t* __restrict__ nK, uint16_t* __restrict__ nQ,
+                        uint16_t* __restrict__ nV, uint16_t* __restrict__ nT, uint16_t* __restrict__ nP,
+                        float* __restrict__ nC, const uint32_t* __restrict__ xS, const uint32_t* __restrict__ xU,
+                        const int* __restrict__ xLost, uint32_t* __restrict__ unused) __attribute__((always_inline)) {
+    if (!first) store_o();
+    done = left + kC;
+    po += static_cast<int64_t>(kC) * os;
+    fetch(nK, nQ, nV, nT, nP, nC);  // after the last block zeros and that block's T again: no branch around it
+    __asm__ volatile("" ::: "memory");
+    Next::touch(w, rec, pk, pq, pv + wcol, static_cast<int>(a.ks), static_cast<int>(a.qs), static_cast<int>(a.vs), left,
+                a.dk, a.dv - wcol, unused);
+    exchange_barrier();  // leaves the reads of S0 before it to the waves that are waited for
+    floatx4 o[2] = {};
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
-      bf16x8 f[3];
-      cut_pair<3>(S[2 * k], S[2 * k + 1], f);
-      fetch_kq(k, NS, nK, nQ);
-      bf16x8 fk[4], fq[4];
+      const bf16x8 fq = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(w, n), 4 * k + gq)));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = swz<DKP>(tile_row(i, n), 4 * k + gq);
-        fk[i] = as_frag(*reinterpret_cast<const uint4*>(sK + e));
-        fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + e));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[2], X[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[1], X[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[1], O[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) X[i] = mfma_bf(fk[i], f[0], X[i]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) O[i] = mfma_bf(fq[i], f[0], O[i]);
-      __builtin_amdgcn_sched_barrier(kAllButMemory);
+      for (int t = 1; t >= 0; --t) o[t] = mfma_bf(fq, frag(xS, 3 * k + t), o[t]);
     }
-    fetch_part(0, 18, nT);
-    __builtin_amdgcn_sched_barrier(kAllButMemory);
-    // X = diag(beta) (V - diag(e^b) K S0)
+    const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + t4);
+    floatx4 O = o[1] + o[0];
+    O[0] *= c2.x; O[1] *= c2.y; O[2] *= c2.z; O[3] *= c2.w;
+    bf16x8 fp[2][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = tile_row(i, 4 * gq);
-      const uint2 v = read_tr(sV + v_at(t + (n >> 2), 2 * w + ((n >> 1) & 1)) + 4 * (n & 1));
-      const float4 c1 = *reinterpret_cast<const float4*>(sC + t), be = *reinterpret_cast<const float4*>(sC + 192 + t);
-      X[i][0] = __uint_as_float(v.x << 16) * be.x - c1.x * X[i][0];
-      X[i][1] = __uint_as_float(v.x & 0xFFFF0000u) * be.y - c1.y * X[i][1];
-      X[i][2] = __uint_as_float(v.y << 16) * be.z - c1.z * X[i][2];
-      X[i][3] = __uint_as_float(v.y & 0xFFFF0000u) * be.w - c1.w * X[i][3];
+    for (int t = 0; t < 2; ++t) {
+      fp[0][t] = frag(sP, 2 * w + t);
+      if (w >= 2) fp[1][t] = frag(sP, 2 * (w + 2) + t);
     }
-    fetch_part(kFragsT, 12, nP);
-    __builtin_amdgcn_sched_barrier(kAllButMemory);
-    // U = X + (T - I) X
-    floatx4 U[4];
-    const auto solve = [&]() __attribute__((always_inline)) {
-      bf16x8 f[2][3];
-      cut_pair<3>(X[0], X[1], f[0]);
-      cut_pair<3>(X[2], X[3], f[1]);
-      // six chains, the two of a lower tile added at the end
-      floatx4 u[6];
+    exchange_barrier();
+    // O = diag(e^b) Q S0 + P U (the scale is in both)
+    floatx4 z[3] = {};
+    bf16x8 f[2];
 #pragma unroll
-      for (int b = 0; b < 6; ++b) u[b] = b < 4 ? X[b] : floatx4{};
+    for (int t = 0; t < 2; ++t) f[t] = frag(xU, t);
+    const int4 all = *reinterpret_cast<const int4*>(xLost + 4 * n);
+    z[0] = mfma_bf(fp[0][1], f[0], z[0]);
+    O = mfma_bf(fp[0][0], f[0], O);
+    z[0] = mfma_bf(fp[0][0], f[1], z[0]);
+    if (w >= 2) {
 #pragma unroll
-      for (int j = 2; j >= 0; --j) {  // term j of T with terms 2 - j .. 0 of X, the smallest products first
-        bf16x8 t[6];
-#pragma unroll
-        for (int b = 0; b < 6; ++b) t[b] = as_frag(*reinterpret_cast<const uint4*>(sT + ((b * 3 + j) * 64 + lane) * 8));
-#pragma unroll
-        for (int i = 2 - j; i >= 0; --i)
-#pragma unroll
-          for (int b = 0; b < 6; ++b) u[b] = mfma_bf(t[b], f[frag_k(b)][i], u[b]);
-      }
-      U[0] = u[0];
-      U[1] = u[1];
-      U[2] = u[2] + u[4];
-      U[3] = u[3] + u[5];
-    };
-    solve();
-    int lost = kC;  // first token of this column whose u is not finite
-    if (__builtin_expect(any_not_finite(U), 0)) {
-      lost = cut_out(X, gq);
-      solve();
-      lost = min(lost, cut_out(U, gq));
+      for (int t = 0; t < 2; ++t) f[t] = frag(xU, 2 + t);
+      z[1] = mfma_bf(fp[1][1], f[0], z[1]);
+      z[2] = mfma_bf(fp[1][0], f[0], z[2]);
+      z[1] = mfma_bf(fp[1][0], f[1], z[1]);
     }
-    fetch_v(nV, nC);
-    if (!first) store_o();
-    po += static_cast<int64_t>(kC) * os;
-    done = left + kC;
-    advance();
-    __builtin_amdgcn_sched_barrier(kAllButMemory);
-    // O = diag(e^b) Q S0 + P U (the scale is in both), S = e^(b_C) S0 + K^T diag(e^(b_C - b)) U
-    {
-      bf16x8 f[2][2];
-      cut_pair<2>(U[0], U[1], f[0]);
-      cut_pair<2>(U[2], U[3], f[1]);
+    O = ((z[0] + z[1]) + z[2]) + O;
+    const int lost = min(min(all.x, all.y), min(all.z, all.w));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 c2 = *reinterpret_cast<const float4*>(sC + 64 + tile_row(i, 4 * gq));
-        O[i][0] *= c2.x; O[i][1] *= c2.y; O[i][2] *= c2.z; O[i][3] *= c2.w;
-      }
-      bf16x8 ph[6], pl[6];
+    for (int r = 0; r < 4; ++r)
+      if (t4 + r >= lost) O[r] = NAN;
 #pragma unroll
-      for (int b = 0; b < 6; ++b) {
-        ph[b] = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + lane) * 8));
-        pl[b] = as_frag(*reinterpret_cast<const uint4*>(sP + (b * 128 + 64 + lane) * 8));
-      }
-      floatx4 o[6] = {O[0], O[1], O[2], O[3]};
-#pragma unroll
-      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(pl[b], f[frag_k(b)][0], o[b]);
-#pragma unroll
-      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][1], o[b]);
-#pragma unroll
-      for (int b = 0; b < 6; ++b) o[b] = mfma_bf(ph[b], f[frag_k(b)][0], o[b]);
-      O[0] = o[0];
-      O[1] = o[1];
-      O[2] = o[2] + o[4];
-      O[3] = o[3] + o[5];
-    }
-    const bool poisoned = __any(lost < kC);
-    if (__builtin_expect(poisoned, 0)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (tile_row(i, 4 * gq + r) >= lost) O[i][r] = NAN;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const floatx4 v = O[i >> 1];
-      const bf16x2 b = __builtin_convertvector((i & 1 ? floatx2{v[2], v[3]} : floatx2{v[0], v[1]}), bf16x2);
+    for (int i = 0; i < 2; ++i) {
+      const bf16x2 b = __builtin_convertvector((floatx2{O[2 * i], O[2 * i + 1]}), bf16x2);
       __builtin_memcpy(&ready[i], &b, 4);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 c3 = *reinterpret_cast<const float4*>(sC + 128 + tile_row(i, 4 * gq));
-      U[i][0] *= c3.x; U[i][1] *= c3.y; U[i][2] *= c3.z; U[i][3] *= c3.w;
-    }
-    bf16x8 f[2][3];
-    cut_pair<3>(U[0], U[1], f[0]);
-    cut_pair<3>(U[2], U[3], f[1]);
-#pragma unroll
-    for (int j = 0; j < 2 * NS; j += 4) {  // four tiles of the state at a time
-#pragma unroll
-      for (int i = j; i < j + 4; ++i) S[i] *= eC;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        bf16x8 fk[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = 32 * k + 8 * gq + (n >> 2), p = 4 * ((j + i) >> 1) + (n & 3);
-          const uint2 lo = read_tr(sK + swz<DKP>(row, p) + 4 * (i & 1));
-          const uint2 hi = read_tr(sK + swz<DKP>(row + 4, p) + 4 * (i & 1));
-          fk[i] = as_frag(make_uint4(lo.x, lo.y, hi.x, hi.y));
-        }
-#pragma unroll
-        for (int t = 2; t >= 0; --t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) S[j + i] = mfma_bf(fk[i], f[k][t], S[j + i]);
-      }
-    }
-    if (__builtin_expect(poisoned, 0)) {
-#pragma unroll
-      for (int i = 0; i < 2 * NS; ++i)
-        if (lost < kC) S[i] = floatx4{NAN, NAN, NAN, NAN};
     }
   };
   if (blocks > 0) {
-    fetch_kq(0, 1, L[0].K, L[0].Q);
-    fetch_part(0, 18, L[0].T);
-    fetch_part(kFragsT, 12, L[0].P);
-    fetch_v(L[0].V, L[0].C);
-    advance();
+    fetch(L.in[0].K, L.in[0].Q, L.in[0].V, L.in[0].T, L.in[0].P, L.in[0].C);
     for (int c = 0; c < blocks; ++c) {
-      const auto &now = L[c & 1];
-      auto& then = L[(c & 1) ^ 1];
-      landed_barrier();
-      step(c == 0, now.K, now.Q, now.V, now.T, now.P, now.C, then.K, then.Q, then.V, then.T, then.P, then.C);
+      const auto& now = L.in[c & 1];
+      auto& then = L.in[(c & 1) ^ 1];
+      if (c == 0)
+        landed_barrier<0>();
+      else
+        landed_barrier<Next::kLoads>();
+      step(c == 0, now.Q, now.P, now.C, then.K, then.Q, then.V, then.T, then.P, then.C, L.S, L.U, L.lost, L.unused);
     }
     store_o();
     __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing is on its way into LDS when the workgroup ends
   }
-  if (!a.state_out || !in) return;
-#pragma unroll
-  for (int i = 0; i < 2 * NS; ++i)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = tile_row(i, 4 * gq + r);
-      if (d < a.dk) a.state_out[at + static_cast<int64_t>(d) * a.dv] = S[i][r];
-    }
 }
 
 int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
@@ -1002,13 +1382,21 @@ int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 constexpr int64_t kFew = 6;
 constexpr int64_t kCus = 256;
 
-template <int DKP, int W>
+template <int DKP>
 void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
+  const int64_t heads = int64_t(a.nseq) * a.hv;
   const dim3 blocks(static_cast<unsigned>(ws_blocks(a.nseq, a.total)), static_cast<unsigned>(a.hv));
   hipLaunchKernelGGL(delta_prep<DKP>, blocks, dim3(256), 0, st, a, ws);
-  const int cols = static_cast<int>(ceil_div(a.dv, 16 * W));
-  const dim3 grid(static_cast<unsigned>(ceil_div(int64_t(a.nseq) * a.hv, 8) * 8 * cols));
-  hipLaunchKernelGGL((delta_scan<DKP, W>), grid, dim3(64 * W), 0, st, a, ws, cols);
+  // Few heads: where 16 columns a workgroup still find a CU each (us with delta_prep, quarters against 64 columns,
+  // 2048 tokens: 16, 32 and 64 heads of 128 x 128: 69 and 106, 79 and 111, 150 and 127; 64 and 128 heads of
+  // 64 x 64: 78 and 93, 145 and 123; 4 heads of 128 x 128, 8192 tokens: 216 and 359).
+  const bool few = heads * ceil_div(a.dv, 16) <= kCus;
+  const int cols = static_cast<int>(ceil_div(a.dv, few ? 16 : kCols));
+  const dim3 grid(static_cast<unsigned>(ceil_div(heads, 8) * 8 * cols));
+  if (few)
+    hipLaunchKernelGGL(delta_scan_quarters<DKP>, grid, dim3(512), 0, st, a, ws, cols);
+  else
+    hipLaunchKernelGGL(delta_scan<DKP>, grid, dim3(512), 0, st, a, ws, cols);
 }
 
 // sizes, strides and alignment shared by the prompt and the step
@@ -1049,18 +1437,10 @@ extern "C" int bllm_gated_delta(const void* q, const void* k, const void* v, con
   if (!ws || ws_bytes < bllm_gated_delta_workspace(nseq, total, hv, dk, dv) || !aligned16(ws)) return BLLM_E_WS;
   hipStream_t st = static_cast<hipStream_t>(stream);
   float* w = static_cast<float*>(ws);
-  // The LDS holds one workgroup a CU whatever its columns: the most columns of
-  // 128, 64 and 32 that still give every CU one (us: 512 heads of 128 columns,
-  // 2048 tokens, 638, 735, 1028; 128 heads, 8192 tokens, 813, 726, 989; 4 heads 577, 425, 401).
-  const int64_t heads = nseq * hv;
   if (total <= kFew * nseq)
     recurrent_launch(a, st);
-  else if (dv > 64 && heads * ceil_div(dv, 128) >= kCus)
-    dk <= 64 ? blocked_launch<64, 8>(a, w, st) : blocked_launch<128, 8>(a, w, st);
-  else if (dv > 32 && heads * ceil_div(dv, 64) >= kCus)
-    dk <= 64 ? blocked_launch<64, 4>(a, w, st) : blocked_launch<128, 4>(a, w, st);
   else
-    dk <= 64 ? blocked_launch<64, 2>(a, w, st) : blocked_launch<128, 2>(a, w, st);
+    dk <= 64 ? blocked_launch<64>(a, w, st) : blocked_launch<128>(a, w, st);
   return launch_status();
 }
 
