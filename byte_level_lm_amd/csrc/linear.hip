@@ -92,6 +92,25 @@ __device__ inline void store_some(const LinArgs& a, int64_t at, float sx, const 
   }
 }
 
+// four fp32 results, of which `count` exist
+__device__ inline void store_four(const LinArgs& a, int64_t at, float sx, const float* sw, const float* bias,
+                                  const intx4& x, int count) {
+  typedef uint32_t loose4 __attribute__((ext_vector_type(4), aligned(4)));
+  float u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = static_cast<float>(x[i]) * (sx * sw[i]) + bias[i];
+  float* y = static_cast<float*>(a.y) + at;
+  if (count >= 4) {
+    loose4 v;
+    __builtin_memcpy(&v, u, 16);
+    *reinterpret_cast<loose4*>(y) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < count) y[i] = u[i];
+  }
+}
+
 // ---------------------------------------------------------------- few tokens
 
 // A workgroup owns 16 MT tokens and 32 channels; its eight waves take K in
@@ -170,15 +189,20 @@ __global__ __launch_bounds__(512) void linear_few(LinArgs a) {
 
 // ---------------------------------------------------------------- tiles
 
-// Channel of row r of weight tile j: tiles interleave in fours of rows, four
-// tiles at a time, so that a lane holds sixteen consecutive channels.
-__device__ inline int chan16(int j, int r) { return 64 * (j >> 2) + 16 * (r >> 2) + 4 * (j & 3) + (r & 3); }
+// Channel of row r of weight tile j.  For bf16 two tiles interleave in fours of
+// rows, so that a lane's two hold eight consecutive channels: either way a store
+// is 16 bytes and four lanes' stores 64 in a row (5003 x 1551, K 768 to fp32:
+// 25 us with runs of sixteen channels a lane, 19 so).
+template <int DT>
+__device__ inline int tile_chan(int j, int r) {
+  return DT == BLLM_F32 ? 16 * j + r : 32 * (j >> 1) + 8 * (r >> 2) + 4 * (j & 1) + (r & 3);
+}
 
 // 16-byte piece p of row r of a staged tile (rows of kBK bytes) lies at piece
-// p ^ (r / 4 % 4) for tokens and p ^ (r / 16 % 4) for weights: the sixteen rows
+// p ^ (r / 4 % 4), where tiles interleave at p ^ (r / 8 % 4): the sixteen rows
 // of a fragment read start in different banks
-__device__ inline int swz_x(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
-__device__ inline int swz_w(int row, int p) { return row * kBK + ((p ^ ((row >> 4) & 3)) << 4); }
+__device__ inline int swz(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
+__device__ inline int swz_pairs(int row, int p) { return row * kBK + ((p ^ ((row >> 3) & 3)) << 4); }
 
 __device__ inline void to_lds(Buffer b, int at, int k, int8_t* lds) {
   typedef __attribute__((address_space(3))) void lds_void;
@@ -221,6 +245,7 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
   constexpr int NW = 2 * WN;                              // waves, as 2 x WN
   constexpr int MT = TM / 32, NT = TN / WN / 16;          // 16 x 16 tiles of a wave
   constexpr int UX = TM * kBK / (1024 * NW), U = UX + TN * kBK / (1024 * NW);  // loads of 1 KB a wave makes for a step
+  constexpr bool kPairs = DT == BLLM_BF16;                // weight tiles interleave
   constexpr int JB = NT / 2 - 1;                          // the weight tile before which the waves meet
   struct Stage {
     int8_t X[TM * kBK], W[TN * kBK];
@@ -242,7 +267,7 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
   int lt = t, lk = 0, off[U];
   Buffer bx, bw;
   static_assert(NW % 4 == 0, "row / 16 of a wave's loads is w modulo 4");
-  const int prow = lane >> 2, pkx = 16 * ((lane & 3) ^ ((lane >> 4) & 3)), pkw = 16 * ((lane & 3) ^ (w & 3));
+  const int prow = lane >> 2, pkx = 16 * ((lane & 3) ^ ((lane >> 4) & 3)), pkw = kPairs ? 16 * ((lane & 3) ^ ((2 * w + (lane >> 5)) & 3)) : pkx;
   const auto aim = [&]() __attribute__((always_inline)) {
     const Where at = tile_at(lt, mt, nt, TM, TN);
     const int rx = min(static_cast<int>(a.m) - at.row, TM), rw = min(static_cast<int>(a.n) - at.col, TN);
@@ -272,12 +297,13 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
 
   intx4 acc[NT][MT] = {};
   intx4 fx[MT], fw[NT];
-  const int rx0 = swz_x(wr + n, gq), rw0 = swz_w(wc + chan16(0, n), gq);
+  const int rx0 = swz(wr + n, gq);
+  const int cn = wc + tile_chan<DT>(0, n), rw0 = kPairs ? swz_pairs(cn, gq) : swz(cn, gq);
   const auto read_x = [&](int i, const int8_t* X) __attribute__((always_inline)) {
     return *reinterpret_cast<const intx4*>(X + rx0 + 16 * i * kBK);  // 16 rows on, the pieces are exchanged alike
   };
   const auto read_w = [&](int j, const int8_t* W) __attribute__((always_inline)) {
-    return *reinterpret_cast<const intx4*>(W + rw0 + (64 * (j >> 2) + 4 * (j & 3)) * kBK);  // and so for these
+    return *reinterpret_cast<const intx4*>(W + rw0 + tile_chan<DT>(j, 0) * kBK);  // and so for these
   };
   // One step, with `more` if there is one to load.  The buffers are restrict
   // arguments: no fragment read has to wait for loads that fill another one.
@@ -353,13 +379,14 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
-    static_assert(NT == 4 && TN + TM <= 128 * WN, "a lane's channels are one run of sixteen, one scale a thread");
-    const int c0 = wc + 16 * gq, count = static_cast<int>(a.n) - at.col - c0;
+    static_assert(NT == 4 && TN + TM <= 128 * WN, "a lane has sixteen channels, a thread one scale");
+    const int c0 = wc + tile_chan<DT>(0, 4 * gq), count = static_cast<int>(a.n) - at.col - c0;
     float sw[16], bias[16];
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      *reinterpret_cast<float4*>(sw + i) = *reinterpret_cast<const float4*>(sScale + TM + c0 + i);
-      *reinterpret_cast<float4*>(bias + i) = *reinterpret_cast<const float4*>(sScale + TM + TN + c0 + i);
+    for (int j = 0; j < 4; ++j) {
+      const int c = TM + c0 + tile_chan<DT>(j, 0);
+      *reinterpret_cast<float4*>(sw + 4 * j) = *reinterpret_cast<const float4*>(sScale + c);
+      *reinterpret_cast<float4*>(bias + 4 * j) = *reinterpret_cast<const float4*>(sScale + TN + c);
     }
 #pragma unroll
     for (int r = 0; r < MT; ++r) {
@@ -367,13 +394,19 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
       const int64_t to = static_cast<int64_t>(row) * a.n + at.col + c0;
       const float sx = sScale[wr + 16 * r + n];
 #pragma unroll
-      for (int q = 0; q < 4; q += 2) {
-        if (whole || (row < m && count >= 4 * q + 8))
-          store_whole<DT>(a, to + 4 * q, sx, sw + 4 * q, bias + 4 * q, acc[q][r], acc[q + 1][r]);
-        else if (row < m && count > 4 * q)
-          store_some<DT>(a, to + 4 * q, sx, sw + 4 * q, bias + 4 * q, acc[q][r], acc[q + 1][r], count - 4 * q);
-        acc[q][r] = acc[q + 1][r] = intx4{};
+      for (int j = 0; j < 4; j += kPairs ? 2 : 1) {
+        const int c = tile_chan<DT>(j, 0);
+        if constexpr (kPairs) {
+          if (whole || (row < m && count >= c + 8))
+            store_whole<DT>(a, to + c, sx, sw + 4 * j, bias + 4 * j, acc[j][r], acc[j + 1][r]);
+          else if (row < m && count > c)
+            store_some<DT>(a, to + c, sx, sw + 4 * j, bias + 4 * j, acc[j][r], acc[j + 1][r], count - c);
+        } else if (row < m) {
+          store_four(a, to + c, sx, sw + 4 * j, bias + 4 * j, acc[j][r], count - c);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j][r] = intx4{};
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -420,21 +453,23 @@ extern "C" int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8
   // workgroups than CUs, so that K's waves are spread widest (us by 16, 32, 64
   // tokens a workgroup: 100 x 1000, K 1024: 4.5, 5.2, 6.9; 300 x 1024, K 4096:
   // 19.2, 17.6, 14.9).  Up to 64 tokens weights are read once whatever n is.
-  // Else the largest tile that at least half of the CUs (all of them for 128 x
-  // 128) get one of (64 x 128, 128 x 128, 256 x 256: 1024 x 2048, K 2048: 13.8,
-  // 17.3, 28.4; 1000 x 6144, K 1536: 24.0, 20.0, 26.0; 8192 x 1536, K 1536:
-  // 42.4, 33.5, 28.7).
+  // Else the largest tile that three quarters of the CUs (all of them for 128 x
+  // 128) get one of.  Two LDS buffers where several workgroups share a CU, four
+  // where one has it (64 x 128, 128 x 128 with two and with four, 256 x 256; bf16:
+  // 1024 x 2048, K 2048: 13.5, 16.3, 16.7, 27.0; 1000 x 6144, K 1536: 20.9, 18.9,
+  // 19.5, 25.6; 5003 x 1551, K 768: 22.1, 19.7, 22.2, 23.4; 8192 x 1536, K 1536:
+  // 38.1, 28.5, 30.7, 27.0; 4096 x 4096, K 4096: 115, 91, 89, 63).
   if (ceil_div(m, 16) * col32 <= kCus || m <= 16)
     few_launch<1>(a, dtype, st);
   else if (ceil_div(m, 32) * col32 <= kCus || m <= 32)
     few_launch<2>(a, dtype, st);
   else if (ceil_div(m, 64) * col32 <= kCus || m <= 64)
     few_launch<4>(a, dtype, st);
-  else if (ceil_div(m, 256) * ceil_div(n, 256) >= kCus / 2)
+  else if (ceil_div(m, 256) * ceil_div(n, 256) >= kCus / 4 * 3)
     tiles_launch<256, 256, 4, 4>(a, dtype, st);
   else if (ceil_div(m, 128) * ceil_div(n, 128) >= kCus)
-    tiles_launch<128, 128, 2, 4>(a, dtype, st);
+    tiles_launch<128, 128, 2, 2>(a, dtype, st);
   else
-    tiles_launch<64, 128, 2, 4>(a, dtype, st);
+    tiles_launch<64, 128, 2, 2>(a, dtype, st);
   return launch_status();
 }

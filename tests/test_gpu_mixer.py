@@ -130,7 +130,7 @@ LIN = [(1, 1, 16), (1, 512, 512), (3, 17, 48), (16, 1536, 512), (17, 96, 1040), 
        (100, 777, 4096), (129, 257, 768), (300, 40, 131056), (257, 512, 192), (1000, 1551, 336), (2, 8192, 128),
        (513, 1024, 2048),
        # tiles of 128 x 128 and of 256 x 256, several of those a workgroup, K shorter than a step or ending inside one
-       (2048, 2100, 80), (4000, 2200, 144), (9000, 2200, 48), (4100, 2060, 336)]
+       (2048, 2100, 80), (4000, 2200, 144), (9000, 2200, 48), (4100, 2060, 336), (6200, 2060, 336)]
 
 
 @pytest.mark.parametrize("m,n,k", LIN)
@@ -211,7 +211,7 @@ DELTA = [
     ([1], 1, 1, 8, 8), ([5], 1, 1, 16, 16), ([63, 64, 65], 1, 2, 64, 64), ([0, 3, 0, 130, 1], 2, 2, 128, 128),
     ([200], 2, 6, 32, 40), ([77, 128], 3, 3, 40, 24), ([300, 17], 1, 1, 128, 256), ([129], 2, 2, 96, 72),
     ([7] * 40, 1, 4, 64, 32), ([520], 1, 1, 72, 136), ([1000, 0, 10], 1, 1, 64, 128),
-    # enough heads and columns that a workgroup takes 64 columns
+    # enough heads and columns that a workgroup takes 64 columns; the others split a head's columns in sixteens
     ([70, 0, 9, 64] * 8, 2, 8, 128, 72), ([65, 3] * 20, 1, 8, 24, 40), ([33, 66] * 16, 8, 8, 128, 64),
     ([80, 1] * 16, 1, 8, 64, 128),
     # few tokens a sequence on average, one of them long
@@ -268,6 +268,38 @@ def test_gated_delta_nonfinite_stays_in_its_sequence_and_head(B):
     for s, h in [(0, 0), (0, 1), (1, 0), (2, 0), (2, 1)]:
         assert row_rel_err(S[s, h].reshape(1, -1), S_o[s, h].reshape(1, -1)) <= STATE_TOL
     assert np.isfinite(o[:150]).all() and np.isfinite(o[190:]).all() and np.isfinite(o[150:190, 0]).all()
+
+
+@pytest.mark.parametrize("nseq", [3, 40])
+@pytest.mark.parametrize("what", ["v nan", "v inf", "k nan", "q inf", "state"])
+def test_gated_delta_nonfinite_stays_after_its_token_and_in_its_column(B, nseq, what):
+    """With few and with many heads: one value that is not finite in sequence 1, head 1, token 70 (or in its state)."""
+    rng = np.random.default_rng(16)
+    off, q, k, v, g, beta = _delta_inputs(rng, [150] * nseq, 2, 2, 128, 64)
+    S0 = rng.standard_normal((nseq, 2, 128, 64)).astype(np.float32)
+    o_o, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=128 ** -0.5, unit_qk=True, state=S0)
+    at, end = 150 + 70, 300
+    lost, gone = np.zeros(o_o.shape, bool), np.zeros(S_o.shape, bool)
+    if what[0] == "v":
+        v[at, 1, 3] = np.nan if what == "v nan" else np.inf
+        lost[at:end, 1, 3] = True
+        gone[1, 1, :, 3] = True
+    elif what[0] == "k":
+        k[at, 1, 5] = np.nan
+        lost[at:end, 1] = True
+        gone[1, 1] = True
+    elif what[0] == "q":
+        q[at, 1, 5] = np.inf
+        lost[at, 1] = True
+    else:
+        S0[1, 1, 9, 33] = -np.inf
+        lost[150:end, 1, 33] = True
+        gone[1, 1, :, 33] = True
+    o, S = B.gated_delta(*_strided(q, k, v), to_dev(g), to_dev(beta), to_dev(off), state_in=to_dev(S0))
+    o, S = to_np(o), to_np(S)
+    assert not np.isfinite(o[lost]).any() and not np.isfinite(S[gone]).any()
+    assert np.isfinite(o[~lost]).all() and np.isfinite(S[~gone]).all()
+    _check_delta(to_dev(np.where(lost, o_o, o).astype(np.float32)), to_dev(np.where(gone, S_o, S).astype(np.float32)), o_o, S_o)
 
 
 def test_gated_delta_windows_equal_the_whole_and_long_stream(B):
