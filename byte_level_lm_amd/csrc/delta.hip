@@ -703,45 +703,44 @@ __device__ inline void landed_barrier() {
   exchange_barrier();
 }
 
-// The scan with 64 columns on eight waves.  Wave i < 4 holds 16 columns of the
-// state, every row, on the way from state to state; wave 4 + i takes the outputs
+// The scan with 16 G columns on 2 G waves.  Wave i < G holds 16 columns of the
+// state, every row, on the way from state to state; wave G + i takes the outputs
 // of these columns, half a block behind, and the loads.  It gets S and U through
 // LDS, cut into the two terms that the outputs take.
-constexpr int kGroups = 4, kCols = 16 * kGroups;
-template <int DKP>
+template <int DKP, int G>
 struct ScanLds {
   uint16_t K[2][kC * DKP], T[2][2 * kFragsT];
   float C[2][256];                         // a block's and the next's
-  uint16_t V[kC * kCols], Q[kC * DKP], P[2 * kFragsP];
-  uint32_t S[kGroups][2 * DKP / 32 * 256], U[kGroups][4 * 256];  // fragments: 64 lanes x 8 terms, 1 KB each
-  int lost[kCols];                         // first token of the column whose u is not finite
+  uint16_t V[kC * 16 * G], Q[kC * DKP], P[2 * kFragsP];
+  uint32_t S[G][2 * DKP / 32 * 256], U[G][4 * 256];  // fragments: 64 lanes x 8 terms, 1 KB each
+  int lost[16 * G];                         // first token of the column whose u is not finite
 };
-static_assert(sizeof(ScanLds<128>) <= 160 * 1024, "LDS of a CU");
+static_assert(sizeof(ScanLds<128, 4>) <= 160 * 1024, "LDS of a CU");
 
-template <int DKP>
-__global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, int cols) {
+template <int DKP, int G>
+__global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* ws, int cols) {
   constexpr int NS = DKP / 32;         // inner steps of 32 over the state's rows
   constexpr int PR = DKP / 8;          // pieces of a staged row
-  constexpr int NK = PR / 4;           // pieces of K (and of Q) a thread loads
-  __shared__ __align__(1024) ScanLds<DKP> L;
+  constexpr int NK = PR / G;           // pieces of K (and of Q) a thread loads
+  __shared__ __align__(1024) ScanLds<DKP, G> L;
   const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, tid = 64 * w + lane;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % G, tid = 64 * w + lane;
   // the column parts of a head follow each other on one XCD, whose L2 then holds its K, Q, T and P once
   const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
   if (head >= a.nseq * a.hv) return;
   const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
-  const int wcol = part * kCols, col = wcol + 16 * w + n;
+  const int wcol = part * 16 * G, col = wcol + 16 * w + n;
   const bool in = col < a.dv;
   int64_t t0, t1;
   seq_span(a, s, &t0, &t1);
   const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
   const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
   const int64_t next_rec = static_cast<int64_t>(a.hv) * kRec;
-  const auto v_at = [](int row, int p) { return row * kCols + 8 * (p ^ (row & 2)); };
+  const auto v_at = [](int row, int p) { return row * 16 * G + 8 * (p ^ (row & 2)); };
   const auto frag = [&](const void* f, int i) __attribute__((always_inline)) {
     return as_frag(*(reinterpret_cast<const uint4*>(f) + i * 64 + lane));
   };
-  if (wave < kGroups) {
+  if (wave < G) {
     const int64_t at = static_cast<int64_t>(head) * a.dk * a.dv + col;
     floatx4 S[2 * NS];
 #pragma unroll
@@ -890,25 +889,26 @@ __global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, 
   int ak[NK], aq[NK], av[2];
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    const int row = (i * 256 + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
+    const int row = (i * 64 * G + tid) / PR, p = (swz<DKP>(row, tid % PR) >> 3) % PR;
     ak[i] = piece_at(row, a.ks, 8 * p, a.dk);
     aq[i] = piece_at(row, a.qs, 8 * p, a.dk);
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int row = (i * 256 + tid) / 8, p = (v_at(row, tid % 8) >> 3) % 8;
+    const int row = (i * 64 * G + tid) / (2 * G), p = (v_at(row, tid % (2 * G)) >> 3) % (2 * G);
     av[i] = piece_at(row, a.vs, wcol + 8 * p, a.dv);
   }
+  constexpr int kTc = 20 / G;
   const auto fetch_ktc = [&](uint16_t* nK, uint16_t* nT, float* nC) __attribute__((always_inline)) {
     const Rows K = rows_at(pk, a.ks, left, a.dk);
     const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rec), 0, 4 * kRec, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) to_lds(K, ak[i], nK + (i * 4 + w) * 512);
+    for (int i = 0; i < NK; ++i) to_lds(K, ak[i], nK + (i * G + w) * 512);
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {  // 18 KB of T, then the decays, twice to keep the waves' loads alike
-      const bool t = i < 4 || w < 2;
-      to_lds(R, (t ? (4 * i + w) * 1024 : 4 * kFrags) + 16 * lane,
-             t ? static_cast<void*>(nT + (4 * i + w) * 512) : static_cast<void*>(nC));
+    for (int i = 0; i < kTc; ++i) {  // 18 KB of T, then the decays, twice to keep the waves' loads alike
+      const int u = i * G + w;
+      to_lds(R, (u < 18 ? u * 1024 : 4 * kFrags) + 16 * lane,
+             u < 18 ? static_cast<void*>(nT + u * 512) : static_cast<void*>(nC));
     }
     pk += kC * a.ks;
     if (left > kC) rec += next_rec;
@@ -916,7 +916,7 @@ __global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, 
   const auto fetch_v = [&](uint16_t* nV) __attribute__((always_inline)) {
     const Rows V = rows_at(pv, a.vs, left, a.dv);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) to_lds(V, av[i], nV + (i * 4 + w) * 512);
+    for (int i = 0; i < 2; ++i) to_lds(V, av[i], nV + (i * G + w) * 512);
     pv += kC * a.vs;
     left -= kC;
   };
@@ -973,7 +973,7 @@ __global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, 
     const int tokens = left + kC;
     const Rows Q = rows_at(pq, a.qs, tokens, a.dk);
 #pragma unroll
-    for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * 4 + w) * 512);
+    for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * G + w) * 512);
     pq += kC * a.qs;
     __asm__ volatile("" ::: "memory");  // Q before the others: they are counted
     fetch_ktc(nK, nT, nC);  // after the last block zeros and that block's T again: no branch around it
@@ -985,7 +985,7 @@ __global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, 
                                const uint32_t* __restrict__ sS, const float* __restrict__ sC) __attribute__((always_inline)) {
     const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(recp), 0, 4 * kRec, 0x00027000);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) to_lds(R, 4 * kFragsT + (4 * i + w) * 1024 + 16 * lane, nP + (4 * i + w) * 512);
+    for (int i = 0; i < 12 / G; ++i) to_lds(R, 4 * kFragsT + (i * G + w) * 1024 + 16 * lane, nP + (i * G + w) * 512);
     recp += next_rec;
     fetch_v(nV);
 #pragma unroll
@@ -1016,7 +1016,7 @@ __global__ __launch_bounds__(512) void delta_scan(DeltaArgs a, const float* ws, 
       const int i = c & 1;
       landed_barrier<0>();
       first_half(L.Q, L.K[i ^ 1], L.T[i ^ 1], L.C[i ^ 1], L.P, L.U[w], L.lost);
-      landed_barrier<NK + 5 + kStores>();  // Q
+      landed_barrier<NK + kTc + kStores>();  // Q
       second_half(L.P, L.V, L.Q, L.S[w], L.C[i]);
     }
     landed_barrier<0>();  // nothing is on its way into LDS when the workgroup ends
@@ -1387,16 +1387,21 @@ void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
   const int64_t heads = int64_t(a.nseq) * a.hv;
   const dim3 blocks(static_cast<unsigned>(ws_blocks(a.nseq, a.total)), static_cast<unsigned>(a.hv));
   hipLaunchKernelGGL(delta_prep<DKP>, blocks, dim3(256), 0, st, a, ws);
-  // Few heads: where 16 columns a workgroup still find a CU each (us with delta_prep, quarters against 64 columns,
-  // 2048 tokens: 16, 32 and 64 heads of 128 x 128: 69 and 106, 79 and 111, 150 and 127; 64 and 128 heads of
-  // 64 x 64: 78 and 93, 145 and 123; 4 heads of 128 x 128, 8192 tokens: 216 and 359).
-  const bool few = heads * ceil_div(a.dv, 16) <= kCus;
-  const int cols = static_cast<int>(ceil_div(a.dv, few ? 16 : kCols));
-  const dim3 grid(static_cast<unsigned>(ceil_div(heads, 8) * 8 * cols));
-  if (few)
-    hipLaunchKernelGGL(delta_scan_quarters<DKP>, grid, dim3(512), 0, st, a, ws, cols);
+  // The narrowest workgroups that still find a CU each: a block takes a workgroup 1.6 us with 16 columns, 2.3 with
+  // 32, 2.7 with 64 (4 heads of 128 x 128), but the CU the same for any (us with delta_prep at 16, 32, 64 columns:
+  // 4 heads of 128 x 128, 8192 tokens 215, 311, 360; 32, 64, 128 of them, 2048 tokens 79, 100, 111; 150, 117, 127;
+  // 306, 238, 179; 128 heads of 64 x 64, 16 ragged prompts 437, 365, 397).
+  const auto scan = [&](auto kernel, int threads, int width) {
+    const int cols = static_cast<int>(ceil_div(a.dv, width));
+    const dim3 grid(static_cast<unsigned>(ceil_div(heads, 8) * 8 * cols));
+    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, a, ws, cols);
+  };
+  if (heads * ceil_div(a.dv, 16) <= kCus)
+    scan(delta_scan_quarters<DKP>, 512, 16);
+  else if (heads * ceil_div(a.dv, 32) <= kCus)
+    scan(delta_scan<DKP, 2>, 256, 32);
   else
-    hipLaunchKernelGGL(delta_scan<DKP>, grid, dim3(512), 0, st, a, ws, cols);
+    scan(delta_scan<DKP, 4>, 512, 64);
 }
 
 // sizes, strides and alignment shared by the prompt and the step
