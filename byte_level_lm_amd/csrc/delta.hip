@@ -337,12 +337,13 @@ __device__ inline void to_lds(Rows r, int at, void* lds) {
 }
 
 // LDS image of a block's keys or queries: rows of DKP values in 16-byte pieces,
-// the pieces of a row exchanged so that neither the rows of a tile at one piece
-// nor the 4 x 4 pieces of a transposing read meet in a bank
+// the pieces of a row exchanged so that neither the sixteen lanes of a fragment
+// read that LDS serves together (eight rows at one piece, eight at the next) nor
+// the 4 x 4 pieces of a transposing read meet in a bank
 template <int DKP>
 __device__ inline int swz(int row, int pc) {
-  if (DKP == 128) return row * 128 + ((pc ^ ((row & 3) << 2 | ((row >> 3) & 3))) << 3);
-  return row * 64 + ((pc ^ ((row & 2) << 1 | ((row >> 3) & 3))) << 3);
+  if (DKP == 128) return row * 128 + ((pc ^ ((row & 3) << 2 | (-(row >> 3) & 3))) << 3);
+  return row * 64 + ((pc ^ ((row & 2) << 1 | (-(row >> 3) & 3))) << 3);
 }
 
 // inclusive sum over the lanes of a wave, in fp64, by row shifts and readlanes

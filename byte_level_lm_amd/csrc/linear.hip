@@ -200,10 +200,11 @@ __device__ inline int tile_chan(int j, int r) {
 }
 
 // 16-byte piece p of row r of a staged tile (rows of kBK bytes) lies at piece
-// p ^ (r / 4 % 4), where tiles interleave at p ^ (r / 8 % 4): the sixteen rows
-// of a fragment read start in different banks
-__device__ inline int swz(int row, int p) { return row * kBK + ((p ^ ((row >> 2) & 3)) << 4); }
-__device__ inline int swz_pairs(int row, int p) { return row * kBK + ((p ^ ((row >> 3) & 3)) << 4); }
+// p ^ (-(r / 4) % 4), where tiles interleave at p ^ (-(r / 8) % 4): the sixteen
+// lanes that LDS serves together (four rows of one piece and four of another,
+// twice) start in different banks
+__device__ inline int swz(int row, int p) { return row * kBK + ((p ^ (-(row >> 2) & 3)) << 4); }
+__device__ inline int swz_pairs(int row, int p) { return row * kBK + ((p ^ (-(row >> 3) & 3)) << 4); }
 
 __device__ inline void to_lds(Buffer b, int at, int k, int8_t* lds) {
   typedef __attribute__((address_space(3))) void lds_void;
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
   int lt = t, lk = 0, off[U];
   Buffer bx, bw;
   static_assert(NW % 4 == 0, "row / 16 of a wave's loads is w modulo 4");
-  const int prow = lane >> 2, pkx = 16 * ((lane & 3) ^ ((lane >> 4) & 3)), pkw = kPairs ? 16 * ((lane & 3) ^ ((2 * w + (lane >> 5)) & 3)) : pkx;
+  const int prow = lane >> 2, pkx = 16 * ((lane & 3) ^ (-(lane >> 4) & 3)), pkw = kPairs ? 16 * ((lane & 3) ^ (-(2 * w + (lane >> 5)) & 3)) : pkx;
   const auto aim = [&]() __attribute__((always_inline)) {
     const Where at = tile_at(lt, mt, nt, TM, TN);
     const int rx = min(static_cast<int>(a.m) - at.row, TM), rw = min(static_cast<int>(a.n) - at.col, TN);
