@@ -34,6 +34,9 @@
 // from the state before it,
 //   S_t^T q = a_t S_{t-1}^T q + (k.q) u_t,
 // so a token costs one reduction over the eight lane groups.
+#include <algorithm>
+#include <cmath>
+
 #include "common.h"
 
 namespace bllm {
@@ -1068,7 +1071,7 @@ struct Ahead {
 // by the wave that made them) goes through LDS, with three barriers a block.
 // The chain from barrier to barrier bounds it: LDS latency, six to twelve products
 // and the cutting of a tile or two (4 heads of 128 x 128, 8192 tokens: 203 us,
-// 1.6 us a block; with one wave for all of it 3.1 us).
+// 1.6 us a block; with one wave for all of it 3.1 us; in five segments 41 + 56 us).
 template <int DKP>
 struct QuarterLds {
   struct {
@@ -1107,21 +1110,47 @@ __device__ inline void put_tile(uint32_t* f, int i, int lane, const floatx4& x) 
     *reinterpret_cast<uint2*>(f + (((i >> 1) * N + t) * 64 + lane) * 4 + 2 * (i & 1)) = make_uint2(w[2 * t], w[2 * t + 1]);
 }
 
-template <int DKP>
-__global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const float* ws, int cols) {
+// A long sequence of few heads in segments of `len` blocks.  The state after a
+// segment is linear in the state before it, S' = M S + N: kTransfer finds [N | M]
+// of every segment but the last at once, as the scan from a zero state and, with
+// zero values, from the unit columns; kSegments walks these to its segment's
+// first state, then scans the segment.
+enum Part { kWhole, kTransfer, kSegments };
+struct Segments {
+  float* m;  // for each segment and head DKP rows of [N | M], 16 ceil(dv / 16) + DKP values each
+  int len;
+};
+__device__ __host__ inline int64_t segment_slot(int64_t t0, int s, int len) { return t0 / kC / len + s; }
+
+template <int DKP, Part PART>
+__global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const float* ws, int cols, Segments sg) {
   constexpr int NS = DKP / 32, PR = DKP / 8, NK = PR / 4, TS = DKP / 64;  // TS: tiles of the state a wave holds
   __shared__ __align__(1024) QuarterLds<DKP> L;
   const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave & 3, tid = 64 * w + lane;
-  const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
-  if (head >= a.nseq * a.hv) return;
+  // the column parts of a head and segment follow each other on one XCD
+  const int id = blockIdx.x, part = id / 8 % cols, unit = id / (8 * cols) * 8 + id % 8, heads = a.nseq * a.hv;
+  const int seg = PART == kWhole ? 0 : unit / heads, head = unit - seg * heads;
+  if (PART == kWhole && unit >= heads) return;
   const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
   const int wcol = part * 16, col = wcol + n;
   const bool in = col < a.dv;
   int64_t t0, t1;
   seq_span(a, s, &t0, &t1);
+  const int64_t record = t0 / kC + s + (PART == kWhole ? 0 : int64_t(seg) * sg.len);
+  const int pitch = (a.dv + 15) / 16 * 16 + DKP;
+  const float* m = nullptr;  // of the sequence's first segment
+  bool last = true;
+  if (PART != kWhole) {
+    const int segments = max(static_cast<int>((t1 - t0 + int64_t(sg.len) * kC - 1) / (int64_t(sg.len) * kC)), 1);
+    last = seg == segments - 1;
+    if (PART == kTransfer ? seg >= segments - 1 : seg >= segments) return;
+    m = sg.m + (segment_slot(t0, s, sg.len) * a.hv + h) * DKP * pitch;
+    t0 += int64_t(seg) * sg.len * kC;
+    t1 = min(t1, t0 + int64_t(sg.len) * kC);
+  }
   const int blocks = static_cast<int>((t1 - t0 + kC - 1) / kC);
-  const float* rec = ws + ((t0 / kC + s) * a.hv + h) * kRec;
+  const float* rec = ws + (record * a.hv + h) * kRec;
   const int64_t next_rec = static_cast<int64_t>(a.hv) * kRec;
   const int t4 = tile_row(w, 4 * gq);  // the lane's tokens: t4 .. t4 + 3
   const auto frag = [&](const void* f, int i) __attribute__((always_inline)) {
@@ -1135,7 +1164,10 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int d = tile_row(TS * w + i, 4 * gq + r);
-        S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+        if (PART == kTransfer)
+          S[i][r] = d == wcol - (pitch - DKP) + n ? 1.0f : 0.0f;
+        else
+          S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
       }
     const auto put_state = [&]() __attribute__((always_inline)) {
       if constexpr (TS == 2) {
@@ -1211,7 +1243,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
       floatx4 U = ((u[2] + u[5]) + (u[1] + u[4])) + (u[0] + u[3]);
       if (__builtin_expect(tile_not_finite(U), 0)) lost = min(lost, cut_out_tile(&U, t4));
       if (gq == 0) L.lost[4 * n + w] = lost;
-      put_tile<2>(L.U, w, lane, U);
+      if (PART != kTransfer) put_tile<2>(L.U, w, lane, U);
       U[0] *= c3.x; U[1] *= c3.y; U[2] *= c3.z; U[3] *= c3.w;
       put_tile<3>(L.U + 4 * 256, w, lane, U);
       exchange_barrier();
@@ -1242,6 +1274,44 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
       }
       put_state();
     };
+    if constexpr (PART == kSegments) {
+      for (int j = 0; j < seg; ++j, m += static_cast<int64_t>(a.hv) * DKP * pitch) {  // S = M S + N
+        float4 row[TS][2 * NS];
+        floatx4 c[TS][3];
+#pragma unroll
+        for (int i = 0; i < TS; ++i) {
+          const float* of = m + tile_row(TS * w + i, n) * pitch + (pitch - DKP) + 8 * gq;
+#pragma unroll
+          for (int k = 0; k < 2 * NS; ++k) row[i][k] = *reinterpret_cast<const float4*>(of + 32 * (k >> 1) + 4 * (k & 1));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) c[i][0][r] = m[tile_row(TS * w + i, 4 * gq + r) * pitch + col];
+          c[i][1] = c[i][2] = floatx4{};
+        }
+        put_state();
+        exchange_barrier();
+#pragma unroll
+        for (int k = 0; k < NS; ++k) {
+          bf16x8 fs[3];
+#pragma unroll
+          for (int t = 0; t < 3; ++t) fs[t] = frag(L.S, 3 * k + t);
+#pragma unroll
+          for (int i = 0; i < TS; ++i) {
+            bf16x8 fm[3];
+            const float4 lo = row[i][2 * k], hi = row[i][2 * k + 1];
+            cut_pair<3>(floatx4{lo.x, lo.y, lo.z, lo.w}, floatx4{hi.x, hi.y, hi.z, hi.w}, fm);
+            c[i][2] = mfma_bf(fm[2], fs[0], c[i][2]);
+            c[i][1] = mfma_bf(fm[1], fs[0], c[i][1]);
+            c[i][0] = mfma_bf(fm[0], fs[0], c[i][0]);
+            c[i][2] = mfma_bf(fm[1], fs[1], c[i][2]);
+            c[i][1] = mfma_bf(fm[0], fs[1], c[i][1]);
+            c[i][2] = mfma_bf(fm[0], fs[2], c[i][2]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < TS; ++i) S[i] = (c[i][2] + c[i][1]) + c[i][0];
+        exchange_barrier();
+      }
+    }
     if (blocks > 0) {
       put_state();
       float eC = rec[kFrags + 256];
@@ -1253,7 +1323,15 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
         step(L.in[c & 1], e);
       }
     }
-    if (!a.state_out || !in) return;
+    if constexpr (PART == kTransfer) {
+      float* to = const_cast<float*>(m) + static_cast<int64_t>(seg) * a.hv * DKP * pitch + col;
+#pragma unroll
+      for (int i = 0; i < TS; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[tile_row(TS * w + i, 4 * gq + r) * pitch] = S[i][r];
+      return;
+    }
+    if (!a.state_out || !in || !last) return;
 #pragma unroll
     for (int i = 0; i < TS; ++i)
 #pragma unroll
@@ -1288,10 +1366,12 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
 #pragma unroll
     for (int i = 0; i < 5; ++i)
       if (i < 4 || w < 2) to_lds(R, (4 * i + w) * 1024 + 16 * lane, nT + (4 * i + w) * 512);
+    if (PART != kTransfer) {
 #pragma unroll
-    for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * 4 + w) * 512);
+      for (int i = 0; i < NK; ++i) to_lds(Q, aq[i], nQ + (i * 4 + w) * 512);
 #pragma unroll
-    for (int i = 0; i < 3; ++i) to_lds(R, 4 * kFragsT + (4 * i + w) * 1024 + 16 * lane, nP + (4 * i + w) * 512);
+      for (int i = 0; i < 3; ++i) to_lds(R, 4 * kFragsT + (4 * i + w) * 1024 + 16 * lane, nP + (4 * i + w) * 512);
+    }
     if (left > kC) rec += next_rec;
     pk += kC * a.ks;
     pq += kC * a.qs;
@@ -1317,7 +1397,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
                         uint16_t* __restrict__ nV, uint16_t* __restrict__ nT, uint16_t* __restrict__ nP,
                         float* __restrict__ nC, const uint32_t* __restrict__ xS, const uint32_t* __restrict__ xU,
                         const int* __restrict__ xLost, uint32_t* __restrict__ unused) __attribute__((always_inline)) {
-    if (!first) store_o();
+    if (PART != kTransfer && !first) store_o();
     done = left + kC;
     po += static_cast<int64_t>(kC) * os;
     fetch(nK, nQ, nV, nT, nP, nC);  // after the last block zeros and that block's T again: no branch around it
@@ -1325,6 +1405,10 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
     Next::touch(w, rec, pk, pq, pv + wcol, static_cast<int>(a.ks), static_cast<int>(a.qs), static_cast<int>(a.vs), left,
                 a.dk, a.dv - wcol, unused);
     exchange_barrier();  // leaves the reads of S0 before it to the waves that are waited for
+    if constexpr (PART == kTransfer) {
+      exchange_barrier();
+      return;
+    }
     floatx4 o[2] = {};
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
@@ -1371,6 +1455,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
   };
   if (blocks > 0) {
     fetch(L.in[0].K, L.in[0].Q, L.in[0].V, L.in[0].T, L.in[0].P, L.in[0].C);
+    for (int j = 0; PART == kSegments && j < 2 * seg; ++j) exchange_barrier();  // beside M S + N
     for (int c = 0; c < blocks; ++c) {
       const auto& now = L.in[c & 1];
       auto& then = L.in[(c & 1) ^ 1];
@@ -1380,7 +1465,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
         landed_barrier<Next::kLoads>();
       step(c == 0, now.Q, now.P, now.C, then.K, then.Q, then.V, then.T, then.P, then.C, L.S, L.U, L.lost, L.unused);
     }
-    store_o();
+    if (PART != kTransfer) store_o();
     __builtin_amdgcn_s_waitcnt(0x0F70);  // nothing is on its way into LDS when the workgroup ends
   }
 }
@@ -1392,26 +1477,61 @@ int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 constexpr int64_t kFew = 6;
 constexpr int64_t kCus = 256;
 
+// How a call's blocks are scanned: 4-byte words of the blocks' records and of the
+// whole workspace, and the segments' length in blocks with the most segments that
+// a sequence can have (0: each whole).
+struct Plan {
+  int64_t records, words;
+  int len, most;
+};
+// Segments where at least three of them find their workgroups a CU each, of [N | M] as of the scan.  A block more
+// in each costs 3 us, a segment more 2 to 3: lengths of 1.2 times the root of the blocks, at least 6.  (us with
+// delta_prep, whole and in 3, 5, 8, 12 segments: 1 head of 128 x 128, 8192 tokens 210, 142, 99, 82, 76; 4 heads,
+// which have CUs for 5, 212, 148, 106, 110, 138; 2048 tokens 63, 54, 47, 57, 78; 1024 tokens 37 either way; 16 heads,
+// which have them for 2, 231, 287, 314, 341, 416.)
+constexpr int64_t kMinLen = 6, kMinSegments = 3;
+Plan plan_of(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv) {
+  Plan p{ws_blocks(nseq, total) * hv * kRec, 0, 0, 0};
+  p.words = p.records;
+  const int64_t dkp = dk <= 64 ? 64 : 128, groups = nseq * hv * ceil_div(dv, 16), pairs = groups + nseq * hv * dkp / 16;
+  const int64_t blocks = ceil_div(total, kC), mean = ceil_div(blocks, nseq);
+  const int64_t at_once = std::min(kCus / groups, kCus / pairs + 1);
+  if (at_once < kMinSegments) return p;
+  const int64_t root = static_cast<int64_t>(std::ceil(1.2 * std::sqrt(static_cast<double>(mean))));
+  const int64_t len = std::max({kMinLen, root, ceil_div(mean, at_once)});
+  if (mean <= (kMinSegments - 1) * len) return p;
+  p.len = static_cast<int>(len);
+  p.most = static_cast<int>(ceil_div(blocks, len));
+  p.words += (p.most + nseq) * hv * dkp * (ceil_div(dv, 16) * 16 + dkp);
+  return p;
+}
+
 template <int DKP>
 void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
   const int64_t heads = int64_t(a.nseq) * a.hv;
   const dim3 blocks(static_cast<unsigned>(ws_blocks(a.nseq, a.total)), static_cast<unsigned>(a.hv));
   hipLaunchKernelGGL(delta_prep<DKP>, blocks, dim3(256), 0, st, a, ws);
+  const auto grid = [](int64_t units, int64_t cols) { return dim3(static_cast<unsigned>(ceil_div(units, 8) * 8 * cols)); };
+  const int by16 = static_cast<int>(ceil_div(a.dv, 16)), by32 = (by16 + 1) / 2, by64 = (by16 + 3) / 4;
+  const Plan plan = plan_of(a.nseq, a.total, a.hv, a.dk, a.dv);
   // The narrowest workgroups that still find a CU each: a block takes a workgroup 1.6 us with 16 columns, 2.3 with
   // 32, 2.7 with 64 (4 heads of 128 x 128), but the CU the same for any (us with delta_prep at 16, 32, 64 columns:
   // 4 heads of 128 x 128, 8192 tokens 215, 311, 360; 32, 64, 128 of them, 2048 tokens 79, 100, 111; 150, 117, 127;
   // 306, 238, 179; 128 heads of 64 x 64, 16 ragged prompts 437, 365, 397).
-  const auto scan = [&](auto kernel, int threads, int width) {
-    const int cols = static_cast<int>(ceil_div(a.dv, width));
-    const dim3 grid(static_cast<unsigned>(ceil_div(heads, 8) * 8 * cols));
-    hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, st, a, ws, cols);
-  };
-  if (heads * ceil_div(a.dv, 16) <= kCus)
-    scan(delta_scan_quarters<DKP>, 512, 16);
-  else if (heads * ceil_div(a.dv, 32) <= kCus)
-    scan(delta_scan<DKP, 2>, 256, 32);
-  else
-    scan(delta_scan<DKP, 4>, 512, 64);
+  if (plan.len) {
+    const Segments sg{ws + plan.records, plan.len};
+    const int both = by16 + DKP / 16;
+    hipLaunchKernelGGL((delta_scan_quarters<DKP, kTransfer>), grid(heads * (plan.most - 1), both), dim3(512), 0, st, a, ws,
+                       both, sg);
+    hipLaunchKernelGGL((delta_scan_quarters<DKP, kSegments>), grid(heads * plan.most, by16), dim3(512), 0, st, a, ws, by16,
+                       sg);
+  } else if (heads * by16 <= kCus) {
+    hipLaunchKernelGGL((delta_scan_quarters<DKP, kWhole>), grid(heads, by16), dim3(512), 0, st, a, ws, by16, Segments{});
+  } else if (heads * by32 <= kCus) {
+    hipLaunchKernelGGL((delta_scan<DKP, 2>), grid(heads, by32), dim3(256), 0, st, a, ws, by32);
+  } else {
+    hipLaunchKernelGGL((delta_scan<DKP, 4>), grid(heads, by64), dim3(512), 0, st, a, ws, by64);
+  }
 }
 
 // sizes, strides and alignment shared by the prompt and the step
@@ -1434,7 +1554,7 @@ using namespace bllm;
 
 extern "C" size_t bllm_gated_delta_workspace(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv) {
   if (nseq < 1 || total < 0 || hv < 1 || dk < 1 || dv < 1) return 0;
-  return static_cast<size_t>(ws_blocks(nseq, total)) * hv * kRec * 4;
+  return static_cast<size_t>(plan_of(nseq, total, hv, dk, dv).words) * 4;
 }
 
 extern "C" int bllm_gated_delta(const void* q, const void* k, const void* v, const float* g, const float* beta,

@@ -214,6 +214,9 @@ DELTA = [
     # enough heads and columns that a workgroup takes 64 columns; the others split a head's columns in sixteens
     ([70, 0, 9, 64] * 8, 2, 8, 128, 72), ([65, 3] * 20, 1, 8, 24, 40), ([33, 66] * 16, 8, 8, 128, 64),
     ([80, 1] * 16, 1, 8, 64, 128),
+    # long sequences of few heads, in segments
+    ([1600], 2, 2, 128, 128), ([1700], 1, 4, 64, 40), ([3000, 0, 100], 1, 1, 40, 24), ([1024], 1, 1, 128, 8),
+    ([64 * 21], 1, 2, 72, 136), ([1153, 1200], 1, 1, 8, 64),
     # few tokens a sequence on average, one of them long
     ([1, 0, 2] * 10 + [90], 2, 4, 64, 40), ([3, 5], 1, 2, 104, 136),
 ]
@@ -295,6 +298,37 @@ def test_gated_delta_nonfinite_stays_after_its_token_and_in_its_column(B, nseq, 
         S0[1, 1, 9, 33] = -np.inf
         lost[150:end, 1, 33] = True
         gone[1, 1, :, 33] = True
+    o, S = B.gated_delta(*_strided(q, k, v), to_dev(g), to_dev(beta), to_dev(off), state_in=to_dev(S0))
+    o, S = to_np(o), to_np(S)
+    assert not np.isfinite(o[lost]).any() and not np.isfinite(S[gone]).any()
+    assert np.isfinite(o[~lost]).all() and np.isfinite(S[~gone]).all()
+    _check_delta(to_dev(np.where(lost, o_o, o).astype(np.float32)), to_dev(np.where(gone, S_o, S).astype(np.float32)), o_o, S_o)
+
+
+@pytest.mark.parametrize("what", ["v nan", "k inf", "state", "gate"])
+def test_gated_delta_nonfinite_in_a_long_sequence(B, what):
+    """The same where a sequence of few heads goes in segments: what is lost starts at token 900 of head 1 (or at 0)."""
+    rng = np.random.default_rng(17)
+    off, q, k, v, g, beta = _delta_inputs(rng, [2000], 1, 2, 64, 48, spread=0.05)
+    S0 = rng.standard_normal((1, 2, 64, 48)).astype(np.float32)
+    o_o, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=0.125, unit_qk=True, state=S0)
+    lost, gone = np.zeros(o_o.shape, bool), np.zeros(S_o.shape, bool)
+    if what == "v nan":
+        v[900, 1, 3] = np.nan
+        lost[900:, 1, 3] = True
+        gone[0, 1, :, 3] = True
+    elif what == "state":
+        S0[0, 1, 9, 33] = np.nan
+        lost[:, 1, 33] = True
+        gone[0, 1, :, 33] = True
+    elif what == "gate":
+        g[900, 1] = np.nan
+        lost[900:, 1] = True
+        gone[0, 1] = True
+    else:  # the key's heads share it
+        k[900, 0, 5] = np.inf
+        lost[900:] = True
+        gone[0] = True
     o, S = B.gated_delta(*_strided(q, k, v), to_dev(g), to_dev(beta), to_dev(off), state_in=to_dev(S0))
     o, S = to_np(o), to_np(S)
     assert not np.isfinite(o[lost]).any() and not np.isfinite(S[gone]).any()
