@@ -1113,11 +1113,14 @@ __device__ inline void put_tile(uint32_t* f, int i, int lane, const floatx4& x) 
 // A long sequence of few heads in segments of `len` blocks.  The state after a
 // segment is linear in the state before it, S' = M S + N: kTransfer finds [N | M]
 // of every segment but the last at once, as the scan from a zero state and, with
-// zero values, from the unit columns; kSegments walks these to its segment's
-// first state, then scans the segment.
+// zero values, from the unit columns; the first segment starts from its state
+// and needs no M.  kSegments walks these to its segment's first state, then
+// scans the segment.  The sequence's state is copied by kTransfer, so that in
+// kSegments nobody reads the array to which the last segment may write.
 enum Part { kWhole, kTransfer, kSegments };
 struct Segments {
-  float* m;  // for each segment and head DKP rows of [N | M], 16 ceil(dv / 16) + DKP values each
+  float* m;      // for each segment and head DKP rows of [N | M], 16 ceil(dv / 16) + DKP values each
+  float* first;  // for each sequence and head DKP rows of its state, 16 ceil(dv / 16) values each
   int len;
 };
 __device__ __host__ inline int64_t segment_slot(int64_t t0, int s, int len) { return t0 / kC / len + s; }
@@ -1139,12 +1142,13 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
   seq_span(a, s, &t0, &t1);
   const int64_t record = t0 / kC + s + (PART == kWhole ? 0 : int64_t(seg) * sg.len);
   const int pitch = (a.dv + 15) / 16 * 16 + DKP;
-  const float* m = nullptr;  // of the sequence's first segment
+  float *m = nullptr, *first = nullptr;  // [N | M] of the sequence's first segment
   bool last = true;
   if (PART != kWhole) {
     const int segments = max(static_cast<int>((t1 - t0 + int64_t(sg.len) * kC - 1) / (int64_t(sg.len) * kC)), 1);
     last = seg == segments - 1;
-    if (PART == kTransfer ? seg >= segments - 1 : seg >= segments) return;
+    if (PART == kTransfer ? seg >= segments - 1 || (seg == 0 && wcol >= pitch - DKP) : seg >= segments) return;
+    if (segments > 1) first = sg.first + static_cast<int64_t>(head) * DKP * (pitch - DKP) + col;
     m = sg.m + (segment_slot(t0, s, sg.len) * a.hv + h) * DKP * pitch;
     t0 += int64_t(seg) * sg.len * kC;
     t1 = min(t1, t0 + int64_t(sg.len) * kC);
@@ -1164,10 +1168,19 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int d = tile_row(TS * w + i, 4 * gq + r);
-        if (PART == kTransfer)
+        const auto given = [&]() {
+          return a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+        };
+        if (PART == kTransfer && seg > 0)
           S[i][r] = d == wcol - (pitch - DKP) + n ? 1.0f : 0.0f;
+        else if (PART == kTransfer)
+          first[d * (pitch - DKP)] = S[i][r] = given();
+        else if (PART == kSegments && seg > 0)
+          S[i][r] = m[d * pitch + col];
+        else if (PART == kSegments && first)
+          S[i][r] = first[d * (pitch - DKP)];
         else
-          S[i][r] = a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
+          S[i][r] = given();
       }
     const auto put_state = [&]() __attribute__((always_inline)) {
       if constexpr (TS == 2) {
@@ -1275,7 +1288,8 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
       put_state();
     };
     if constexpr (PART == kSegments) {
-      for (int j = 0; j < seg; ++j, m += static_cast<int64_t>(a.hv) * DKP * pitch) {  // S = M S + N
+      for (int j = 1; j < seg; ++j) {  // S = M S + N
+        m += static_cast<int64_t>(a.hv) * DKP * pitch;
         float4 row[TS][2 * NS];
         floatx4 c[TS][3];
 #pragma unroll
@@ -1324,7 +1338,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
       }
     }
     if constexpr (PART == kTransfer) {
-      float* to = const_cast<float*>(m) + static_cast<int64_t>(seg) * a.hv * DKP * pitch + col;
+      float* to = m + static_cast<int64_t>(seg) * a.hv * DKP * pitch + col;
 #pragma unroll
       for (int i = 0; i < TS; ++i)
 #pragma unroll
@@ -1455,7 +1469,7 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
   };
   if (blocks > 0) {
     fetch(L.in[0].K, L.in[0].Q, L.in[0].V, L.in[0].T, L.in[0].P, L.in[0].C);
-    for (int j = 0; PART == kSegments && j < 2 * seg; ++j) exchange_barrier();  // beside M S + N
+    for (int j = 2; PART == kSegments && j < 2 * seg; ++j) exchange_barrier();  // beside M S + N
     for (int c = 0; c < blocks; ++c) {
       const auto& now = L.in[c & 1];
       auto& then = L.in[(c & 1) ^ 1];
@@ -1477,11 +1491,11 @@ int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 constexpr int64_t kFew = 6;
 constexpr int64_t kCus = 256;
 
-// How a call's blocks are scanned: 4-byte words of the blocks' records and of the
-// whole workspace, and the segments' length in blocks with the most segments that
-// a sequence can have (0: each whole).
+// How a call's blocks are scanned: 4-byte words of the blocks' records, to the end
+// of the segments' maps and of the whole workspace, and the segments' length in
+// blocks with the most segments that a sequence can have (0: each whole).
 struct Plan {
-  int64_t records, words;
+  int64_t records, maps, words;
   int len, most;
 };
 // Segments where at least three of them find their workgroups a CU each, of [N | M] as of the scan.  A block more
@@ -1491,18 +1505,19 @@ struct Plan {
 // which have them for 2, 231, 287, 314, 341, 416.)
 constexpr int64_t kMinLen = 6, kMinSegments = 3;
 Plan plan_of(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv) {
-  Plan p{ws_blocks(nseq, total) * hv * kRec, 0, 0, 0};
+  Plan p{ws_blocks(nseq, total) * hv * kRec, 0, 0, 0, 0};
   p.words = p.records;
-  const int64_t dkp = dk <= 64 ? 64 : 128, groups = nseq * hv * ceil_div(dv, 16), pairs = groups + nseq * hv * dkp / 16;
+  const int64_t dkp = dk <= 64 ? 64 : 128, groups = nseq * hv * ceil_div(dv, 16), units = nseq * hv * dkp / 16;
   const int64_t blocks = ceil_div(total, kC), mean = ceil_div(blocks, nseq);
-  const int64_t at_once = std::min(kCus / groups, kCus / pairs + 1);
+  const int64_t at_once = std::min(kCus / groups, (kCus + groups + 2 * units) / (groups + units));
   if (at_once < kMinSegments) return p;
   const int64_t root = static_cast<int64_t>(std::ceil(1.2 * std::sqrt(static_cast<double>(mean))));
   const int64_t len = std::max({kMinLen, root, ceil_div(mean, at_once)});
   if (mean <= (kMinSegments - 1) * len) return p;
   p.len = static_cast<int>(len);
   p.most = static_cast<int>(ceil_div(blocks, len));
-  p.words += (p.most + nseq) * hv * dkp * (ceil_div(dv, 16) * 16 + dkp);
+  p.maps = p.records + (p.most + nseq) * hv * dkp * (ceil_div(dv, 16) * 16 + dkp);
+  p.words = p.maps + nseq * hv * dkp * ceil_div(dv, 16) * 16;
   return p;
 }
 
@@ -1519,7 +1534,7 @@ void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
   // 4 heads of 128 x 128, 8192 tokens 215, 311, 360; 32, 64, 128 of them, 2048 tokens 79, 100, 111; 150, 117, 127;
   // 306, 238, 179; 128 heads of 64 x 64, 16 ragged prompts 437, 365, 397).
   if (plan.len) {
-    const Segments sg{ws + plan.records, plan.len};
+    const Segments sg{ws + plan.records, ws + plan.maps, plan.len};
     const int both = by16 + DKP / 16;
     hipLaunchKernelGGL((delta_scan_quarters<DKP, kTransfer>), grid(heads * (plan.most - 1), both), dim3(512), 0, st, a, ws,
                        both, sg);
