@@ -16,7 +16,7 @@
 // four or five cycles, so the scans leave to a wave on the way from state to state
 // what only it can do and give outputs and loads to others.  delta_scan, for many
 // heads, has 16 columns and every row on a wave; delta_scan_quarters, for few, a
-// quarter of the rows.  What one product makes the next takes as it lies: a
+// quarter of the rows, and takes long sequences in segments at once.  What one product makes the next takes as it lies: a
 // 16 x 16 accumulator has a lane's four rows where the next product wants its
 // inner index, once the tiles' rows are numbered 8 (r / 4) + r % 4 (+ 4 for the
 // second tile of a pair), which costs nothing.
