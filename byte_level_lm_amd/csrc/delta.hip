@@ -1071,7 +1071,7 @@ struct Ahead {
 // by the wave that made them) goes through LDS, with three barriers a block.
 // The chain from barrier to barrier bounds it: LDS latency, six to twelve products
 // and the cutting of a tile or two (4 heads of 128 x 128, 8192 tokens: 203 us,
-// 1.6 us a block; with one wave for all of it 3.1 us; in five segments 41 + 56 us).
+// 1.6 us a block; with one wave for all of it 3.1 us; in five segments 41 + 50 us).
 template <int DKP>
 struct QuarterLds {
   struct {
@@ -1119,10 +1119,11 @@ __device__ inline void put_tile(uint32_t* f, int i, int lane, const floatx4& x) 
 // kSegments nobody reads the array to which the last segment may write.
 enum Part { kWhole, kTransfer, kSegments };
 struct Segments {
-  float* m;      // for each segment and head DKP rows of [N | M], 16 ceil(dv / 16) + DKP values each
+  float* m;      // for each segment and head N, DKP rows of 16 ceil(dv / 16) values, and M's fragments in three bf16 terms
   float* first;  // for each sequence and head DKP rows of its state, 16 ceil(dv / 16) values each
   int len;
 };
+__device__ __host__ constexpr int map_words(int dkp, int pitch) { return dkp * pitch + dkp * dkp * 3 / 2; }
 __device__ __host__ inline int64_t segment_slot(int64_t t0, int s, int len) { return t0 / kC / len + s; }
 
 template <int DKP, Part PART>
@@ -1141,15 +1142,15 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
   int64_t t0, t1;
   seq_span(a, s, &t0, &t1);
   const int64_t record = t0 / kC + s + (PART == kWhole ? 0 : int64_t(seg) * sg.len);
-  const int pitch = (a.dv + 15) / 16 * 16 + DKP;
+  const int pitch = (a.dv + 15) / 16 * 16, next_map = a.hv * map_words(DKP, pitch);
   float *m = nullptr, *first = nullptr;  // [N | M] of the sequence's first segment
   bool last = true;
   if (PART != kWhole) {
     const int segments = max(static_cast<int>((t1 - t0 + int64_t(sg.len) * kC - 1) / (int64_t(sg.len) * kC)), 1);
     last = seg == segments - 1;
-    if (PART == kTransfer ? seg >= segments - 1 || (seg == 0 && wcol >= pitch - DKP) : seg >= segments) return;
-    if (segments > 1) first = sg.first + static_cast<int64_t>(head) * DKP * (pitch - DKP) + col;
-    m = sg.m + (segment_slot(t0, s, sg.len) * a.hv + h) * DKP * pitch;
+    if (PART == kTransfer ? seg >= segments - 1 || (seg == 0 && wcol >= pitch) : seg >= segments) return;
+    if (segments > 1) first = sg.first + static_cast<int64_t>(head) * DKP * pitch + col;
+    m = sg.m + (segment_slot(t0, s, sg.len) * a.hv + h) * map_words(DKP, pitch);
     t0 += int64_t(seg) * sg.len * kC;
     t1 = min(t1, t0 + int64_t(sg.len) * kC);
   }
@@ -1172,13 +1173,13 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
           return a.state_in && in && d < a.dk ? a.state_in[at + static_cast<int64_t>(d) * a.dv] : 0.0f;
         };
         if (PART == kTransfer && seg > 0)
-          S[i][r] = d == wcol - (pitch - DKP) + n ? 1.0f : 0.0f;
+          S[i][r] = d == wcol - pitch + n ? 1.0f : 0.0f;
         else if (PART == kTransfer)
-          first[d * (pitch - DKP)] = S[i][r] = given();
+          first[d * pitch] = S[i][r] = given();
         else if (PART == kSegments && seg > 0)
           S[i][r] = m[d * pitch + col];
         else if (PART == kSegments && first)
-          S[i][r] = first[d * (pitch - DKP)];
+          S[i][r] = first[d * pitch];
         else
           S[i][r] = given();
       }
@@ -1289,14 +1290,15 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
     };
     if constexpr (PART == kSegments) {
       for (int j = 1; j < seg; ++j) {  // S = M S + N
-        m += static_cast<int64_t>(a.hv) * DKP * pitch;
-        float4 row[TS][2 * NS];
+        m += next_map;
+        bf16x8 fm[TS][NS][3];
         floatx4 c[TS][3];
 #pragma unroll
         for (int i = 0; i < TS; ++i) {
-          const float* of = m + tile_row(TS * w + i, n) * pitch + (pitch - DKP) + 8 * gq;
 #pragma unroll
-          for (int k = 0; k < 2 * NS; ++k) row[i][k] = *reinterpret_cast<const float4*>(of + 32 * (k >> 1) + 4 * (k & 1));
+          for (int k = 0; k < NS; ++k)
+#pragma unroll
+            for (int t = 0; t < 3; ++t) fm[i][k][t] = frag(m + DKP * pitch, ((TS * w + i) * NS + k) * 3 + t);
 #pragma unroll
           for (int r = 0; r < 4; ++r) c[i][0][r] = m[tile_row(TS * w + i, 4 * gq + r) * pitch + col];
           c[i][1] = c[i][2] = floatx4{};
@@ -1310,15 +1312,12 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
           for (int t = 0; t < 3; ++t) fs[t] = frag(L.S, 3 * k + t);
 #pragma unroll
           for (int i = 0; i < TS; ++i) {
-            bf16x8 fm[3];
-            const float4 lo = row[i][2 * k], hi = row[i][2 * k + 1];
-            cut_pair<3>(floatx4{lo.x, lo.y, lo.z, lo.w}, floatx4{hi.x, hi.y, hi.z, hi.w}, fm);
-            c[i][2] = mfma_bf(fm[2], fs[0], c[i][2]);
-            c[i][1] = mfma_bf(fm[1], fs[0], c[i][1]);
-            c[i][0] = mfma_bf(fm[0], fs[0], c[i][0]);
-            c[i][2] = mfma_bf(fm[1], fs[1], c[i][2]);
-            c[i][1] = mfma_bf(fm[0], fs[1], c[i][1]);
-            c[i][2] = mfma_bf(fm[0], fs[2], c[i][2]);
+            c[i][2] = mfma_bf(fm[i][k][2], fs[0], c[i][2]);
+            c[i][1] = mfma_bf(fm[i][k][1], fs[0], c[i][1]);
+            c[i][0] = mfma_bf(fm[i][k][0], fs[0], c[i][0]);
+            c[i][2] = mfma_bf(fm[i][k][1], fs[1], c[i][2]);
+            c[i][1] = mfma_bf(fm[i][k][0], fs[1], c[i][1]);
+            c[i][2] = mfma_bf(fm[i][k][0], fs[2], c[i][2]);
           }
         }
 #pragma unroll
@@ -1338,11 +1337,30 @@ __global__ __launch_bounds__(512) void delta_scan_quarters(DeltaArgs a, const fl
       }
     }
     if constexpr (PART == kTransfer) {
-      float* to = m + static_cast<int64_t>(seg) * a.hv * DKP * pitch + col;
+      m += seg * static_cast<int64_t>(next_map);
+      if (wcol < pitch) {
 #pragma unroll
-      for (int i = 0; i < TS; ++i)
+        for (int i = 0; i < TS; ++i)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[tile_row(TS * w + i, 4 * gq + r) * pitch] = S[i][r];
+          for (int r = 0; r < 4; ++r) m[tile_row(TS * w + i, 4 * gq + r) * pitch + col] = S[i][r];
+      } else {  // column c of M: value c % 8 of the lanes of its eight columns and this row
+        const int c = col - pitch;
+        uint16_t* to = reinterpret_cast<uint16_t*>(m + DKP * pitch) +
+                       ((TS * w * NS + (c >> 5)) * 192 + ((c & 31) >> 3) * 16 + 4 * gq) * 8 + (c & 7);
+#pragma unroll
+        for (int i = 0; i < TS; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            uint32_t terms[3];
+            cut<3>(S[i][r], S[i][r + 1], terms, 1);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+              uint16_t* at = to + (i * NS * 192 + t * 64 + r) * 8;
+              at[0] = static_cast<uint16_t>(terms[t]);
+              at[8] = static_cast<uint16_t>(terms[t] >> 16);
+            }
+          }
+      }
       return;
     }
     if (!a.state_out || !in || !last) return;
@@ -1516,7 +1534,7 @@ Plan plan_of(int64_t nseq, int64_t total, int64_t hv, int64_t dk, int64_t dv) {
   if (mean <= (kMinSegments - 1) * len) return p;
   p.len = static_cast<int>(len);
   p.most = static_cast<int>(ceil_div(blocks, len));
-  p.maps = p.records + (p.most + nseq) * hv * dkp * (ceil_div(dv, 16) * 16 + dkp);
+  p.maps = p.records + (p.most + nseq) * hv * map_words(static_cast<int>(dkp), static_cast<int>(ceil_div(dv, 16) * 16));
   p.words = p.maps + nseq * hv * dkp * ceil_div(dv, 16) * 16;
   return p;
 }
