@@ -370,6 +370,26 @@ def test_gated_delta_offsets_outside_the_batch_stay_inside(B):
     _check_delta(o, S, o_o, S_o)
 
 
+@pytest.mark.parametrize("lengths,hv,dk,dv", [([2000], 2, 128, 128), ([1700, 64, 1], 1, 64, 40), ([1024], 1, 8, 8),
+                                              ([150] * 40, 8, 128, 64), ([130], 1, 72, 136)])
+def test_gated_delta_stays_in_its_workspace(B, lengths, hv, dk, dv):
+    """The size that the library names is enough: nothing behind it is written; a smaller one is refused."""
+    import torch
+    rng = np.random.default_rng(18)
+    say("workspace", lengths[:3], hv, dk, dv)
+    off, q, k, v, g, beta = _delta_inputs(rng, lengths, hv, hv, dk, dv, spread=0.05)
+    size = B.gated_delta_workspace(len(lengths), int(off[-1]), hv, dk, dv)
+    buf = torch.full((size + 65536,), 0x5A, dtype=torch.uint8, device="cuda")
+    S0 = rng.standard_normal((len(lengths), hv, dk, dv)).astype(np.float32)
+    o_o, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=dk ** -0.5, unit_qk=True, state=S0)
+    args = (*_strided(q, k, v), to_dev(g), to_dev(beta), to_dev(off))
+    o, S = B.gated_delta(*args, state_in=to_dev(S0), ws=buf[:size])
+    _check_delta(o, S, o_o, S_o)
+    assert torch.all(buf[size:] == 0x5A)
+    with pytest.raises(ValueError):
+        B.gated_delta(*args, state_in=to_dev(S0), ws=buf[:size - 4])
+
+
 @pytest.mark.parametrize("nseq,hk,hv,dk,dv", [(1, 1, 1, 8, 8), (1, 4, 4, 128, 128), (5, 2, 4, 64, 64), (33, 1, 3, 40, 72),
                                               (3, 1, 1, 16, 1024), (130, 2, 2, 128, 32)])
 @pytest.mark.parametrize("unit", [True, False])
