@@ -28,8 +28,8 @@
 // zero of T or P: such entries are cut out of the products, and what depends
 // on them (its column's later rows and state) is set to NaN afterwards.
 //
-// Recurrent form, for steps and prompts of a few tokens.  A wave owns 32 columns of one head's state: lane (i, c),
-// i = lane / 8, c = lane % 8, holds rows R i .. R i + R - 1 of columns
+// Recurrent form, for steps and prompts of a few tokens.  A wave owns 32 columns
+// of one head's state: lane (i, c), i = lane / 8, c = lane % 8, holds rows R i .. R i + R - 1 of columns
 // 4 c .. 4 c + 3 in registers.  Both sums over dk that a token needs are taken
 // from the state before it,
 //   S_t^T q = a_t S_{t-1}^T q + (k.q) u_t,
@@ -506,7 +506,8 @@ __global__ __launch_bounds__(256, 4) void delta_prep(DeltaArgs a, float* ws) {
         }
       }
     }
-    if (__builtin_expect(__any(z != 0.0f), 0)) {  // entries that are not finite: none enters the inverse, rows from the first on are lost
+    if (__builtin_expect(__any(z != 0.0f), 0)) {
+      // entries that are not finite: none enters the inverse, rows from the first on are lost
 #pragma unroll
       for (int part = 0; part < 2; ++part) {
         const int i = part ? i1 : i0, t = 16 * i + 4 * gq;
@@ -767,7 +768,8 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
       for (int k = 0; k < NS; ++k) {
         bf16x8 fk[4], f[3];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fk[i] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(tile_row(i, n), 4 * k + gq)));
+        for (int i = 0; i < 4; ++i)
+          fk[i] = as_frag(*reinterpret_cast<const uint4*>(sK + swz<DKP>(tile_row(i, n), 4 * k + gq)));
         cut_pair<3>(S[2 * k], S[2 * k + 1], f);
 #pragma unroll
         for (int t = 0; t < 2; ++t) *reinterpret_cast<bf16x8*>(L.S[w] + ((2 * k + t) * 64 + lane) * 4) = f[t];
@@ -992,7 +994,8 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
     done = tokens;
   };
   const auto second_half = [&](uint16_t* __restrict__ nP, uint16_t* __restrict__ nV, const uint16_t* __restrict__ sQ,
-                               const uint32_t* __restrict__ sS, const float* __restrict__ sC) __attribute__((always_inline)) {
+                               const uint32_t* __restrict__ sS,
+                               const float* __restrict__ sC) __attribute__((always_inline)) {
     const Rows R = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(recp), 0, 4 * kRec, 0x00027000);
 #pragma unroll
     for (int i = 0; i < 12 / G; ++i) to_lds(R, 4 * kFragsT + (i * G + w) * 1024 + 16 * lane, nP + (i * G + w) * 512);
@@ -1006,7 +1009,8 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
 #pragma unroll
       for (int t = 0; t < 2; ++t) f[t] = frag(sS, 2 * k + t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(i, n), 4 * k + gq)));
+      for (int i = 0; i < 4; ++i)
+        fq[i] = as_frag(*reinterpret_cast<const uint4*>(sQ + swz<DKP>(tile_row(i, n), 4 * k + gq)));
 #pragma unroll
       for (int t = 1; t >= 0; --t)
 #pragma unroll
@@ -1036,7 +1040,8 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
 
 // Brings a block's lines into L2, a quarter of a kilobyte of LDS taking what nobody reads:
 // the way from memory is about as long as a block takes, so the loads into LDS alone,
-// a block ahead, come late (8 heads of 64 x 64, 16 ragged prompts: 390 us without, 333 with).
+// a block ahead, come late (16 ragged prompts of 8 heads of 64 x 64 at 16 columns a workgroup: 390
+// us without, 333 with).
 // NV lines of 64 columns of v; every wave of NW issues kLoads.
 template <int DKP, int NV, int NW>
 struct Ahead {
@@ -1051,7 +1056,9 @@ struct Ahead {
       int64_t base = reinterpret_cast<int64_t>(rec);
       int stride = 64, line = 8192 * u, width = 0, bytes = 4 * kRec;
       if (m >= 0) {
-        base = m < kRows ? reinterpret_cast<int64_t>(k) : m < 2 * kRows ? reinterpret_cast<int64_t>(q) : reinterpret_cast<int64_t>(v);
+        base = m < kRows       ? reinterpret_cast<int64_t>(k)
+               : m < 2 * kRows ? reinterpret_cast<int64_t>(q)
+                               : reinterpret_cast<int64_t>(v);
         stride = m < kRows ? +ks : m < 2 * kRows ? +qs : +vs;
         width = m < 2 * kRows ? +dk : +dv;
         line = 128 * (m < kRows ? m : m < 2 * kRows ? m - kRows : m - 2 * kRows);
@@ -1574,8 +1581,8 @@ int delta_check(const DeltaArgs& a, int dtype, int64_t nseq, int64_t hk, int64_t
     return BLLM_E_INVAL;
   if (a.total > 0 && (!a.q || !a.k || !a.v || !a.g || !a.beta || !a.o)) return BLLM_E_INVAL;
   if (dtype != BLLM_BF16 || dk % 8 != 0 || dk > 128 || dv % 8 != 0 || dv > 1024 || hv > 1024 || nseq > 65535 ||
-      a.total >= (int64_t(1) << 31) || a.qs >= kMaxStride || a.ks >= kMaxStride || a.vs >= kMaxStride || a.qs % 8 != 0 || a.ks % 8 != 0 || a.vs % 8 != 0 || !aligned16(a.q) ||
-      !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.o) || !aligned16(a.state_in) || !aligned16(a.state_out))
+      a.total >= (int64_t(1) << 31) || a.qs >= kMaxStride || a.ks >= kMaxStride || a.vs >= kMaxStride ||
+      a.qs % 8 != 0 || a.ks % 8 != 0 || a.vs % 8 != 0 || !aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.o) || !aligned16(a.state_in) || !aligned16(a.state_out))
     return BLLM_E_NOTSUP;
   return BLLM_OK;
 }

@@ -385,6 +385,8 @@ def _is(name, t, shape, dtype):
 def _out(name, t, shape, dtype, like):
     """The caller's output, or a new one on the device of ``like``."""
     if t is None:
+        if like.shape == shape:  # half the time of building the shape again
+            return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
         return like.new_empty(shape, dtype=dtype)
     _is(name, t, shape, dtype)
     return t
@@ -486,7 +488,7 @@ def _delta_args(q, k, v, g, beta, o_out):
         raise TypeError("q, k and v must have one dtype")
     _is("g", g, (total, hv), torch.float32)
     _is("beta", beta, (total, hv), torch.float32)
-    o_out = _out("o_out", o_out, (total, hv, dv), dt, q)
+    o_out = _out("o_out", o_out, v.shape, dt, v)
     return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), _dt(q)),
             (hk, hv, dk, dv, *strides), o_out)
 
