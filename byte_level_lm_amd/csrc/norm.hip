@@ -4,7 +4,9 @@
 //   s = x + residual (fp32),  r = 1 / sqrt(mean(s^2) + eps),  y = (s w) r
 //   8 bits: t = s w,  a = max |t|,  q = rne(t * (127 * (1 / a))),  scale = a r / 127
 // r divides out of q, so q depends on no sum's order: it is the same whole
-// number whatever the split of the row over threads.
+// number whatever the split of the row over threads.  a is the maximum of the
+// bits of |t|: in that order infinity lies above every finite value and NaN
+// above infinity, so neither can leave a row with a finite scale.
 //
 // Bound by the bytes: x and the residual are read once, held in registers as
 // they came (a row's 16-byte pieces over the lanes) and the outputs written
@@ -47,15 +49,18 @@ __device__ inline void unpack(const uint4& v, float* x) {
 }
 __device__ inline uint4 piece(const void* p, int64_t i) { return static_cast<const uint4*>(p)[i]; }
 
-// the row's divisor and 8-bit scales from its sum of squares and largest |t|
+// |t| as the maximum takes it
+__device__ inline uint32_t magnitude(float t) { return __float_as_uint(t) & 0x7FFFFFFFu; }
+
+// the row's divisor and 8-bit scales from its sum of squares and the bits of its largest |t|
 struct RowScale {
   float r, inv, scale;
 };
-__device__ inline RowScale row_scale(const NormArgs& a, float ss, float top) {
+__device__ inline RowScale row_scale(const NormArgs& a, float ss, uint32_t bits) {
   RowScale s;
-  // a NaN in the row is lost by the maximum but not by the sum: it reaches r, y and the scale
-  s.r = a.w ? 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps) : (ss == ss ? 1.0f : ss);
-  const bool some = !(top < kTiny);
+  const float top = __uint_as_float(bits);
+  s.r = a.w ? 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps) : 1.0f;
+  const bool some = !(top < kTiny);  // also where top is NaN, which then is the scale
   s.inv = some ? 127.0f * (1.0f / top) : 0.0f;
   s.scale = some ? top * s.r / 127.0f : 0.0f;
   return s;
@@ -115,9 +120,9 @@ __device__ inline void weights(const NormArgs& a, int64_t c, float* w) {
 }
 
 template <int G>
-__device__ inline float group_max(float v) {
+__device__ inline uint32_t group_max(uint32_t v) {
 #pragma unroll
-  for (int off = G / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, kWave));
+  for (int off = G / 2; off >= 1; off >>= 1) v = max(v, __shfl_xor(v, off, kWave));
   return v;
 }
 
@@ -125,7 +130,8 @@ __device__ inline float group_max(float v) {
 template <int DT, bool RES, bool Q8, int G, int P>
 __global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
   constexpr int N = Vec<DT>::N, NT = G > 256 ? G : 256, GW = G < 64 ? G : 64;
-  __shared__ float sSum[16], sMax[16];
+  __shared__ float sSum[16];
+  __shared__ uint32_t sMax[16];
   const int pieces = a.d / N, in = threadIdx.x % G;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (NT / G) + threadIdx.x / G;
   if (G <= 64 && row >= a.rows) return;
@@ -140,7 +146,8 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
       if (RES) r[p] = piece(a.res, base + c);
     }
   }
-  float ss = 0.0f, top = 0.0f;
+  float ss = 0.0f;
+  uint32_t top = 0;
 #pragma unroll
   for (int p = 0; p < P; ++p) {
     const int c = in + p * G;
@@ -151,7 +158,7 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       ss = fmaf(s[i], s[i], ss);
-      if (Q8) top = fmaxf(top, fabsf(s[i] * w[i]));
+      if (Q8) top = max(top, magnitude(s[i] * w[i]));
     }
   }
   ss = group_sum<GW>(ss);
@@ -162,11 +169,12 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
       sMax[threadIdx.x >> 6] = top;
     }
     __syncthreads();
-    ss = top = 0.0f;
+    ss = 0.0f;
+    top = 0;
 #pragma unroll
     for (int i = 0; i < G / 64; ++i) {
       ss += sSum[i];
-      top = fmaxf(top, sMax[i]);
+      top = max(top, sMax[i]);
     }
   }
   const RowScale rs = row_scale(a, ss, top);
@@ -186,10 +194,12 @@ __global__ __launch_bounds__(G > 256 ? G : 256) void norm_rows(NormArgs a) {
 template <int DT, bool RES, bool Q8>
 __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
   constexpr int N = Vec<DT>::N;
-  __shared__ float sSum[16], sMax[16];
+  __shared__ float sSum[16];
+  __shared__ uint32_t sMax[16];
   const int pieces = a.d / N;
   const int64_t base = static_cast<int64_t>(blockIdx.x) * pieces;
-  float ss = 0.0f, top = 0.0f;
+  float ss = 0.0f;
+  uint32_t top = 0;
   for (int c = threadIdx.x; c < pieces; c += 1024) {
     float s[N], w[N];
     sum_piece<DT, RES>(piece(a.x, base + c), RES ? piece(a.res, base + c) : uint4{}, s);
@@ -197,7 +207,7 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       ss = fmaf(s[i], s[i], ss);
-      top = fmaxf(top, fabsf(s[i] * w[i]));
+      top = max(top, magnitude(s[i] * w[i]));
     }
   }
   ss = group_sum<64>(ss);
@@ -207,10 +217,11 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
     sMax[threadIdx.x >> 6] = top;
   }
   __syncthreads();
-  ss = top = 0.0f;
+  ss = 0.0f;
+  top = 0;
   for (int i = 0; i < 16; ++i) {
     ss += sSum[i];
-    top = fmaxf(top, sMax[i]);
+    top = max(top, sMax[i]);
   }
   const RowScale rs = row_scale(a, ss, top);
   for (int c = threadIdx.x; c < pieces; c += 1024) {

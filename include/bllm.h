@@ -407,8 +407,9 @@ int bllm_rmsnorm(const void* x, const void* residual, const void* w, int dtype, 
  *   scale_out = a / (127 sqrt(mean(s^2) + eps)),
  * so y ~ q_out * scale_out.  The norm's divisor cancels in q_out, which is
  * therefore the same for every order of the sums.  Rows with a < 1e-30 give
- * q = 0 and scale = 0.  A row that holds a NaN or an infinity gets a scale
- * that is not finite (and unspecified q).
+ * q = 0 and scale = 0.  A row whose s or t holds a NaN or an infinity (its
+ * own, the residual's or the weights') gets a scale that is not finite (and
+ * unspecified q).
  * q_out : int8 [rows x d]; scale_out : fp32 [rows].  Other arguments and
  * errors as bllm_rmsnorm; q_out and scale_out overlap no other argument.
  */

@@ -18,12 +18,15 @@ def rmsnorm(x, w, eps, residual=None):
 
 def quant_rows_q8(t):
     """8-bit rows of t and their step a / 127, decided in fp32 as the kernel
-    decides: q = rne(t * (127 * (1 / a))) with each operation rounded to fp32."""
+    decides: q = rne(t * (127 * (1 / a))) with each operation rounded to fp32.
+    The step of a row that holds a NaN or an infinity is not finite (and q unspecified)."""
     t = np.asarray(t, dtype=np.float32)
     a = np.max(np.abs(t), axis=1)
-    inv = np.where(a >= np.float32(1e-30), np.float32(127.0) * (np.float32(1.0) / np.maximum(a, np.float32(1e-30))), np.float32(0.0))
+    small = a < np.float32(1e-30)  # a NaN is not
+    inv = np.where(small, np.float32(0.0), np.float32(127.0) * (np.float32(1.0) / np.maximum(a, np.float32(1e-30))))
     q = np.rint(t * inv.astype(np.float32)[:, None])
-    return np.clip(q, -127, 127).astype(np.int8), np.where(a >= np.float32(1e-30), a, 0.0).astype(np.float64) / 127.0
+    return (np.clip(np.where(np.isnan(q), 0.0, q), -127, 127).astype(np.int8),
+            np.where(small, 0.0, a).astype(np.float64) / 127.0)
 
 
 def rmsnorm_q8(x, w, eps, residual=None):

@@ -1,0 +1,95 @@
+"""The mixer block's operators at their ends: rows without one finite value, sizes past one launch's
+limits, and the bits that the states keep."""
+import numpy as np
+import pytest
+
+import oracle
+from synthdata import bf16_round
+from tests.helpers import to_dev, to_np, say
+
+
+@pytest.fixture(scope="module")
+def B():
+    import byte_level_lm_amd as B
+    B.lib()
+    return B
+
+
+# ---------------------------------------------------------------- 8-bit rows that hold a NaN or an infinity
+
+def _lost_rows(d):
+    """(x, w, lost): rows of d values, which of them have no finite 8-bit form.  w is NaN nowhere; its last entry is 0."""
+    rng = np.random.default_rng(d)
+    x = rng.standard_normal((10, d)).astype(np.float32)
+    w = np.ones(d, np.float32)
+    w[-1] = 0.0
+    x[1] = np.nan                       # nothing but NaN
+    x[2] = 0.0; x[2, 3] = np.nan        # NaN and zeros
+    x[3] = -np.inf
+    x[4, d // 2] = np.nan
+    x[5] = 0.0; x[5, 1] = np.inf
+    x[6, -1] = np.inf                   # under a weight of 0
+    x[7] = 1e-35; x[7, 0] = np.nan      # beside values that alone would become zeros
+    x[8] = 0.0
+    lost = np.array([False] + [True] * 7 + [False] * 2)
+    return x, w, lost
+
+
+@pytest.mark.parametrize("d", [8, 64])
+def test_oracle_rows_that_are_not_finite_have_no_finite_scale(d):
+    x, w, lost = _lost_rows(d)
+    with np.errstate(all="ignore"):
+        _, plain = oracle.quant_rows_q8(x)
+        _, scale, _ = oracle.rmsnorm_q8(x, w, 1e-6)
+        _, by_weight, _ = oracle.rmsnorm_q8(np.ones((2, d)), np.where(np.arange(d) == 2, np.nan, 1.0), 1e-6)
+    assert np.array_equal(~np.isfinite(plain), lost) and np.array_equal(~np.isfinite(scale), lost)
+    assert plain[8] == 0 and scale[8] == 0
+    assert not np.isfinite(by_weight).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [8, 64, 256, 512, 1024, 2048, 4096, 16384, 40000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_are_not_finite_have_no_finite_scale(B, d, dtype):
+    """Each width has its split of a row over threads, the last its second pass over memory."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    say("rows not finite", d, dtype)
+    x, w, lost = _lost_rows(d)
+    x = bf16_round(x)
+    dx, dw = to_dev(x, dt), to_dev(w, dt)
+    q, scale = B.quant_rows_q8(dx)
+    assert np.array_equal(~np.isfinite(to_np(scale)), lost)
+    q_o, step = oracle.quant_rows_q8(x[~lost])
+    assert np.array_equal(to_np(q)[~lost], q_o) and np.array_equal(to_np(scale)[~lost] == 0, step == 0)
+    q, scale, _ = B.rmsnorm_q8(dx, dw)
+    assert np.array_equal(~np.isfinite(to_np(scale)), lost)
+    q_o, _, _ = oracle.rmsnorm_q8(x[~lost], w, 1e-6)
+    assert np.array_equal(to_np(q)[~lost], q_o)
+    # split between x and the residual, many rows (another split of the row)
+    half = torch.zeros_like(dx)
+    half[:, ::2] = dx[:, ::2]
+    _, scale, _ = B.rmsnorm_q8(half.repeat(500, 1), dw, residual=(dx - half).nan_to_num(0.0, 0.0, 0.0).repeat(500, 1))
+    even = ~np.isfinite(x[:, ::2]).all(1)
+    assert np.array_equal(~np.isfinite(to_np(scale)).reshape(500, 10), np.tile(even, (500, 1)))
+    # a weight alone
+    for bad in (np.nan, np.inf):
+        w2 = np.ones(d, np.float32)
+        w2[d // 2 + 1] = bad
+        _, scale, _ = B.rmsnorm_q8(torch.ones(3, d, dtype=dt, device="cuda"), to_dev(w2, dt))
+        assert not np.isfinite(to_np(scale)).any()
+
+
+@pytest.mark.gpu
+def test_nan_reaches_the_rows_behind_a_block(B):
+    """A row lost in one product stays lost through the next norm and product."""
+    import torch
+    rng = np.random.default_rng(2)
+    d = 128
+    w8, ws = B.quant_rows_q8(to_dev(rng.standard_normal((d, d)).astype(np.float32)))
+    x = torch.randn(5, d, device="cuda").to(torch.bfloat16)
+    x[3] = float("nan")
+    for _ in range(3):
+        q, s, _ = B.rmsnorm_q8(x, torch.ones(d, device="cuda", dtype=torch.bfloat16))
+        x = B.linear_i8(q, s, w8, ws)
+    assert torch.isnan(x[3]).all() and torch.isfinite(x[[0, 1, 2, 4]]).all()
