@@ -234,12 +234,31 @@ __global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
 }
 
 constexpr int64_t kFewRows = 4096;
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1;  // of one launch, along x
+
+// a call's rows in slices of `most` of them, as many as one launch has threads for
+template <int DT, typename Launch>
+void in_slices(NormArgs a, int64_t most, const Launch& launch) {
+  for (int64_t left = a.rows; left > 0; left -= a.rows) {
+    a.rows = left < most ? left : most;
+    launch(a);
+    const int64_t n = a.rows * a.d, bytes = n * elem_size(DT);
+    a.x = static_cast<const char*>(a.x) + bytes;
+    if (a.res) a.res = static_cast<const char*>(a.res) + bytes;
+    if (a.res_out) a.res_out = static_cast<char*>(a.res_out) + bytes;
+    if (a.y) a.y = static_cast<char*>(a.y) + bytes;
+    if (a.q) a.q += n;
+    if (a.scale) a.scale += a.rows;
+  }
+}
 
 template <int DT, bool RES, bool Q8, int G, int P>
 void rows_launch(const NormArgs& a, hipStream_t st) {
-  constexpr int NT = G > 256 ? G : 256;
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, NT / G)));
-  hipLaunchKernelGGL((norm_rows<DT, RES, Q8, G, P>), grid, dim3(NT), 0, st, a);
+  constexpr int NT = G > 256 ? G : 256, R = NT / G;  // rows of a workgroup
+  in_slices<DT>(a, kMaxThreads / NT * R, [st](const NormArgs& a) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.rows, R)));
+    hipLaunchKernelGGL((norm_rows<DT, RES, Q8, G, P>), grid, dim3(NT), 0, st, a);
+  });
 }
 
 // The smallest group whose lanes hold the row in four pieces or fewer: more rows
@@ -265,7 +284,9 @@ void norm_launch_as(const NormArgs& a, hipStream_t st) {
   else if (pieces <= 4096)
     rows_launch<DT, RES, Q8, 1024, 4>(a, st);
   else
-    hipLaunchKernelGGL((norm_long<DT, RES, Q8>), dim3(static_cast<unsigned>(a.rows)), dim3(1024), 0, st, a);
+    in_slices<DT>(a, kMaxThreads / 1024, [st](const NormArgs& a) {
+      hipLaunchKernelGGL((norm_long<DT, RES, Q8>), dim3(static_cast<unsigned>(a.rows)), dim3(1024), 0, st, a);
+    });
 }
 
 template <int DT>

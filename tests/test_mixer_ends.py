@@ -93,3 +93,55 @@ def test_nan_reaches_the_rows_behind_a_block(B):
         q, s, _ = B.rmsnorm_q8(x, torch.ones(d, device="cuda", dtype=torch.bfloat16))
         x = B.linear_i8(q, s, w8, ws)
     assert torch.isnan(x[3]).all() and torch.isfinite(x[[0, 1, 2, 4]]).all()
+
+
+# ---------------------------------------------------------------- more rows than one launch has threads for
+
+def _room(gigabytes):
+    import torch
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gigabytes * 1e9:
+        pytest.skip(f"needs {gigabytes} GB of free GPU memory")
+
+
+@pytest.mark.gpu
+def test_rows_past_the_threads_of_a_launch(B):
+    """2^28 rows of part of a wave each: every row right, the last ones among them."""
+    import torch
+    rows, d = (1 << 28) + 21, 8
+    say("rows", rows, d)
+    _room(16)
+    top = (torch.arange(rows, device="cuda", dtype=torch.int32) % 119 + 9).to(torch.bfloat16)
+    x = top[:, None].repeat(1, d)
+    x[:, 3] = 0.0
+    q, scale = B.quant_rows_q8(x)
+    want = torch.full((d,), 127, dtype=torch.int8, device="cuda")
+    want[3] = 0
+    assert all(bool((part == want).all()) for part in q.split(1 << 26))
+    # the scale as the type of one row gives it, for each of its 119 values
+    few, s_few = B.quant_rows_q8(x[:119].contiguous())
+    at = torch.arange(rows, device="cuda", dtype=torch.int32) % 119
+    assert all(bool((a == s_few[b.long()]).all()) for a, b in zip(scale.split(1 << 26), at.split(1 << 26)))
+    np.testing.assert_allclose(to_np(s_few), to_np(top[:119]) / 127.0, rtol=2.0 ** -23)
+
+
+@pytest.mark.gpu
+def test_wide_rows_past_the_threads_of_a_launch(B):
+    """2^22 rows of a workgroup of 1024 each, in place."""
+    import torch
+    rows, d = (1 << 22) + 3, 8200
+    say("rows", rows, d)
+    dt = torch.bfloat16
+    _room(rows * d * 2 / 1e9 + 8)
+    rng = np.random.default_rng(d)
+    some = bf16_round(rng.standard_normal((6, d)).astype(np.float32))
+    at = [0, 1, (1 << 22) - 2, (1 << 22) - 1, rows - 2, rows - 1]
+    w = torch.ones(d, dtype=dt, device="cuda")
+    y_o, _ = B.rmsnorm(to_dev(some, dt), w)
+    x = torch.zeros(rows, d, dtype=dt, device="cuda")
+    for i, r in enumerate(at):
+        x[r] = to_dev(some[i], dt)
+    y, _ = B.rmsnorm(x, w, y_out=x)
+    for i, r in enumerate(at):
+        assert torch.equal(y[r], y_o[i])
+    assert not y[2:2000].any() and not y[(1 << 22) - 2000:(1 << 22) - 2].any()
