@@ -123,7 +123,9 @@ __global__ __launch_bounds__(512) void linear_few(LinArgs a) {
   __shared__ intx4 sAcc[NW / 2][2 * MT][64];
   const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 16 * MT, col0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
+  const int64_t col0 = (static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x) * 32;
+  if (col0 >= a.n) return;
   const int8_t *pw[2], *px[MT];
 #pragma unroll
   for (int j = 0; j < 2; ++j) pw[j] = a.wq + min(col0 + chan(j, n), a.n - 1) * a.k + 16 * gq;
@@ -418,7 +420,10 @@ __global__ __launch_bounds__(128 * WN, 2) void linear_tiles(LinArgs a, int mt, i
 
 template <int MT>
 void few_launch(const LinArgs& a, int dtype, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(a.n, 32)), static_cast<unsigned>(ceil_div(a.m, 16 * MT)));
+  // one launch has fewer than 2^32 threads along x: beyond, the channels go on along z
+  const int64_t cols = ceil_div(a.n, 32), x = std::min(cols, int64_t(1) << 22);
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(ceil_div(a.m, 16 * MT)),
+                  static_cast<unsigned>(ceil_div(cols, x)));
   if (dtype == BLLM_F32)
     hipLaunchKernelGGL((linear_few<BLLM_F32, MT>), grid, dim3(512), 0, st, a);
   else

@@ -145,3 +145,20 @@ def test_wide_rows_past_the_threads_of_a_launch(B):
     for i, r in enumerate(at):
         assert torch.equal(y[r], y_o[i])
     assert not y[2:2000].any() and not y[(1 << 22) - 2000:(1 << 22) - 2].any()
+
+
+@pytest.mark.gpu
+def test_channels_past_the_threads_of_a_launch(B):
+    """2^28 output channels of a product of few tokens."""
+    import torch
+    m, n, k = 2, (1 << 28) + 41, 16
+    say("channels", m, n, k)
+    _room(24)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    wq = torch.randint(-128, 128, (n, k), dtype=torch.int8, device="cuda", generator=gen)
+    xq = torch.randint(-128, 128, (m, k), dtype=torch.int8, device="cuda", generator=gen)
+    sx = torch.tensor([1.0, 0.5], device="cuda")
+    y = B.linear_i8(xq, sx, wq, torch.ones(n, device="cuda"), out_dtype=torch.float32)
+    for a in range(0, n, 1 << 24):  # sums below 2^24: exact in fp32
+        b = min(a + (1 << 24), n)
+        assert torch.equal(y[:, a:b], (xq.float() @ wq[a:b].float().t()) * sx[:, None])
