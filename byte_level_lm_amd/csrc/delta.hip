@@ -737,7 +737,7 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
   const int lane = threadIdx.x & 63, n = lane & 15, gq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave % G, tid = 64 * w + lane;
   // the column parts of a head follow each other on one XCD, whose L2 then holds its K, Q, T and P once
-  const int id = blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
+  const int id = blockIdx.y * gridDim.x + blockIdx.x, part = id / 8 % cols, head = id / (8 * cols) * 8 + id % 8;
   if (head >= a.nseq * a.hv) return;
   const int s = head / a.hv, h = head % a.hv, kh = h / (a.hv / a.hk);
   const int wcol = part * 16 * G, col = wcol + 16 * w + n;
@@ -1551,7 +1551,12 @@ void blocked_launch(const DeltaArgs& a, float* ws, hipStream_t st) {
   const int64_t heads = int64_t(a.nseq) * a.hv;
   const dim3 blocks(static_cast<unsigned>(ws_blocks(a.nseq, a.total)), static_cast<unsigned>(a.hv));
   hipLaunchKernelGGL(delta_prep<DKP>, blocks, dim3(256), 0, st, a, ws);
-  const auto grid = [](int64_t units, int64_t cols) { return dim3(static_cast<unsigned>(ceil_div(units, 8) * 8 * cols)); };
+  // Workgroups of all column parts, in eights.  One launch has fewer than 2^32 threads along x: past 2^22
+  // workgroups, which only delta_scan can have, they go on along y.
+  const auto grid = [](int64_t units, int64_t cols) {
+    const int64_t all = ceil_div(units, 8) * 8 * cols, x = std::min(all, int64_t(1) << 22);
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(ceil_div(all, x)));
+  };
   const int by16 = static_cast<int>(ceil_div(a.dv, 16)), by32 = (by16 + 1) / 2, by64 = (by16 + 3) / 4;
   const Plan plan = plan_of(a.nseq, a.total, a.hv, a.dk, a.dv);
   // The narrowest workgroups that still find a CU each: a block takes a workgroup 1.6 us with 16 columns, 2.3 with

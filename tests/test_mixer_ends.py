@@ -162,3 +162,34 @@ def test_channels_past_the_threads_of_a_launch(B):
     for a in range(0, n, 1 << 24):  # sums below 2^24: exact in fp32
         b = min(a + (1 << 24), n)
         assert torch.equal(y[:, a:b], (xq.float() @ wq[a:b].float().t()) * sx[:, None])
+
+
+@pytest.mark.gpu
+def test_heads_past_the_threads_of_a_launch(B):
+    """Short sequences whose heads and columns need more workgroups than one launch has along x: the last
+    sequences equal those computed alone, and the oracle's."""
+    import torch
+    nseq, tokens, hv, dk, dv = 8192, 7, 65, 8, 1024
+    say("heads", nseq, tokens, hv, dk, dv)
+    _room(60)
+    n, bf = nseq * tokens, torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k = (torch.randn(n, 1, dk, device="cuda", dtype=bf, generator=gen) for _ in range(2))
+    v = torch.randn(n, hv, dv, device="cuda", dtype=bf, generator=gen)
+    g = -0.2 * torch.rand(n, hv, device="cuda", generator=gen)
+    beta = torch.rand(n, hv, device="cuda", generator=gen)
+    off = torch.arange(nseq + 1, device="cuda") * tokens
+    o = torch.full((n, hv, dv), float("nan"), device="cuda", dtype=bf)
+    B.gated_delta(q, k, v, g, beta, off, want_state=False, o_out=o)
+    few = 128
+    for first in (0, nseq - few):
+        rows = slice(first * tokens, (first + few) * tokens)
+        alone, _ = B.gated_delta(q[rows], k[rows], v[rows], g[rows], beta[rows], off[:few + 1], want_state=False)
+        assert torch.equal(o[rows], alone)
+    assert all(bool(torch.isfinite(part).all()) for part in o.split(4096))
+    last = slice(n - tokens, n)
+    o_o, _ = oracle.gated_delta(*(to_np(t[last]) for t in (q, k, v, g, beta)), np.array([0, tokens]),
+                                scale=dk ** -0.5, unit_qk=True)
+    # one rounding to bf16 (within 2^-8 of an element) beside operands of 16 bits
+    err = np.linalg.norm(to_np(o[last]) - o_o, axis=2) / np.linalg.norm(o_o, axis=2)
+    assert err.max() <= 2.0 ** -8
