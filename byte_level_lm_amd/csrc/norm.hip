@@ -52,6 +52,14 @@ __device__ inline uint4 piece(const void* p, int64_t i) { return static_cast<con
 // |t| as the maximum takes it
 __device__ inline uint32_t magnitude(float t) { return __float_as_uint(t) & 0x7FFFFFFFu; }
 
+// 1 / sqrt(v), rounded once: the quotient of a rounded root is off by up to a unit in the last place, which
+// one step of Newton's iteration takes away (1 - v r^2 from exact products).  0 and infinity stay as they are.
+__device__ inline float inverse_root(float v) {
+  const float r = 1.0f / sqrtf(v), h = v * r;
+  const float e = fmaf(-h, r, 1.0f) - fmaf(v, r, -h) * r;
+  return fabsf(e) < 1.0f ? fmaf(0.5f * r, e, r) : r;
+}
+
 // the row's divisor and 8-bit scales from its sum of squares and the bits of its largest |t|
 struct RowScale {
   float r, inv, scale;
@@ -59,7 +67,7 @@ struct RowScale {
 __device__ inline RowScale row_scale(const NormArgs& a, float ss, uint32_t bits) {
   RowScale s;
   const float top = __uint_as_float(bits);
-  s.r = a.w ? 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps) : 1.0f;
+  s.r = a.w ? inverse_root(ss / static_cast<float>(a.d) + a.eps) : 1.0f;
   const bool some = !(top < kTiny);  // also where top is NaN, which then is the scale
   s.inv = some ? 127.0f * (1.0f / top) : 0.0f;
   s.scale = some ? top * s.r / 127.0f : 0.0f;

@@ -193,3 +193,37 @@ def test_heads_past_the_threads_of_a_launch(B):
     # one rounding to bf16 (within 2^-8 of an element) beside operands of 16 bits
     err = np.linalg.norm(to_np(o[last]) - o_o, axis=2) / np.linalg.norm(o_o, axis=2)
     assert err.max() <= 2.0 ** -8
+
+
+# ---------------------------------------------------------------- the norm's divisor
+
+@pytest.mark.gpu
+def test_the_norms_divisor_is_rounded_once(B):
+    """Rows whose mean square is exact in fp32, with a first value and weight of 1: y there is the divisor
+    itself, within half a unit in the last place (and 1 % of one for the correction's own arithmetic)."""
+    i, j = np.meshgrid(np.arange(128), np.arange(128))
+    x = np.zeros((128 * 128, 4), np.float32)
+    x[:, 0], x[:, 1], x[:, 2] = 1.0, i.ravel() / 64.0, j.ravel() / 64.0
+    y, _ = B.rmsnorm(to_dev(x), to_dev(np.ones(4, np.float32)), eps=0.0)
+    r = to_np(y)[:, 0]
+    want = 1.0 / np.sqrt(np.sum(x.astype(np.float64) ** 2, axis=1) / 4.0)
+    assert np.max(np.abs(r - want) / np.spacing(want.astype(np.float32))) <= 0.51
+
+
+@pytest.mark.gpu
+def test_the_norms_divisor_at_its_ends(B):
+    """Mean squares of zero, of subnormal numbers and past the largest number; eps alone."""
+    x = np.zeros((5, 4), np.float32)
+    x[1] = 1e-20
+    x[2] = 1e20       # its square is infinite: zeros
+    x[3] = 1e-22
+    x[4, 0] = 2.0
+    with np.errstate(all="ignore"):
+        y = to_np(B.rmsnorm(to_dev(x), to_dev(np.ones(4, np.float32)), eps=0.0)[0])
+    assert np.isnan(y[0]).all() and not y[2].any()
+    np.testing.assert_allclose(y[1], 1.0, rtol=1e-4)  # 1e-40 has 17 bits
+    np.testing.assert_allclose(y[4], [2.0, 0, 0, 0], rtol=2.0 ** -22)
+    assert np.isfinite(y[3]).all() or np.isinf(y[3]).all()
+    y = to_np(B.rmsnorm(to_dev(x), to_dev(np.ones(4, np.float32)), eps=1e-6)[0])
+    np.testing.assert_allclose(y[1], 1e-20 * 1e3, rtol=2.0 ** -20)
+    assert not y[0].any()
