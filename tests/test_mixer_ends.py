@@ -227,3 +227,70 @@ def test_the_norms_divisor_at_its_ends(B):
     y = to_np(B.rmsnorm(to_dev(x), to_dev(np.ones(4, np.float32)), eps=1e-6)[0])
     np.testing.assert_allclose(y[1], 1e-20 * 1e3, rtol=2.0 ** -20)
     assert not y[0].any()
+
+
+# ---------------------------------------------------------------- bits of the gated delta rule's state
+
+# Every value of a state takes at most twelve fp32 roundings in a block: of K S0 and its product with the decay
+# (3), the difference from V (1), U (3), its decay (2), the state's decay and sum (3).  Each is at most 2^-24 of its
+# size, and what former blocks left fades with the state itself.  An operand on the state's way with 16 bits instead
+# of 24 leaves 0.9e-6 to 1.5e-5 in these cases, whichever it is (K S0's S, the system's right side, its inverse, U).
+STATE_BITS_TOL = 12 * 2.0 ** -24
+
+BITS = [
+    # few heads: four waves to 16 columns
+    ([200, 130], 1, 2, 128, 64), ([300], 2, 2, 64, 64), ([250], 1, 1, 8, 16),
+    # 32 and 64 columns a workgroup
+    ([150, 200] * 8, 1, 8, 64, 64), ([129] * 8, 2, 8, 128, 128), ([100, 140] * 18, 2, 8, 64, 40), ([129] * 17, 2, 8, 128, 128),
+    # long sequences of few heads in segments
+    ([3000], 1, 2, 128, 128), ([1700], 1, 1, 64, 40), ([2600, 1900], 1, 1, 128, 32),
+    # token by token
+    ([5, 6, 4, 7], 2, 4, 128, 64),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("alike", [False, True])
+@pytest.mark.parametrize("lengths,hk,hv,dk,dv", BITS)
+def test_gated_delta_state_keeps_24_bits(B, lengths, hk, hv, dk, dv, alike):
+    """Keys of their own, and keys that share most of their direction, whose triangular system is far from one."""
+    rng = np.random.default_rng(sum(lengths) + dk + dv)
+    say("state bits", lengths[:4], hk, hv, dk, dv, alike)
+    off = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64)
+    n = int(off[-1])
+    q, k = rng.standard_normal((2, n, hk, dk))
+    if alike:
+        k = k + 2.0 * rng.standard_normal((hk, dk))
+    q, k = bf16_round(q.astype(np.float32)), bf16_round(k.astype(np.float32))
+    v = bf16_round(rng.standard_normal((n, hv, dv)).astype(np.float32))
+    g = (-0.05 * rng.random((n, hv)) ** 3).astype(np.float32)
+    beta = rng.random((n, hv)).astype(np.float32)
+    S0 = rng.standard_normal((len(lengths), hv, dk, dv)).astype(np.float32)
+    _, S_o = oracle.gated_delta(q, k, v, g, beta, off, scale=dk ** -0.5, unit_qk=True, state=S0)
+    import torch
+    bf = torch.bfloat16
+    _, S = B.gated_delta(to_dev(q, bf), to_dev(k, bf), to_dev(v, bf), to_dev(g), to_dev(beta), to_dev(off),
+                         state_in=to_dev(S0))
+    err = np.linalg.norm((to_np(S) - S_o).reshape(len(lengths) * hv, -1), axis=1)
+    err /= np.linalg.norm(S_o.reshape(len(lengths) * hv, -1), axis=1)
+    say("largest error", err.max())
+    assert err.max() <= STATE_BITS_TOL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lengths,hv,dk,dv", [([3000], 4, 128, 128), ([150, 0, 64] * 6, 8, 64, 64), ([90, 300] * 17, 8, 128, 128)])
+def test_gated_delta_repeats_itself(B, lengths, hv, dk, dv):
+    """The same call gives the same bits, beside other work and into memory that held something else."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    off = to_dev(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64))
+    n, bf = sum(lengths), torch.bfloat16
+    q, k, v = (torch.randn(n, hv, w, device="cuda", dtype=bf, generator=gen) for w in (dk, dk, dv))
+    g, beta = -0.1 * torch.rand(n, hv, device="cuda", generator=gen), torch.rand(n, hv, device="cuda", generator=gen)
+    o, S = B.gated_delta(q, k, v, g, beta, off)
+    ws = torch.empty(B.gated_delta_workspace(len(lengths), n, hv, dk, dv), dtype=torch.uint8, device="cuda")
+    for fill in (0, 0xFF, 0x3F):
+        ws.fill_(fill)
+        o2, S2 = torch.full_like(o, float("nan")), torch.full_like(S, float("nan"))
+        B.gated_delta(q, k, v, g, beta, off, o_out=o2, state_out=S2, ws=ws)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
