@@ -499,6 +499,8 @@ def gated_delta(q, k, v, g, beta, offsets, *, scale=None, unit_qk: bool = True, 
     be strided), g and beta fp32 [total, hv], offsets int64 [nseq + 1].  Returns (o [total, hv, dv],
     state fp32 [nseq, hv, dk, dv] or None); state_out may be state_in (updated in place).  scale
     defaults to dk ** -0.5; unit_qk scales every q and k row to unit length first."""
+    if state_out is not None and not want_state:
+        raise ValueError("state_out needs want_state")
     ptrs, dims, o_out = _delta_args(q, k, v, g, beta, o_out)
     hk, hv, dk, dv = dims[:4]
     if offsets.dtype != torch.int64 or offsets.dim() != 1 or offsets.numel() < 2:

@@ -294,3 +294,13 @@ def test_gated_delta_repeats_itself(B, lengths, hv, dk, dv):
         o2, S2 = torch.full_like(o, float("nan")), torch.full_like(S, float("nan"))
         B.gated_delta(q, k, v, g, beta, off, o_out=o2, state_out=S2, ws=ws)
         assert torch.equal(o, o2) and torch.equal(S, S2)
+
+
+# ---------------------------------------------------------------- the Python layer
+
+def test_a_state_out_that_is_not_wanted_is_refused():
+    import torch
+    import byte_level_lm_amd as B
+    x, off = torch.zeros(4, 1, 8), torch.tensor([0, 4])
+    with pytest.raises(ValueError, match="state_out needs want_state"):
+        B.gated_delta(x, x, x, x[:, :, 0], x[:, :, 0], off, want_state=False, state_out=torch.zeros(1, 1, 8, 8))
