@@ -34,9 +34,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# the raw handle of the current stream without building a Stream object; not a public name of torch
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream():
-    # the raw handle of torch.cuda.current_stream(), without building the Stream object
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ws(nbytes: int, ws, device):

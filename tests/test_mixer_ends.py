@@ -304,3 +304,29 @@ def test_a_state_out_that_is_not_wanted_is_refused():
     x, off = torch.zeros(4, 1, 8), torch.tensor([0, 4])
     with pytest.raises(ValueError, match="state_out needs want_state"):
         B.gated_delta(x, x, x, x[:, :, 0], x[:, :, 0], off, want_state=False, state_out=torch.zeros(1, 1, 8, 8))
+
+
+def test_the_current_stream_without_the_raw_call(monkeypatch):
+    """A torch that lacks the raw handle's call: the binding takes the public one."""
+    import importlib.util
+    import types
+    import torch
+    from byte_level_lm_amd import ops
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=1234))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    spec = importlib.util.spec_from_file_location("byte_level_lm_amd._ops_again", ops.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    assert again._stream() == 1234
+
+
+@pytest.mark.gpu
+def test_calls_go_to_the_current_stream(B):
+    import torch
+    from byte_level_lm_amd import ops
+    assert ops._stream() == torch.cuda.current_stream().cuda_stream
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        assert ops._stream() == side.cuda_stream != 0
+    assert ops._stream() == torch.cuda.current_stream().cuda_stream
