@@ -85,7 +85,7 @@ __device__ inline void row_words(const uint16_t* p, int left, uint32_t* w) {
 }
 
 // R = ceil(dk / 8) rounded up to 2, 4, 8 or 16 rows for each lane.  Many steps
-// are bound by the states' way in and out (8000 of 128 x 128: 1.05 GB in 186 us,
+// are bound by the states' way in and out (8000 of 128 x 128: 1.05 GB in 187 us,
 // 5.6 TB/s, more than a copy), one by latency (4 of them: 6.8 us).
 template <int R>
 __global__ __launch_bounds__(256) void delta_recurrent(DeltaArgs a) {
@@ -394,8 +394,8 @@ __device__ inline floatx4 column4(const float* t) {  // entries r kLd of a colum
 // fp32 MFMA, whose accumulators feed the second product as they are.  Gates
 // are summed in fp64, in units of ln 2, so that a difference of two sums is as
 // good as an fp32 gate however far the block has decayed.  Many blocks run at
-// the rate of a copy (128 heads of 128, 8192 tokens: 1.05 GB in 204 us), few are
-// bound by the chain of these steps (4 such heads: 512 blocks in 12.6 us).
+// the rate of a copy (128 heads of 128, 8192 tokens: 1.05 GB in 206 us), few are
+// bound by the chain of these steps (4 such heads: 512 blocks in 12.4 us).
 //
 // A decay e^(b_t - b_u) is a quotient that must not be formed from its terms
 // (both can underflow).  Between two tiles it is the product of three factors
@@ -1040,8 +1040,8 @@ __global__ __launch_bounds__(128 * G) void delta_scan(DeltaArgs a, const float* 
 
 // Brings a block's lines into L2, a quarter of a kilobyte of LDS taking what nobody reads:
 // the way from memory is about as long as a block takes, so the loads into LDS alone,
-// a block ahead, come late (16 ragged prompts of 8 heads of 64 x 64 at 16 columns a workgroup: 390
-// us without, 333 with).
+// a block ahead, come late (the scan of 16 ragged prompts of 8 heads of 64 x 64 at 16 columns a
+// workgroup: 360 us without, 334 with; delta_prep's 95 before it are apart).
 // NV lines of 64 columns of v; every wave of NW issues kLoads.
 template <int DKP, int NV, int NW>
 struct Ahead {
@@ -1513,6 +1513,8 @@ int64_t ws_blocks(int64_t nseq, int64_t total) { return total / kC + nseq; }
 
 // Prompts of at most kFew tokens on average go token by token, 1.7 us a token after the first (4 heads of
 // 128 x 128, 1 and 64 streams: 4 tokens 11.9 and 14.4 us against 17.4 and 25.8 in a block; 8 tokens 18.7 and 21.3).
+// The mean decides, as lengths lie on the device: one long sequence among many of a few tokens goes token by token
+// too, and plan_of counts short sequences as it counts long ones.
 constexpr int64_t kFew = 6;
 constexpr int64_t kCus = 256;
 

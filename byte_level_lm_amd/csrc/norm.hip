@@ -270,7 +270,7 @@ void rows_launch(const NormArgs& a, hipStream_t st) {
 }
 
 // The smallest group whose lanes hold the row in four pieces or fewer: more rows
-// a wave, more loads in flight (262144 x 512 in bf16 with the residual: 174 us).
+// a wave, more loads in flight (262144 x 512 in bf16 with the residual: 173 us).
 // A few rows only wait for their own chain, which a piece a lane makes shortest.
 template <int DT, bool RES, bool Q8>
 void norm_launch_as(const NormArgs& a, hipStream_t st) {

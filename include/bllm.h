@@ -456,11 +456,21 @@ int bllm_linear_i8(const int8_t* xq, const float* x_scale, const int8_t* wq, con
  *            v likewise with v_stride and dv: column slices of a wider
  *            projection output need no copy.  Strides are multiples of 8.
  * g, beta  : fp32 [total x hv].  g = -inf forgets the state.
- * offsets  : int64 [nseq+1] device; sequences of length 0 pass their state on.
+ * offsets  : int64 [nseq+1] device, ascending; sequences of length 0 pass
+ *            their state on; rows of o_out that no sequence has are left.
  * state_in : fp32 [nseq x hv x dk x dv] or NULL (zero); state_out : the same
  *            shape or NULL; may equal state_in (updated in place).
  * o_out    : bf16 [total x hv x dv], dense.
  * ws       : bllm_gated_delta_workspace(nseq, total, hv, dk, dv) bytes.
+ * Numbers  : states keep 24 bits on every way to the next state.  In blocks,
+ *            the products behind o take their fp32 operands (the state, u and
+ *            the weights within the block) with 16 bits, an error of about
+ *            2^-16 of |state| |q| beside o's own rounding to 8.
+ * Speed    : up to 6 tokens a sequence in the mean, total / nseq, a call goes
+ *            token by token (1.7 us a token of the longest), beyond that in
+ *            blocks of 64, in segments where the mean is long and heads are
+ *            few.  Long prompts and streams of a few tokens do best in calls
+ *            of their own.
  * Errors   : BLLM_E_INVAL for null pointers (q, k, v, g, beta and o_out may
  *            be NULL when total = 0), sizes below 1, hv not a multiple of hk,
  *            strides shorter than the heads, NaN scale; BLLM_E_NOTSUP for a
