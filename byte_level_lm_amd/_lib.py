@@ -13,7 +13,7 @@ LIB_PATH = os.environ.get("BLLM_LIB", os.path.join(_HERE, "libbllm.so"))
 
 OK, E_INVAL, E_NOTSUP, E_WS, E_HIP = 0, -1, -2, -3, -4
 S_CAPACITY, S_NONFINITE, S_INCOMPLETE = 1, 2, 4
-F32, BF16 = 0, 1
+F32, BF16, I8 = 0, 1, 2
 
 _p = C.c_void_p
 _i64 = C.c_int64
@@ -61,6 +61,16 @@ _SIGS = {
                                    _i64, C.c_double, C.c_int, _p, _p, _p, _p, C.c_size_t, _p]),
     "bllm_gated_delta_step": (C.c_int, [_p, _p, _p, _p, _p, C.c_int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
                                         C.c_double, C.c_int, _p, _p, _p, _i64, _p, _p]),
+    "bllm_kv_write": (C.c_int, [_p, _p, C.c_int, _p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, C.c_int, _i64,
+                                _i64, _p, _p, _p, _p, _p]),
+    "bllm_kv_read": (C.c_int, [_p, _p, _p, _p, C.c_int, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _i64, _p, C.c_int,
+                               _p, _p, _p]),
+    "bllm_attention_workspace": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64, _i64]),
+    "bllm_attention": (C.c_int, [_p, _p, _p, C.c_int, _p, _p, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64,
+                                 C.c_double, C.c_int, _i64, C.c_double, _p, _p, _p, _p, C.c_size_t, _p]),
+    "bllm_attention_step_workspace": (C.c_size_t, [_i64, _i64, _i64, _i64, _i64]),
+    "bllm_attention_step": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i64, _i64, _p, _p, _p, _p, C.c_int, _i64, _i64,
+                                      _p, _i64, _p, C.c_double, _i64, C.c_double, _p, _p, _p, _p, C.c_size_t, _p]),
 }
 EXPORTS = tuple(_SIGS)
 

@@ -1,0 +1,104 @@
+// What the calls around attention share: the pages of a cache of keys and
+// values, ragged batches, and which keys a query sees.
+#pragma once
+
+#include "common.h"
+
+namespace bllm {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions and distances then fit 32 bits
+constexpr int64_t kMaxHeads = 1024, kMaxSeqs = 65535, kMaxStride = int64_t(1) << 22;
+
+// the pages of a call: rows of d values, [npages x hkv x page]
+struct Pages {
+  const int32_t* table;  // [nseq x cols]
+  int cols, npages;
+  int shift;             // page == 1 << shift
+  int hkv, d;
+  // row of position p of stream s for head 0, or -1 where it has no page (head h: + h << shift)
+  __device__ inline int64_t row(int s, int64_t p) const {
+    const int64_t c = p >> shift;
+    if (p < 0 || c >= cols) return -1;
+    const int id = table[static_cast<int64_t>(s) * cols + c];
+    if (id < 0 || id >= npages) return -1;
+    return ((static_cast<int64_t>(id) * hkv) << shift) + (p & ((1 << shift) - 1));
+  }
+};
+
+__device__ inline int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// rows of sequence s, cut at the arrays' `total` rows
+__device__ inline void seq_rows(const int64_t* offsets, int s, int64_t total, int64_t* t0, int64_t* t1) {
+  *t0 = uniform64(min(max(offsets[s], int64_t(0)), total));
+  *t1 = uniform64(min(max(offsets[s + 1], *t0), total));
+}
+
+// Last s in [0, n) for which slot(s) <= t (slot ascending, slot(0) <= t), by a
+// whole wave: every lane asks about one of 64 places at once, one trip to
+// memory for up to 64 sequences, two for up to 4096.
+template <typename Slot>
+__device__ inline int wave_find(int n, int64_t t, const Slot& slot) {
+  int lo = 0, hi = n;
+  for (;;) {
+    const int step = (hi - lo + kWave - 1) / kWave, at = lo + lane_id() * step;
+    const bool before = at < hi && slot(min(at, n - 1)) <= t;
+    const int k = max(static_cast<int>(__popcll(__ballot(before))) - 1, 0);
+    lo += k * step;
+    if (step == 1) return lo;
+    hi = min(hi, lo + step);
+  }
+}
+
+// scores and visibility, as the entry points take them
+struct Mask {
+  float scale;
+  float cap;             // 0: none
+  const float* slopes;   // or null
+  const int32_t* prefix; // or null
+  int window;            // 0: none
+  int causal;
+};
+
+inline bool page_shift(int64_t page, int* shift) {
+  for (*shift = 4; *shift <= 8; ++*shift)
+    if (page == int64_t(1) << *shift) return true;
+  return false;
+}
+
+// arguments that the calls on pages share
+inline int pages_check(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                       int pages_dtype, int64_t npages, int64_t page, int64_t hkv, int64_t d, const int32_t* table,
+                       int64_t cols, int64_t nseq, Pages* p) {
+  const bool q8 = pages_dtype == BLLM_I8;
+  if (!k_pages || !v_pages || !table || npages < 1 || page < 1 || hkv < 1 || d < 1 || cols < 1 || nseq < 1 ||
+      q8 != (k_scale != nullptr) || q8 != (v_scale != nullptr))
+    return BLLM_E_INVAL;
+  if ((!q8 && pages_dtype != BLLM_BF16) || !page_shift(page, &p->shift) || d % (q8 ? 16 : 8) != 0 || d > 256 ||
+      hkv > kMaxHeads || nseq > kMaxSeqs || npages >= int64_t(1) << 31 || cols > kMaxTokens / page ||
+      !aligned16(k_pages) || !aligned16(v_pages) || (reinterpret_cast<uintptr_t>(k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(v_scale) & 3u))
+    return BLLM_E_NOTSUP;
+  p->table = table;
+  p->cols = static_cast<int>(cols);
+  p->npages = static_cast<int>(npages);
+  p->hkv = static_cast<int>(hkv);
+  p->d = static_cast<int>(d);
+  return BLLM_OK;
+}
+
+inline int mask_make(double scale, int causal, int64_t window, double cap, const float* slopes, const int32_t* prefix,
+                     Mask* m) {
+  if (scale != scale || window < 0 || !(cap >= 0.0 && cap <= 3.0e38)) return BLLM_E_INVAL;
+  // a window past every distance is none
+  *m = Mask{static_cast<float>(scale), static_cast<float>(cap), slopes, prefix,
+            static_cast<int>(window > kMaxTokens ? 0 : window), causal != 0};
+  return BLLM_OK;
+}
+
+inline bool stride_ok(int64_t stride) { return stride % 8 == 0 && stride < kMaxStride; }
+
+}  // namespace bllm

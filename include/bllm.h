@@ -10,6 +10,8 @@
  * and, for the encoder beside them, a mixer block in serving:
  *   bllm_rmsnorm_q8 -> bllm_linear_i8 -> bllm_gated_delta (or _step)
  *                  -> bllm_rmsnorm_q8 -> bllm_linear_i8
+ * whose mixer may also be attention, as the global model's is:
+ *   bllm_kv_write -> bllm_attention (or _step), bllm_kv_read to go on with a prompt
  *
  * Sources of the operations (page titles; sections as on the page):
  *   [BG]  "ByteGen: A Tokenizer-Free Generative Model for Orderbook Events in
@@ -72,6 +74,7 @@ extern "C" {
 /* dtypes */
 #define BLLM_F32 0
 #define BLLM_BF16 1
+#define BLLM_I8 2 /* pages of keys and values only: 8-bit codes with a scale for each row */
 
 int bllm_version(void);
 const char* bllm_status_string(int code);
@@ -505,6 +508,117 @@ int bllm_gated_delta_step(const void* q, const void* k, const void* v, const flo
                           int64_t q_stride, int64_t k_stride, int64_t v_stride, double scale, int unit_qk,
                           const float* state_in, float* state_out, const int32_t* slots, int64_t nslots,
                           void* o_out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Attention in serving: a cache of keys and values in pages, attention of
+ * packed prompts, and attention of one new token of each stream over its
+ * pages.  The local encoder of [BF4] attends within a window, its global model
+ * to every earlier chunk.
+ *
+ * Pages : k_pages and v_pages hold [npages x hkv x page] rows of d values.
+ *         pages_dtype BLLM_BF16: rows of bf16, no scales.  BLLM_I8: int8 rows,
+ *         row value = code * scale, with k_scale and v_scale fp32 [npages x hkv x page].
+ * table : int32 [nseq x cols] device: position p of stream s is row p % page of
+ *         page table[s * cols + p / page].  An entry outside [0, npages) is no
+ *         page: what lies there is not written, reads as zero and is not
+ *         attended to.  So are positions past cols * page.
+ * Limits of all four calls: bf16 rows of q, k, v and o; d a multiple of 8 (of 16
+ *         with 8-bit pages) up to 256; page 16, 32, 64, 128 or 256; cols * page,
+ *         total and total_k at most 2^30; hq, hkv at most 1024, nseq at most 65535;
+ *         token strides multiples of 8, below 2^22; npages below 2^31.
+ */
+
+/*
+ * bllm_kv_write -- rows of k and v into their pages: row i of sequence s goes to
+ * position start[s] + i.  With 8-bit pages a row is quantised as it is written,
+ * as bllm_quant_rows_q8 does: a = max |x|, code = rne(x * (127 * (1 / a))),
+ * scale = a / 127; a < 1e-30 gives zeros with scale 0, a row with a NaN or an
+ * infinity a scale that is not finite.
+ * k, v    : bf16, token t of head i at t * k_stride + i * d (v_stride alike).
+ * offsets : int64 [nseq+1] device, or NULL: one row of each stream, total = nseq.
+ *           Rows behind the last sequence are not written.
+ * start   : int32 [nseq] device or NULL (zero).  Positions below zero are not written.
+ * Two rows of one call at the same place are an error of the caller.
+ * Errors  : BLLM_E_INVAL for null pointers (k and v may be NULL when total = 0),
+ *           scales missing with 8-bit pages or given without, sizes below 1
+ *           (total below 0), strides shorter than the heads, total other than nseq
+ *           without offsets; BLLM_E_NOTSUP outside the limits above or off 16
+ *           bytes (scales off 4).
+ */
+int bllm_kv_write(const void* k, const void* v, int dtype, const int64_t* offsets, int64_t nseq, int64_t total,
+                  int64_t hkv, int64_t d, int64_t k_stride, int64_t v_stride, const int32_t* start,
+                  const int32_t* table, int64_t cols, int pages_dtype, int64_t npages, int64_t page,
+                  void* k_pages, void* v_pages, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * bllm_kv_read -- the positions start[s] .. of every sequence s back as packed
+ * rows: row offsets[s] + i of k_out and v_out is position start[s] + i.  8-bit
+ * rows come as code * scale rounded to bf16.
+ * offsets : int64 [nseq+1] device.  k_out, v_out : bf16 [total x hkv x d], dense;
+ *           rows behind the last sequence are left.
+ * Other arguments and errors as bllm_kv_write (k_out and v_out may be NULL when total = 0).
+ */
+int bllm_kv_read(const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                 int pages_dtype, int64_t npages, int64_t page, int64_t hkv, int64_t d, const int32_t* table,
+                 int64_t cols, const int64_t* offsets, int64_t nseq, int64_t total, const int32_t* start, int dtype,
+                 void* k_out, void* v_out, void* stream);
+
+/*
+ * bllm_attention -- softmax attention over a ragged batch.  Query i of a sequence
+ * with n queries and m keys stands at position t = i + m - n, key j at j:
+ *   s_ij = scale q_i . k_j;   cap > 0: s_ij = cap tanh(s_ij / cap);
+ *   slopes: s_ij -= slopes[h] |t - j|
+ *   o_i  = sum_j e^{s_ij} v_j / sum_j e^{s_ij} over the keys that i sees:
+ *          j < m, and j < prefix[s] or (j <= t if causal, and |t - j| < window if
+ *          window > 0)
+ * A query that sees no key gets zeros.  A key that a query does not see has no
+ * part in its output, whatever its rows hold (NaN and infinities too).
+ * Query head h uses key head h / (hq / hkv).
+ * q        : bf16, token t of head i at t * q_stride + i * d; k and v likewise.
+ * offsets  : int64 [nseq+1] device, ascending, of the queries; rows of o_out
+ *            that no sequence has are left.
+ * k_offsets: int64 [nseq+1] device, of the keys and values, or NULL: the
+ *            queries' (then total_k = total).
+ * prefix   : int32 [nseq] device or NULL;  slopes : fp32 [hq] device or NULL.
+ * o_out    : bf16 [total x hq x d], dense.
+ * ws       : bllm_attention_workspace(nseq, total, total_k, hq, hkv, d) bytes.
+ * Numbers  : products of bf16 values, sums, maxima and the softmax's sum in
+ *            fp32.  The weights are rounded to bf16 (8 bits) for the product with v, and
+ *            their sum is taken of the rounded ones: o is off by about 2^-9 of
+ *            the typical |v| from that, beside its own rounding to bf16.
+ * Errors   : BLLM_E_INVAL for null pointers (q, k, v and o_out may be NULL when
+ *            their rows are none), sizes below 1 (totals below 0), hq not a
+ *            multiple of hkv, strides shorter than the heads, NaN scale, window
+ *            below 0, cap below 0 or not finite, total_k other than total without
+ *            k_offsets; BLLM_E_NOTSUP outside the limits above or off 16
+ *            bytes; BLLM_E_WS.
+ */
+size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t total_k, int64_t hq, int64_t hkv, int64_t d);
+int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,
+                   const int64_t* k_offsets, int64_t nseq, int64_t total, int64_t total_k, int64_t hq, int64_t hkv,
+                   int64_t d, int64_t q_stride, int64_t k_stride, int64_t v_stride, double scale, int causal,
+                   int64_t window, double cap, const float* slopes, const int32_t* prefix, void* o_out, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
+ * bllm_attention_step -- attention of one new token of each of nseq streams
+ * over its pages: the formulas of bllm_attention with one query at the last of
+ * lengths[s] positions (the new token's own row is written first, by
+ * bllm_kv_write).
+ * lengths : int32 [nseq] device, cut at [0, cols * page]; 0 gives zeros.
+ * o_out   : bf16 [nseq x hq x d], dense.
+ * ws      : bllm_attention_step_workspace(nseq, hq, hkv, d, cols * page) bytes.
+ * Numbers : as bllm_attention, with the weights (times v's scales) in two bf16
+ *           terms, 16 bits.
+ * Other arguments and errors as bllm_attention and bllm_kv_write.
+ */
+size_t bllm_attention_step_workspace(int64_t nseq, int64_t hq, int64_t hkv, int64_t d, int64_t positions);
+int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64_t hq, int64_t hkv, int64_t d,
+                        int64_t q_stride, const void* k_pages, const void* v_pages, const float* k_scale,
+                        const float* v_scale, int pages_dtype, int64_t npages, int64_t page, const int32_t* table,
+                        int64_t cols, const int32_t* lengths, double scale, int64_t window, double cap,
+                        const float* slopes, const int32_t* prefix, void* o_out, void* ws, size_t ws_bytes,
+                        void* stream);
 
 #ifdef __cplusplus
 }

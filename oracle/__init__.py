@@ -38,3 +38,4 @@ from .byteflow import (  # noqa: F401
     alpha_of, coding_rate, coding_rate_at, coding_rate_stream, topk_select, topk_select_window, topk_mask, gather, chunk_bins, upsample_bins,
 )
 from .mixer import rmsnorm, rmsnorm_q8, quant_rows_q8, linear_i8, gated_delta  # noqa: F401
+from .attention import kv_write, kv_read, attention, attention_step  # noqa: F401
