@@ -53,6 +53,44 @@ __device__ inline int wave_find(int n, int64_t t, const Slot& slot) {
   }
 }
 
+// ---------------------------------------------------------------- matrix instructions and lanes
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+
+__device__ inline bf16x8 as_frag(uint4 v) { return __builtin_bit_cast(bf16x8, v); }
+// two values to bf16, rounded to nearest even, the first in the lower half
+__device__ inline uint32_t pack2(float a, float b) {
+  bf16x2 v;
+  v[0] = static_cast<__bf16>(a);
+  v[1] = static_cast<__bf16>(b);
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ inline float low_half(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ inline float high_half(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+// maximum and sum with the lane 32 away, and with the lane 16 away
+__device__ inline float max_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float max_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ inline float sum_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ inline float sum_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32: 1 ulp, tiny results are zero
+
 // scores and visibility, as the entry points take them
 struct Mask {
   float scale;
@@ -62,6 +100,11 @@ struct Mask {
   int window;            // 0: none
   int causal;
 };
+
+// cap * tanh(x / cap) as cap - 2 cap / (e^{2 x / cap} + 1): off by about 2^-22 cap
+__device__ inline float capped(float x, float cap, float two_over_cap_log2e) {
+  return cap - 2.0f * cap * __builtin_amdgcn_rcpf(exp2_fast(x * two_over_cap_log2e) + 1.0f);
+}
 
 inline bool page_shift(int64_t page, int* shift) {
   for (*shift = 4; *shift <= 8; ++*shift)
@@ -97,6 +140,11 @@ inline int mask_make(double scale, int causal, int64_t window, double cap, const
   *m = Mask{static_cast<float>(scale), static_cast<float>(cap), slopes, prefix,
             static_cast<int>(window > kMaxTokens ? 0 : window), causal != 0};
   return BLLM_OK;
+}
+
+inline int heads_check(int64_t hq, int64_t hkv, int64_t d) {
+  if (hq < 1 || hkv < 1 || d < 1 || hq % hkv != 0) return BLLM_E_INVAL;
+  return hq > kMaxHeads || d % 8 != 0 || d > 256 ? BLLM_E_NOTSUP : BLLM_OK;
 }
 
 inline bool stride_ok(int64_t stride) { return stride % 8 == 0 && stride < kMaxStride; }

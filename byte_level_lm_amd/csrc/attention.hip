@@ -112,11 +112,6 @@ __global__ __launch_bounds__(64 * kWaves) void attend(AttArgs a) {
   }
 }
 
-int heads_check(int64_t hq, int64_t hkv, int64_t d) {
-  if (hq < 1 || hkv < 1 || d < 1 || hq % hkv != 0) return BLLM_E_INVAL;
-  return hq > kMaxHeads || d % 8 != 0 || d > 256 ? BLLM_E_NOTSUP : BLLM_OK;
-}
-
 unsigned grid_of(int64_t work) {
   const int64_t n = ceil_div(work, kWaves);
   return static_cast<unsigned>(n < (1 << 20) ? n : 1 << 20);
@@ -166,48 +161,5 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.d = static_cast<int>(d);
   hipLaunchKernelGGL((attend<false, false>), dim3(grid_of(total * hq)), dim3(64 * kWaves), 0,
                      static_cast<hipStream_t>(stream), a);
-  return launch_status();
-}
-
-extern "C" size_t bllm_attention_step_workspace(int64_t nseq, int64_t hq, int64_t hkv, int64_t d, int64_t positions) {
-  return nseq < 1 || hq < 1 || hkv < 1 || d < 1 || positions < 1 ? 0 : 16;
-}
-
-extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64_t hq, int64_t hkv, int64_t d,
-                                   int64_t q_stride, const void* k_pages, const void* v_pages, const float* k_scale,
-                                   const float* v_scale, int pages_dtype, int64_t npages, int64_t page,
-                                   const int32_t* table, int64_t cols, const int32_t* lengths, double scale,
-                                   int64_t window, double cap, const float* slopes, const int32_t* prefix, void* o_out,
-                                   void* ws, size_t ws_bytes, void* stream) {
-  AttArgs a{};
-  const int rc = heads_check(hq, hkv, d);
-  if (rc == BLLM_E_INVAL || !q || !lengths || !o_out || q_stride < hq * d ||
-      mask_make(scale, 1, window, cap, slopes, prefix, &a.mask) != BLLM_OK)
-    return BLLM_E_INVAL;
-  const int pc = pages_check(k_pages, v_pages, k_scale, v_scale, pages_dtype, npages, page, hkv, d, table, cols, nseq,
-                             &a.pages);
-  if (pc != BLLM_OK) return pc;
-  if (rc != BLLM_OK || dtype != BLLM_BF16 || !stride_ok(q_stride) || !aligned16(q) || !aligned16(o_out))
-    return BLLM_E_NOTSUP;
-  if (!ws || ws_bytes < bllm_attention_step_workspace(nseq, hq, hkv, d, cols * page)) return BLLM_E_WS;
-  a.q = static_cast<const uint16_t*>(q);
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.lengths = lengths;
-  a.o = static_cast<uint16_t*>(o_out);
-  a.total = nseq;
-  a.q_stride = q_stride;
-  a.nseq = static_cast<int>(nseq);
-  a.hq = static_cast<int>(hq);
-  a.hkv = static_cast<int>(hkv);
-  a.d = static_cast<int>(d);
-  const dim3 grid(grid_of(nseq * hq)), block(64 * kWaves);
-  hipStream_t st = static_cast<hipStream_t>(stream);
-  if (pages_dtype == BLLM_I8)
-    hipLaunchKernelGGL((attend<true, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((attend<true, false>), grid, block, 0, st, a);
   return launch_status();
 }
