@@ -21,8 +21,8 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
-constexpr int kRows = 128;       // queries of a workgroup
-constexpr int kWaves = 4;
+constexpr int kWaves = 4, kRows = 32 * kWaves;  // queries of a workgroup
+constexpr int BN = 32;           // keys of a tile
 constexpr int kXcds = 8;
 constexpr int kRun = 64;         // neighbouring workgroups that one XCD takes in a row
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset past every buffer: reads as zero
@@ -33,7 +33,7 @@ struct AttArgs {
   const int64_t *offsets, *k_offsets;
   uint16_t* o;
   int64_t total, total_k, q_stride, k_stride, v_stride;
-  int64_t first, units, slots;   // this launch's first unit of work, all of them, 128-query slots
+  int64_t first, units, slots;   // this launch's first unit of work, all of them, slots of a workgroup's queries
   int nseq, hq, hkv, group, d;
   Mask mask;
 };
@@ -55,11 +55,21 @@ __device__ inline uint2 read_tr(const uint16_t* p) {
   return __builtin_bit_cast(uint2, v);
 }
 
-// 16-byte piece p of row r of a tile lies at piece p ^ exchange(r): sixteen rows' pieces p lie in all the banks
-// (K's reads), and so do four neighbouring rows' four pieces 4 i .. 4 i + 3 (V's transposing reads)
+// Where a tile's 16-byte pieces lie in LDS, so that the sixteen rows of K's
+// reads lie in all the banks, and so do the four rows and pieces of V's
+// transposing reads.  A load brings a chunk of 1 KB: with D = 128 piece p of a row r
+// is exchanged with p ^ 4 (r % 4) and chunks (of four rows) are a piece
+// apart, which leaves few address registers; else with p ^ exchange(r).
+template <int D>
+constexpr int kChunk = D == 128 ? 520 : 512;  // values from chunk to chunk
 template <int D>
 __device__ inline int exchange(int r) {
-  return D == 64 ? 4 * (r >> 1 & 1) | (r >> 2 & 3) : 4 * (r & 3) | (r >> 2 & 3);
+  return D == 64 ? 4 * (r >> 1 & 1) | (r >> 2 & 3) : D == 128 ? 4 * (r & 3) : 4 * (r & 3) | (r >> 2 & 3);
+}
+
+// sum plus both values of a pair
+__device__ inline float dot2_ones(uint32_t pair, float sum) {
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), __builtin_bit_cast(bf16x2, 0x3F803F80u), sum, false);
 }
 
 // What one query sees: keys lo .. hi and those below front.
@@ -72,6 +82,33 @@ __device__ inline Sight sight(const Mask& m, int t, int keys, int front) {
   s.lo = m.window ? t - m.window + 1 : 0;
   s.hi = min(m.causal ? t : m.window ? t + m.window - 1 : keys - 1, keys - 1);
   s.front = front;
+  return s;
+}
+
+__device__ inline int64_t lane_value(int64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(v), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(v >> 32), lane);
+  return static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// The sequence that has the slot, and its rows of queries and keys.  Up to 63
+// sequences take one trip to memory: their offsets are in the wave's lanes.
+__device__ inline int find_rows(const AttArgs& a, int64_t slot, int64_t* t0, int64_t* t1, int64_t* k0, int64_t* k1) {
+  const auto cut = [](int64_t v, int64_t most) { return min(max(v, int64_t(0)), most); };
+  if (a.nseq < kWave) {
+    const int i = min(lane_id(), a.nseq);
+    const int64_t off = cut(a.offsets[i], a.total), k_off = cut(a.k_offsets[i], a.total_k);
+    const uint64_t before = __ballot(lane_id() < a.nseq && off / kRows + i <= slot);
+    const int s = max(static_cast<int>(__popcll(before)) - 1, 0);
+    *t0 = lane_value(off, s);
+    *t1 = max(lane_value(off, s + 1), *t0);
+    *k0 = lane_value(k_off, s);
+    *k1 = max(lane_value(k_off, s + 1), *k0);
+    return s;
+  }
+  const int s = uniform(wave_find(a.nseq, slot, [&](int i) { return cut(a.offsets[i], a.total) / kRows + i; }));
+  seq_rows(a.offsets, s, a.total, t0, t1);
+  seq_rows(a.k_offsets, s, a.total_k, k0, k1);
   return s;
 }
 
@@ -117,14 +154,15 @@ __device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t
 }
 
 // GEN: with a cap or slopes
-template <int D, int BN, bool GEN>
-__global__ __launch_bounds__(64 * kWaves, 2) void prompt_tiles(AttArgs a) {
+template <int D, bool GEN>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void prompt_tiles(AttArgs a) {
   constexpr int NS = D / 16;               // steps of the first product
   constexpr int NB = D / 32;               // 32-column blocks of the second
-  constexpr int NK = BN / 32;              // 32-key blocks of a tile
   constexpr int RPI = 512 / D;             // rows of a 1 KB load
   constexpr int U = BN / RPI / kWaves;     // loads a wave makes for K, and for V
-  __shared__ __align__(1024) uint16_t sK[2][BN * D], sV[2][BN * D];
+  // four arrays: a fragment's read then waits for no load that fills another one
+  constexpr int kTile = BN / RPI * kChunk<D>;
+  __shared__ __align__(16) uint16_t sK0[kTile], sK1[kTile], sV0[kTile], sV1[kTile];
   const int lane = threadIdx.x & 63, qi = lane & 31, half = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -142,45 +180,44 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_tiles(AttArgs a) {
   const int kh = static_cast<int>(unit / per);
   const int64_t slot = unit % per / a.group;
   const int h = kh * a.group + static_cast<int>(unit % a.group);
-  const int s = wave_find(a.nseq, slot, [&](int i) { return min(max(a.offsets[i], int64_t(0)), a.total) / kRows + i; });
   int64_t t0, t1, k0, k1;
-  seq_rows(a.offsets, s, a.total, &t0, &t1);
-  seq_rows(a.k_offsets, s, a.total_k, &k0, &k1);
+  const int s = find_rows(a, slot, &t0, &t1, &k0, &k1);
   const int n = static_cast<int>(t1 - t0), keys = static_cast<int>(k1 - k0);
   const int back = static_cast<int>(slot - (t0 / kRows + s)), blocks = (n + kRows - 1) / kRows;
   if (back < 0 || back >= blocks) return;
   const int first = (blocks - 1 - back) * kRows;
   const int shift = keys - n;                            // position of query 0
-  const int front = a.mask.prefix ? min(max(a.mask.prefix[s], 0), keys) : 0;
+  const int front = a.mask.prefix ? uniform(min(max(a.mask.prefix[s], 0), keys)) : 0;
 
-  // the tiles that some query of the workgroup sees: [0, b) then [e, f)
+  // the keys that some query of the workgroup sees, in tiles: from 0 to `ahead`, then from `from` to `to`
   const Sight low = sight(a.mask, first + shift, keys, front), high = sight(a.mask, min(first + kRows, n) - 1 + shift, keys, front);
-  int from = max(low.lo, 0), to = high.hi + 1, ahead = front;
-  if (ahead >= from) {
-    from = 0;
-    to = max(to, ahead);
-    ahead = 0;
-  }
-  const int tb = (ahead + BN - 1) / BN, te = max(from / BN, tb), tiles = tb + max((to + BN - 1) / BN - te, 0);
-  const auto key_of = [&](int i) { return (i < tb ? i : i - tb + te) * BN; };
+  int from = max(low.lo, 0) / BN * BN, ahead = (front + BN - 1) / BN * BN;
+  const int to = max(high.hi + 1, front);
+  if (ahead >= from) from = ahead;
+  from = uniform(from);
+  const int tiles = max((ahead + to - from + BN - 1) / BN, ahead / BN);
+  const auto after = [&](int j) { return j + BN == ahead ? from : j + BN; };
   // the wave's own queries
   const int i0 = first + 32 * w, p0 = i0 + shift, p1 = min(i0 + 32, n) - 1 + shift;
   const bool some = i0 < n;
   const Sight w0 = sight(a.mask, p0, keys, front), w1 = sight(a.mask, p1, keys, front);
-  const int t = p0 + qi;
-  const Sight see = sight(a.mask, t, keys, front);
+  // tiles that every query of the wave sees whole (at least these), and tiles of which some query sees a key
+  const int whole0 = uniform(w1.lo <= front ? 0 : w1.lo), whole1 = uniform(max(w0.hi + 1, w1.lo <= front ? front : 0) - BN);
+  const int seen0 = uniform(some ? front : 0), seen1 = uniform(w0.lo - BN + 1), seen2 = uniform(some ? w1.hi : -1);
 
   // queries: 8 values of each 16, negated for a negative scale, so that the largest product has the largest score
-  uint4 fq[NS];
+  bf16x8 fq[NS];
   {
     const uint16_t* q = a.q + (t0 + i0 + qi) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
     const uint32_t sign = a.mask.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      uint4 x = i0 + qi < n && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
-      fq[i] = make_uint4(x.x ^ sign, x.y ^ sign, x.z ^ sign, x.w ^ sign);
+      const uint4 z = i0 + qi < n && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
+      fq[i] = as_frag(make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign));
     }
   }
+  const int t = p0 + qi;
+  const Sight see = sight(a.mask, t, keys, front);
   // x = c1 times the product; with GEN the product becomes x itself
   const float size = fabsf(a.mask.scale), c1 = GEN ? 1.0f : fmaxf(size * kLog2e, 1e-30f);
   const float c2 = GEN && a.mask.cap > 0.0f ? 2.0f * kLog2e / a.mask.cap : 0.0f;
@@ -197,99 +234,108 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_tiles(AttArgs a) {
   }
   const uint16_t* kb = a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * a.d;
   const uint16_t* vb = a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * a.d;
-  const auto load = [&](int j0, uint16_t* K, uint16_t* V) __attribute__((always_inline)) {
-    const int rows = min(keys - j0, BN);  // rows past the end read as zero
-    const Buffer bk = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(kb + j0 * a.k_stride), 0,
-                                                        static_cast<int>(2 * rows * a.k_stride), 0x00027000);
-    const Buffer bv = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(vb + j0 * a.v_stride), 0,
-                                                        static_cast<int>(2 * rows * a.v_stride), 0x00027000);
+  const int kbytes = static_cast<int>(2 * a.k_stride), vbytes = static_cast<int>(2 * a.v_stride);
+  // rows past the end read as zero (behind the last tile too, of which then nothing is read)
+  const auto load = [&](int j0, const uint16_t* base, int bytes, const uint32_t (&at)[U], uint16_t* to) __attribute__((always_inline)) {
+    const int64_t off = static_cast<int64_t>(j0) * bytes;
+    const Buffer b = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<char*>(const_cast<uint16_t*>(base)) + off, 0,
+                                                       uniform(max(min(keys - j0, BN), 0)) * bytes, 0x00027000);
 #pragma unroll
-    for (int u = 0; u < U; ++u) to_lds(bk, ko[u], K + (u * kWaves + w) * 512);
-#pragma unroll
-    for (int u = 0; u < U; ++u) to_lds(bv, vo[u], V + (u * kWaves + w) * 512);
+    for (int u = 0; u < U; ++u) to_lds(b, at[u], to + (u * kWaves + w) * kChunk<D>);
   };
 
-  // reads: K's row qi of 32, pieces 2 i + half; V's rows 4 half + (lane % 16) / 4 of 8, columns by lane / 16 % 2 and lane % 4
-  const int kx = half ^ exchange<D>(qi), kat = qi * D;
+  // reads: K's row qi, pieces 2 e + half; V's rows 4 half + (lane % 16) / 4 of 8, pieces 4 b + vp
+  const int kx = half ^ exchange<D>(qi), kat = qi / RPI * kChunk<D> + qi % RPI * D;
+  const auto k_at = [&](int e) {
+    return D == 128 ? kat + 8 * half + 32 * (e / 2 ^ (qi & 3)) + 16 * (e % 2) : kat + 8 * (kx ^ 2 * e);
+  };
   const int vr = 4 * half + (lane >> 2 & 3), vp = 2 * (lane >> 4 & 1) + (lane >> 1 & 1);
-  const int vat = vr * D + 4 * (lane & 1);
-  const int vx0 = vp ^ exchange<D>(vr), vx1 = vp ^ exchange<D>(vr + 8);
+  const int vat = vr / RPI * kChunk<D> + vr % RPI * D + 4 * (lane & 1);
+  const auto v_at = [&](int r, int b) {  // rows r on, a multiple of 8
+    return r / RPI * kChunk<D> + vat + 8 * ((D == 128 ? vp ^ exchange<D>(vr) : vp ^ exchange<D>(vr + r % 16)) ^ 4 * b);
+  };
 
   float m = -INFINITY, l = 0.0f;
   floatx16 o[NB] = {};
-  const auto step = [&](int i, uint16_t* nK, uint16_t* nV, const uint16_t* __restrict__ cK,
-                        const uint16_t* __restrict__ cV) __attribute__((always_inline)) {
-    landed_barrier();
-    const int j0 = key_of(i);
-    if (i + 1 < tiles) load(key_of(i + 1), nK, nV);
-    // no query of the wave sees a key of the tile
-    if (!some || (j0 >= front && (j0 > w1.hi || j0 + BN <= w0.lo))) return;
-    floatx16 x[NK] = {};
+  const auto products = [&](const uint16_t* K, floatx16& x) __attribute__((always_inline)) {
 #pragma unroll
     for (int e = 0; e < NS; ++e)
+      x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(*reinterpret_cast<const bf16x8*>(K + k_at(e)), fq[e],
+                                                  e ? x : floatx16{}, 0, 0, 0);
+  };
+  // scores of 32 keys made ready, and the maximum that their weights are taken against
+  const auto ready = [&](int j0, floatx16& x) __attribute__((always_inline)) {
+    if (GEN || !(j0 >= whole0 && j0 <= whole1)) {
 #pragma unroll
-      for (int b = 0; b < NK; ++b) {
-        const uint4 f = *reinterpret_cast<const uint4*>(cK + 32 * b * D + kat + 8 * (kx ^ 2 * e));
-        x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(f), as_frag(fq[e]), x[b], 0, 0, 0);
-      }
-    if (GEN) {
-#pragma unroll
-      for (int b = 0; b < NK; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float y = x[b][r] * size;
-          if (c2 != 0.0f) y = capped(y, a.mask.cap, c2);
-          x[b][r] = (y - slope * static_cast<float>(abs(t - (j0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4)))) * kLog2e;
+      for (int r = 0; r < 16; ++r) {
+        const int j = j0 + 8 * (r / 4) + 4 * half + r % 4;
+        if (GEN) {
+          float z = x[r] * size;
+          if (c2 != 0.0f) z = capped(z, a.mask.cap, c2);
+          x[r] = (z - slope * static_cast<float>(abs(t - j))) * kLog2e;
         }
+        x[r] = see.has(j) ? x[r] : -INFINITY;
+      }
     }
-    // every query of the wave sees every key of the tile?
-    const bool whole = j0 + BN <= front || (j0 >= w1.lo && j0 + BN - 1 <= w0.hi);
-    if (!whole) {
+    float z[5];
 #pragma unroll
-      for (int b = 0; b < NK; ++b)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          x[b][r] = see.has(j0 + 32 * b + 8 * (r / 4) + 4 * half + r % 4) ? x[b][r] : -INFINITY;
-    }
-    float top = x[0][0];
-#pragma unroll
-    for (int b = 0; b < NK; ++b)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, x[b][r]);
-    top = max_xor32(top) * c1;
+    for (int r = 0; r < 5; ++r) z[r] = fmaxf(fmaxf(x[3 * r], x[3 * r + 1]), x[3 * r + 2]);
+    const float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), z[2]), fmaxf(fmaxf(z[3], z[4]), x[15])) * c1;
     if (__any(top > m + kSlack)) {
-      const float now = fmaxf(m, top), fall = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
+      const float now = fmaxf(m, max_xor32(top)), fall = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
       m = now;
       l *= fall;
 #pragma unroll
       for (int b = 0; b < NB; ++b) o[b] *= fall;
     }
+  };
+  // their weights, and the second product
+  const auto weigh = [&](const floatx16& x, uint32_t (&p)[8]) __attribute__((always_inline)) {
     const float base = m == -INFINITY ? 0.0f : m;
-    uint32_t p[NK][8];
 #pragma unroll
-    for (int b = 0; b < NK; ++b)
+    for (int r = 0; r < 8; ++r) {
+      p[r] = pack2(exp2_fast(fmaf(x[2 * r], c1, -base)), exp2_fast(fmaf(x[2 * r + 1], c1, -base)));
+      l = dot2_ones(p[r], l);
+    }
+  };
+  const auto apply = [&](const uint32_t (&p)[8], const uint16_t* V) __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float y0 = exp2_fast(fmaf(x[b][2 * r], c1, -base)), y1 = exp2_fast(fmaf(x[b][2 * r + 1], c1, -base));
-        p[b][r] = pack2(y0, y1);
-        l += low_half(p[b][r]) + high_half(p[b][r]);
-      }
-#pragma unroll
-    for (int e = 0; e < 2 * NK; ++e) {  // 16 keys
-      const bf16x8 fp = as_frag(make_uint4(p[e / 2][4 * (e % 2)], p[e / 2][4 * (e % 2) + 1], p[e / 2][4 * (e % 2) + 2],
-                                           p[e / 2][4 * (e % 2) + 3]));
+    for (int e = 0; e < 2; ++e) {  // 16 keys
+      const bf16x8 fp = as_frag(make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint2 f0 = read_tr(cV + 16 * e * D + vat + 8 * (vx0 ^ 4 * b));
-        const uint2 f1 = read_tr(cV + 16 * e * D + 8 * D + vat + 8 * (vx1 ^ 4 * b));
+        const uint2 f0 = read_tr(V + v_at(16 * e, b));
+        const uint2 f1 = read_tr(V + v_at(16 * e + 8, b));
         o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(make_uint4(f0.x, f0.y, f1.x, f1.y)), fp, o[b], 0, 0, 0);
       }
     }
   };
-  if (tiles > 0) load(key_of(0), sK[0], sV[0]);
+  // some query of the wave sees a key of the tile?
+  const auto sees = [&](int j0) { return j0 < seen0 || (j0 >= seen1 && j0 <= seen2); };
+  int j0 = ahead ? 0 : from;
+  // one tile, with the next one's loads on their way
+  const auto step = [&](uint16_t* nK, uint16_t* nV, const uint16_t* cK, const uint16_t* cV) __attribute__((always_inline)) {
+    const int next = after(j0);
+    landed_barrier();
+    load(next, kb, kbytes, ko, nK);
+    load(next, vb, vbytes, vo, nV);
+    if (sees(j0)) {
+      floatx16 x;
+      uint32_t p[8];
+      products(cK, x);
+      ready(j0, x);
+      weigh(x, p);
+      apply(p, cV);
+    }
+    j0 = next;
+  };
+  if (tiles > 0) {
+    load(j0, kb, kbytes, ko, sK0);
+    load(j0, vb, vbytes, vo, sV0);
+  }
   for (int i = 0; i < tiles; i += 2) {
-    step(i, sK[1], sV[1], sK[0], sV[0]);
-    if (i + 1 < tiles) step(i + 1, sK[0], sV[0], sK[1], sV[1]);
+    step(sK1, sV1, sK0, sV0);
+    if (i + 1 < tiles) step(sK0, sV0, sK1, sV1);
   }
   if (!some) return;
 
@@ -302,17 +348,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_tiles(AttArgs a) {
     for (int r = 0; r < 16; ++r) odd = fmaf(o[b][r], 0.0f, odd);  // 0 x infinity and 0 x NaN are NaN
   odd = sum_xor32(odd);
   // lanes of the lower half take columns 0 .. 7 of each 16, of the upper half 8 .. 15
-  const int64_t row = t0 + i0 + qi;
-  uint16_t* out = a.o + (row * a.hq + h) * a.d + 8 * half;
+  uint16_t* out = a.o + ((t0 + i0 + qi) * a.hq + h) * a.d + 8 * half;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t y[4];
+      uint32_t z[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) y[r] = pack2(o[b][8 * e + 2 * r] * inv, o[b][8 * e + 2 * r + 1] * inv);
-      const auto u = __builtin_amdgcn_permlane32_swap(y[0], y[2], false, false);
-      const auto v = __builtin_amdgcn_permlane32_swap(y[1], y[3], false, false);
+      for (int r = 0; r < 4; ++r) z[r] = pack2(o[b][8 * e + 2 * r] * inv, o[b][8 * e + 2 * r + 1] * inv);
+      const auto u = __builtin_amdgcn_permlane32_swap(z[0], z[2], false, false);
+      const auto v = __builtin_amdgcn_permlane32_swap(z[1], z[3], false, false);
       if (i0 + qi < n && 32 * b + 16 * e + 8 * half < a.d)
         *reinterpret_cast<uint4*>(out + 32 * b + 16 * e) = make_uint4(u[0], v[0], u[1], v[1]);
     }
@@ -326,15 +371,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void prompt_tiles(AttArgs a) {
   }
 }
 
-template <int D, int BN>
+template <int D>
 void launch(AttArgs a, hipStream_t st) {
   constexpr int64_t kMost = (int64_t(1) << 32) / (64 * kWaves) - 1;  // workgroups that one launch has threads for
+  a.slots = a.total / kRows + a.nseq;  // sequence s has slots offsets[s] / kRows + s and on
+  a.units = a.slots * a.hq;
   for (a.first = 0; a.first < a.units; a.first += kMost) {
     const dim3 grid(static_cast<unsigned>(a.units - a.first < kMost ? a.units - a.first : kMost)), block(64 * kWaves);
     if (a.mask.cap > 0.0f || a.mask.slopes)
-      hipLaunchKernelGGL((prompt_tiles<D, BN, true>), grid, block, 0, st, a);
+      hipLaunchKernelGGL((prompt_tiles<D, true>), grid, block, 0, st, a);
     else
-      hipLaunchKernelGGL((prompt_tiles<D, BN, false>), grid, block, 0, st, a);
+      hipLaunchKernelGGL((prompt_tiles<D, false>), grid, block, 0, st, a);
   }
 }
 
@@ -376,8 +423,6 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.q_stride = q_stride;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  a.slots = total / kRows + nseq;  // sequence s has slots offsets[s] / 128 + s and on
-  a.units = a.slots * hq;
   a.nseq = static_cast<int>(nseq);
   a.hq = static_cast<int>(hq);
   a.hkv = static_cast<int>(hkv);
@@ -385,10 +430,10 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.d = static_cast<int>(d);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d <= 64)
-    launch<64, 64>(a, st);
+    launch<64>(a, st);
   else if (d <= 128)
-    launch<128, 64>(a, st);
+    launch<128>(a, st);
   else
-    launch<256, 32>(a, st);
+    launch<256>(a, st);
   return launch_status();
 }
