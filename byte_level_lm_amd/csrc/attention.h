@@ -107,6 +107,106 @@ __device__ inline float capped(float x, float cap, float two_over_cap_log2e) {
   return cap - 2.0f * cap * __builtin_amdgcn_rcpf(exp2_fast(x * two_over_cap_log2e) + 1.0f);
 }
 
+// ---------------------------------------------------------------- shares of a query's keys
+
+constexpr int kMaxSplits = 64;   // the lanes of a wave, which joins them
+
+// What each of a query's shares of keys gave (queries: row * hq + head)
+struct Shares {
+  float* part;      // [queries x splits x d], not yet divided by the sum
+  float2* stat;     // [queries x splits]: maximum and sum of the weights against it
+  int splits;
+};
+inline size_t shares_bytes(int64_t queries, int64_t splits, int64_t d) {
+  return 16 + (splits > 1 ? static_cast<size_t>(queries * splits) * (sizeof(float) * d + sizeof(float2)) : 0);
+}
+inline Shares shares_at(void* ws, int64_t queries, int64_t splits) {
+  float2* stat = static_cast<float2*>(ws);
+  return {reinterpret_cast<float*>(stat + (queries * splits + 1) / 2 * 2), stat, static_cast<int>(splits)};
+}
+
+__host__ __device__ inline int join_lanes(int d) { return d <= 32 ? 8 : d <= 64 ? 16 : d <= 128 ? 32 : 64; }  // of four values each
+
+// Joins a query's shares.  Up to kFewSplits of them: join_lanes(d) lanes of a wave, with all
+// their loads in flight at once (beside those of the wave's other queries); more: a wave, whose
+// groups of lanes take the shares in turn.  True where scores were finite and an output is not.
+constexpr int kFewSplits = 8;
+
+__device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int d, uint16_t* o) {
+  const int lanes = join_lanes(d), in = lane_id() & (lanes - 1), col = 4 * in, first = lane_id() - in;
+  if (!mine) query = 0;
+  const float2 st = in < sh.splits ? sh.stat[query * sh.splits + in] : make_float2(-INFINITY, 0.0f);
+  const float* part = sh.part + query * sh.splits * d + (col < d ? col : 0);
+  float4 v[kFewSplits];
+#pragma unroll
+  for (int i = 0; i < kFewSplits; ++i)
+    if (i < sh.splits) v[i] = *reinterpret_cast<const float4*>(part + i * d);
+  float top = st.y == 0.0f ? -INFINITY : st.x;
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  const float weight = st.y == 0.0f ? 0.0f : exp2_fast(st.x - (top == -INFINITY ? 0.0f : top));
+  float sum = weight * st.y;
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, kWave);
+  sum = __shfl(sum, first, kWave);
+  float y[4] = {};
+#pragma unroll
+  for (int i = 0; i < kFewSplits; ++i)
+    if (i < sh.splits) {
+      const float w = __shfl(weight, first + i, kWave);
+      const bool some = __shfl(st.y, first + i, kWave) != 0.0f;  // a share without keys has written no values
+      y[0] = some ? fmaf(w, v[i].x, y[0]) : y[0];
+      y[1] = some ? fmaf(w, v[i].y, y[1]) : y[1];
+      y[2] = some ? fmaf(w, v[i].z, y[2]) : y[2];
+      y[3] = some ? fmaf(w, v[i].w, y[3]) : y[3];
+    }
+  mine = mine && col < d;
+  const bool odd = mine && (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(sum) < INFINITY;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
+  if (mine) *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+  return odd;
+}
+
+__device__ inline bool join_many(const Shares& sh, int64_t query, int d, uint16_t* o) {
+  const int lane = lane_id(), lanes = join_lanes(d), col = 4 * (lane & (lanes - 1));
+  const float2 st = lane < sh.splits ? sh.stat[query * sh.splits + lane] : make_float2(-INFINITY, 0.0f);
+  float top = st.y == 0.0f ? -INFINITY : st.x;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
+  const float weight = st.y == 0.0f ? 0.0f : exp2_fast(st.x - (top == -INFINITY ? 0.0f : top));
+  const float sum = wave_sum(weight * st.y);
+  const bool mine = col < d;
+  const float* part = sh.part + query * sh.splits * d + (mine ? col : 0);
+  float y[4] = {};
+  for (int i0 = 0; i0 < sh.splits; i0 += 8 * kWave / lanes) {
+    float4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * (kWave / lanes) + lane / lanes;
+      v[u] = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(min(i, sh.splits - 1)) * d);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * (kWave / lanes) + lane / lanes;
+      const float w = __shfl(weight, i & 63, kWave);
+      const bool some = __shfl(st.y, i & 63, kWave) != 0.0f && i < sh.splits;
+      y[0] = some ? fmaf(w, v[u].x, y[0]) : y[0];
+      y[1] = some ? fmaf(w, v[u].y, y[1]) : y[1];
+      y[2] = some ? fmaf(w, v[u].z, y[2]) : y[2];
+      y[3] = some ? fmaf(w, v[u].w, y[3]) : y[3];
+    }
+  }
+  for (int off = lanes; off < kWave; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], off, kWave);
+  const bool odd = mine && (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(sum) < INFINITY;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
+  if (mine && lane < lanes) *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+  return odd;
+}
+
 inline bool page_shift(int64_t page, int* shift) {
   for (*shift = 4; *shift <= 8; ++*shift)
     if (page == int64_t(1) << *shift) return true;

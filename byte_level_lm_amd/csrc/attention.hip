@@ -36,6 +36,7 @@ struct AttArgs {
   int64_t first, units, slots;   // this launch's first unit of work, all of them, slots of a workgroup's queries
   int nseq, hq, hkv, group, d;
   Mask mask;
+  Shares shares;
 };
 
 __device__ inline void to_lds(Buffer b, uint32_t at, void* lds) {
@@ -75,7 +76,7 @@ __device__ inline float dot2_ones(uint32_t pair, float sum) {
 // What one query sees: keys lo .. hi and those below front.
 struct Sight {
   int lo, hi, front;
-  __device__ inline bool has(int j) const { return (j >= lo && j <= hi) || j < front; }
+  __device__ inline bool has(int j) const { return ((j >= lo) & (j <= hi)) | (j < front); }
 };
 __device__ inline Sight sight(const Mask& m, int t, int keys, int front) {
   Sight s;
@@ -153,9 +154,9 @@ __device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t
         make_uint2(pack2(o[0] / l, o[1] / l), pack2(o[2] / l, o[3] / l));
 }
 
-// GEN: with a cap or slopes
-template <int D, bool GEN>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void prompt_tiles(AttArgs a) {
+// GEN: with a cap or slopes.  SPLIT: a share of the tiles, to be joined.
+template <int D, bool GEN, bool SPLIT>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void prompt_tiles(AttArgs a) {
   constexpr int NS = D / 16;               // steps of the first product
   constexpr int NB = D / 32;               // 32-column blocks of the second
   constexpr int RPI = 512 / D;             // rows of a 1 KB load
@@ -176,6 +177,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
       unit += (in % kXcds) * kRun + in / kXcds - in;
     }
   }
+  const int split = SPLIT ? static_cast<int>(unit % a.shares.splits) : 0;
+  if (SPLIT) unit /= a.shares.splits;
   const int64_t per = a.slots * a.group;
   const int kh = static_cast<int>(unit / per);
   const int64_t slot = unit % per / a.group;
@@ -195,8 +198,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   const int to = max(high.hi + 1, front);
   if (ahead >= from) from = ahead;
   from = uniform(from);
-  const int tiles = max((ahead + to - from + BN - 1) / BN, ahead / BN);
-  const auto after = [&](int j) { return j + BN == ahead ? from : j + BN; };
+  int tiles = max((ahead + to - from + BN - 1) / BN, ahead / BN), begin = 0;
+  if (SPLIT) {
+    const int share = (tiles + a.shares.splits - 1) / a.shares.splits;
+    begin = split * share;
+    tiles = max(min(share, tiles - begin), 0);
+  }
   // the wave's own queries
   const int i0 = first + 32 * w, p0 = i0 + shift, p1 = min(i0 + 32, n) - 1 + shift;
   const bool some = i0 < n;
@@ -220,8 +227,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   const Sight see = sight(a.mask, t, keys, front);
   // x = c1 times the product; with GEN the product becomes x itself
   const float size = fabsf(a.mask.scale), c1 = GEN ? 1.0f : fmaxf(size * kLog2e, 1e-30f);
-  const float c2 = GEN && a.mask.cap > 0.0f ? 2.0f * kLog2e / a.mask.cap : 0.0f;
-  const float slope = GEN && a.mask.slopes ? a.mask.slopes[h] : 0.0f;
+  const float cap2 = GEN ? a.mask.cap * kLog2e : 0.0f, to_cap = GEN && cap2 != 0.0f ? 2.0f * kLog2e / a.mask.cap * size : 0.0f;
+  const float slope2 = GEN && a.mask.slopes ? a.mask.slopes[h] * kLog2e : 0.0f;
 
   // loads: where the lane's piece of each 1 KB lies
   uint32_t ko[U], vo[U];
@@ -232,14 +239,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
     ko[u] = in ? static_cast<uint32_t>(2 * (r * a.k_stride + 8 * p)) : kOutside;
     vo[u] = in ? static_cast<uint32_t>(2 * (r * a.v_stride + 8 * p)) : kOutside;
   }
-  const uint16_t* kb = a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * a.d;
-  const uint16_t* vb = a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * a.d;
   const int kbytes = static_cast<int>(2 * a.k_stride), vbytes = static_cast<int>(2 * a.v_stride);
+  const char* kb = reinterpret_cast<const char*>(a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * a.d);
+  const char* vb = reinterpret_cast<const char*>(a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * a.d);
   // rows past the end read as zero (behind the last tile too, of which then nothing is read)
-  const auto load = [&](int j0, const uint16_t* base, int bytes, const uint32_t (&at)[U], uint16_t* to) __attribute__((always_inline)) {
-    const int64_t off = static_cast<int64_t>(j0) * bytes;
-    const Buffer b = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<char*>(const_cast<uint16_t*>(base)) + off, 0,
-                                                       uniform(max(min(keys - j0, BN), 0)) * bytes, 0x00027000);
+  const auto load = [&](const char* from, int rows, int bytes, const uint32_t (&at)[U], uint16_t* to) __attribute__((always_inline)) {
+    const Buffer b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, rows * bytes, 0x00027000);
 #pragma unroll
     for (int u = 0; u < U; ++u) to_lds(b, at[u], to + (u * kWaves + w) * kChunk<D>);
   };
@@ -255,7 +260,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
     return r / RPI * kChunk<D> + vat + 8 * ((D == 128 ? vp ^ exchange<D>(vr) : vp ^ exchange<D>(vr + r % 16)) ^ 4 * b);
   };
 
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, base = 0.0f, l = 0.0f;  // weights are 2^(x - base), base = m once there is one
   floatx16 o[NB] = {};
   const auto products = [&](const uint16_t* K, floatx16& x) __attribute__((always_inline)) {
 #pragma unroll
@@ -265,16 +270,38 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   };
   // scores of 32 keys made ready, and the maximum that their weights are taken against
   const auto ready = [&](int j0, floatx16& x) __attribute__((always_inline)) {
-    if (GEN || !(j0 >= whole0 && j0 <= whole1)) {
+    if (GEN) {  // the product becomes x: capped as in capped(), then lowered by the distance
+      if (cap2 != 0.0f) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int j = j0 + 8 * (r / 4) + 4 * half + r % 4;
-        if (GEN) {
-          float z = x[r] * size;
-          if (c2 != 0.0f) z = capped(z, a.mask.cap, c2);
-          x[r] = (z - slope * static_cast<float>(abs(t - j))) * kLog2e;
+        for (int r = 0; r < 16; ++r) x[r] = fmaf(-2.0f * cap2, __builtin_amdgcn_rcpf(exp2_fast(x[r] * to_cap) + 1.0f), cap2);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] *= size * kLog2e;
+      }
+      if (slope2 != 0.0f) {
+        const float far = static_cast<float>(t - j0 - 4 * half);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] = fmaf(-slope2, fabsf(far - static_cast<float>(8 * (r / 4) + r % 4)), x[r]);
+      }
+    }
+    if (!(j0 >= whole0 && j0 <= whole1)) {
+      const int lo = see.lo - j0 - 4 * half, hi = see.hi - j0 - 4 * half;  // of the keys 8 (r / 4) + r % 4
+      if (j0 < front) {
+        const int ahead = front - j0 - 4 * half;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int j = 8 * (r / 4) + r % 4;
+          x[r] = ((j >= lo) & (j <= hi)) | (j < ahead) ? x[r] : -INFINITY;
         }
-        x[r] = see.has(j) ? x[r] : -INFINITY;
+      } else {  // one edge or both
+        if (j0 + BN - 1 > w0.hi) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = 8 * (r / 4) + r % 4 <= hi ? x[r] : -INFINITY;
+        }
+        if (j0 < w1.lo) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[r] = 8 * (r / 4) + r % 4 >= lo ? x[r] : -INFINITY;
+        }
       }
     }
     float z[5];
@@ -282,7 +309,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
     for (int r = 0; r < 5; ++r) z[r] = fmaxf(fmaxf(x[3 * r], x[3 * r + 1]), x[3 * r + 2]);
     const float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), z[2]), fmaxf(fmaxf(z[3], z[4]), x[15])) * c1;
     if (__any(top > m + kSlack)) {
-      const float now = fmaxf(m, max_xor32(top)), fall = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
+      const float now = fmaxf(m, max_xor32(top));
+      base = now == -INFINITY ? 0.0f : now;
+      const float fall = exp2_fast(m - base);
       m = now;
       l *= fall;
 #pragma unroll
@@ -291,7 +320,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   };
   // their weights, and the second product
   const auto weigh = [&](const floatx16& x, uint32_t (&p)[8]) __attribute__((always_inline)) {
-    const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       p[r] = pack2(exp2_fast(fmaf(x[2 * r], c1, -base)), exp2_fast(fmaf(x[2 * r + 1], c1, -base)));
@@ -312,13 +340,26 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   };
   // some query of the wave sees a key of the tile?
   const auto sees = [&](int j0) { return j0 < seen0 || (j0 >= seen1 && j0 <= seen2); };
-  int j0 = ahead ? 0 : from;
+  // the tile that the loads are at; its first row of k and v
+  int j1 = begin * BN < ahead ? begin * BN : from + begin * BN - ahead;
+  const char *kj = kb + static_cast<int64_t>(j1) * kbytes, *vj = vb + static_cast<int64_t>(j1) * vbytes;
+  const auto load_next = [&](uint16_t* K, uint16_t* V) __attribute__((always_inline)) {
+    const int rows = max(uniform(min(keys - j1, BN)), 0);
+    load(kj, rows, kbytes, ko, K);
+    load(vj, rows, vbytes, vo, V);
+    int by = BN;
+    if (j1 + BN == ahead) by = from - j1;
+    j1 += by;
+    kj += static_cast<int64_t>(by) * kbytes;
+    vj += static_cast<int64_t>(by) * vbytes;
+  };
+  int j2 = j1;  // the tile that the products are at
   // one tile, with the next one's loads on their way
   const auto step = [&](uint16_t* nK, uint16_t* nV, const uint16_t* cK, const uint16_t* cV) __attribute__((always_inline)) {
-    const int next = after(j0);
+    const int j0 = j2;
+    j2 = j1;
     landed_barrier();
-    load(next, kb, kbytes, ko, nK);
-    load(next, vb, vbytes, vo, nV);
+    load_next(nK, nV);
     if (sees(j0)) {
       floatx16 x;
       uint32_t p[8];
@@ -327,12 +368,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
       weigh(x, p);
       apply(p, cV);
     }
-    j0 = next;
   };
-  if (tiles > 0) {
-    load(j0, kb, kbytes, ko, sK0);
-    load(j0, vb, vbytes, vo, sV0);
-  }
+  if (tiles > 0) load_next(sK0, sV0);
   for (int i = 0; i < tiles; i += 2) {
     step(sK1, sV1, sK0, sV0);
     if (i + 1 < tiles) step(sK0, sV0, sK1, sV1);
@@ -340,6 +377,20 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   if (!some) return;
 
   l = sum_xor32(l);
+  if (SPLIT) {
+    if (i0 + qi < n) {
+      const int64_t query = (t0 + i0 + qi) * a.hq + h;
+      if (half == 0) a.shares.stat[query * a.shares.splits + split] = make_float2(m, l);
+      float* out = a.shares.part + (query * a.shares.splits + split) * a.d + 4 * half;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (32 * b + 8 * e < a.d && l != 0.0f)
+            *reinterpret_cast<float4*>(out + 32 * b + 8 * e) = make_float4(o[b][4 * e], o[b][4 * e + 1], o[b][4 * e + 2], o[b][4 * e + 3]);
+    }
+    return;
+  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   float odd = 0.0f;
 #pragma unroll
@@ -371,18 +422,57 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
   }
 }
 
+__global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
+  const int lanes = join_lanes(a.d);
+  const int64_t query = (static_cast<int64_t>(blockIdx.x) * 64 * kWaves + threadIdx.x) / lanes, row = query / a.hq;
+  const bool mine = row < a.total && row >= a.offsets[0] && row < a.offsets[a.nseq];
+  uint64_t again = __ballot(join_few(a.shares, query, mine, a.d, a.o));
+  if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores of the join
+  while (again) {  // scores were finite and outputs are not: those queries once more, one by one
+    const int64_t first = lane_value(query, __builtin_ctzll(again));
+    again &= ~__ballot(query == first);
+    const int64_t r = first / a.hq;
+    const int h = static_cast<int>(first - r * a.hq);
+    const int s = uniform(wave_find(a.nseq, r, [&](int i) { return a.offsets[i]; }));
+    int64_t t0, t1, k0, k1;
+    seq_rows(a.offsets, s, a.total, &t0, &t1);
+    seq_rows(a.k_offsets, s, a.total_k, &k0, &k1);
+    if (r < t0 || r >= t1) continue;
+    const int keys = static_cast<int>(k1 - k0), t = static_cast<int>(r - t0 + keys - (t1 - t0));
+    const int front = a.mask.prefix ? min(max(a.mask.prefix[s], 0), keys) : 0;
+    query_alone(a, r, h, k0, t, sight(a.mask, t, keys, front), a.mask.slopes ? a.mask.slopes[h] : 0.0f);
+  }
+}
+
+// Shares of a query's keys: where the workgroups of whole queries would leave
+// CUs without three of them, shares of 256 keys or more do (8 pieces of 64 to 512 queries
+// of 12 heads behind 4096 keys: SPLIT_OFF us whole, SPLIT_ON us in 3 shares).
+int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq) {
+  const int64_t units = (total / kRows + nseq) * hq, want = ceil_div(5 * 256, units), most = keys / 256;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n > kFewSplits ? kFewSplits : n);
+}
+
+template <int D, bool SPLIT>
+void launch_as(const AttArgs& a, dim3 grid, hipStream_t st) {
+  if (a.mask.cap > 0.0f || a.mask.slopes)
+    hipLaunchKernelGGL((prompt_tiles<D, true, SPLIT>), grid, dim3(64 * kWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL((prompt_tiles<D, false, SPLIT>), grid, dim3(64 * kWaves), 0, st, a);
+}
+
 template <int D>
 void launch(AttArgs a, hipStream_t st) {
   constexpr int64_t kMost = (int64_t(1) << 32) / (64 * kWaves) - 1;  // workgroups that one launch has threads for
   a.slots = a.total / kRows + a.nseq;  // sequence s has slots offsets[s] / kRows + s and on
-  a.units = a.slots * a.hq;
-  for (a.first = 0; a.first < a.units; a.first += kMost) {
-    const dim3 grid(static_cast<unsigned>(a.units - a.first < kMost ? a.units - a.first : kMost)), block(64 * kWaves);
-    if (a.mask.cap > 0.0f || a.mask.slopes)
-      hipLaunchKernelGGL((prompt_tiles<D, true>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((prompt_tiles<D, false>), grid, block, 0, st, a);
+  a.units = a.slots * a.hq * a.shares.splits;
+  if (a.shares.splits > 1) {  // few units by the rule of splits_of
+    launch_as<D, true>(a, dim3(static_cast<unsigned>(a.units)), st);
+    hipLaunchKernelGGL(prompt_join, dim3(static_cast<unsigned>(ceil_div(a.total * a.hq * join_lanes(a.d), 64 * kWaves))), dim3(64 * kWaves), 0, st, a);
+    return;
   }
+  for (a.first = 0; a.first < a.units; a.first += kMost)
+    launch_as<D, false>(a, dim3(static_cast<unsigned>(a.units - a.first < kMost ? a.units - a.first : kMost)), st);
 }
 
 }  // namespace
@@ -392,7 +482,10 @@ using namespace bllm;
 
 extern "C" size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t total_k, int64_t hq, int64_t hkv,
                                            int64_t d) {
-  return nseq < 1 || total < 0 || total_k < 0 || hq < 1 || hkv < 1 || d < 1 ? 0 : 16;
+  if (nseq < 1 || nseq > kMaxSeqs || total < 0 || total > kMaxTokens || total_k < 0 || total_k > kMaxTokens ||
+      heads_check(hq, hkv, d) != BLLM_OK)
+    return 0;
+  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq), d);
 }
 
 extern "C" int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,
@@ -408,7 +501,7 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
     return BLLM_E_INVAL;
   if (rc != BLLM_OK || dtype != BLLM_BF16 || nseq > kMaxSeqs || total > kMaxTokens || total_k > kMaxTokens ||
       !stride_ok(q_stride) || !stride_ok(k_stride) || !stride_ok(v_stride) || !aligned16(q) || !aligned16(k) ||
-      !aligned16(v) || !aligned16(o_out))
+      !aligned16(v) || !aligned16(o_out) || !aligned16(ws))
     return BLLM_E_NOTSUP;
   if (!ws || ws_bytes < bllm_attention_workspace(nseq, total, total_k, hq, hkv, d)) return BLLM_E_WS;
   if (total == 0) return BLLM_OK;
@@ -428,6 +521,10 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.hkv = static_cast<int>(hkv);
   a.group = static_cast<int>(hq / hkv);
   a.d = static_cast<int>(d);
+  // a window alone bounds the keys that a query sees, with the workgroup's others
+  int64_t keys = total_k / nseq;
+  if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
+  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d <= 64)
     launch<64>(a, st);

@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kTile = 32;        // keys of a wave's tile
 constexpr int kStepWaves = 4;
-constexpr int kMaxSplits = 64;   // the lanes of a wave, which joins them
 
 struct StepArgs {
   const uint16_t* q;
@@ -30,10 +29,9 @@ struct StepArgs {
   Pages pages;
   const int32_t* lengths;
   uint16_t* o;
-  float* part;      // [nseq x hq x splits x d], not yet divided by the sum
-  float2* stat;     // [nseq x hq x splits]: maximum and sum
+  Shares shares;
   int64_t q_stride;
-  int hq, group, blocks, splits;
+  int hq, group, blocks;  // query heads, those of a key head, blocks of 16 of these
   Mask mask;
 };
 
@@ -49,13 +47,14 @@ struct Seen {
     tiles = max((n + kTile - 1) / kTile - skip, 0);
   }
   __device__ inline int key(int tile) const { return (tile < first ? tile : tile + skip) * kTile; }
-  __device__ inline bool has(int j) const { return j < front || (j >= lo && j < n); }
-  __device__ inline bool all(int j) const { return j + kTile <= front || (j >= lo && j + kTile <= n); }
+  // without branches: the selects that use it then stay selects
+  __device__ inline bool has(int j) const { return (j < front) | ((j >= lo) & (j < n)); }
+  __device__ inline bool all(int j) const { return (j + kTile <= front) | ((j >= lo) & (j + kTile <= n)); }
 };
 
 // GEN: with a cap or slopes
 template <int D, bool Q8, bool GEN>
-__global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
+__global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 1 : Q8 ? 4 : 3) void step_share(StepArgs a) {
   constexpr int VP = D / 16;               // values of a row that a lane has of V
   constexpr int VW = Q8 ? VP / 4 : VP / 2; // their 32-bit words
   constexpr int KP = Q8 ? D / 64 : D / 32; // 16-byte pieces of a row that a lane has of K
@@ -64,10 +63,10 @@ __global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
   __shared__ float sM[kStepWaves][16], sL[kStepWaves][16];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits, kh = rest / a.blocks, block = rest % a.blocks;
+  const int split = blockIdx.x % a.shares.splits, rest = blockIdx.x / a.shares.splits, kh = rest / a.blocks, block = rest % a.blocks;
   const int s = blockIdx.y, d = a.pages.d, h0 = kh * a.group + 16 * block, heads = min(a.group - 16 * block, 16);
   const Seen seen(a, s);
-  const int share = (seen.tiles + a.splits - 1) / a.splits, t0 = split * share, t1 = min(t0 + share, seen.tiles);
+  const int share = (seen.tiles + a.shares.splits - 1) / a.shares.splits, t0 = split * share, t1 = min(t0 + share, seen.tiles);
   const int h = h0 + min(c, heads - 1), t = seen.n - 1;
 
   // the queries, 8 values of each 32 (in the order of K's pieces)
@@ -166,11 +165,11 @@ __global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
       // keys that the query does not see: no score, and zeros for what their rows hold
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool has = page[e / 4] && seen.has(j0 + 16 * (e / 4) + 4 * g + e % 4);
+        const bool has = page[e / 4] & seen.has(j0 + 16 * (e / 4) + 4 * g + e % 4);
         p[e] = has ? p[e] : -INFINITY;
         if (Q8) vs[e / 4][e % 4] = has ? vs[e / 4][e % 4] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) v[e][i] = has ? v[e][i] : 0;
+        for (int i = 0; i < VW; ++i) v[e][i] &= has ? ~0u : 0u;
       }
     }
     float top = p[0];
@@ -242,7 +241,7 @@ __global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
     sum += weight[i] * sL[i][qi];
   }
   const int64_t head = static_cast<int64_t>(s) * a.hq + h0 + qi;
-  if (a.splits > 1 && col == 0) a.stat[head * a.splits + split] = make_float2(top, sum);
+  if (a.shares.splits > 1 && col == 0) a.shares.stat[head * a.shares.splits + split] = make_float2(top, sum);
 #pragma unroll
   for (int i = 0; i < D / 128 + (D < 128); ++i) {
     const int at = 8 * (col + 16 * i);
@@ -252,8 +251,8 @@ __global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
     for (int n = 0; n < kStepWaves; ++n)
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] += weight[n] * sO[n][qi * kPitch + at + e];
-    if (a.splits > 1) {
-      float4* to = reinterpret_cast<float4*>(a.part + (head * a.splits + split) * d + at);
+    if (a.shares.splits > 1) {
+      float4* to = reinterpret_cast<float4*>(a.shares.part + (head * a.shares.splits + split) * d + at);
       to[0] = make_float4(y[0], y[1], y[2], y[3]);
       to[1] = make_float4(y[4], y[5], y[6], y[7]);
     } else {
@@ -264,35 +263,14 @@ __global__ __launch_bounds__(64 * kStepWaves) void step_share(StepArgs a) {
   }
 }
 
-// joins a head's shares: a wave a head, a lane's four values of each share
+template <bool FEW>
 __global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
-  const int lane = threadIdx.x & 63, d = a.pages.d;
-  const int64_t head = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (head >= heads) return;
-  const float2 st = lane < a.splits ? a.stat[head * a.splits + lane] : make_float2(-INFINITY, 0.0f);
-  const uint64_t some = __ballot(st.y != 0.0f);  // shares with keys
-  float top = st.y == 0.0f ? -INFINITY : st.x;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-  const float weight = st.y == 0.0f ? 0.0f : exp2_fast(st.x - (top == -INFINITY ? 0.0f : top));
-  const float sum = wave_sum(weight * st.y);
-  float y[4] = {};
-  const bool mine = 4 * lane < d;
-  const float* part = a.part + head * a.splits * d + 4 * lane;
-#pragma unroll 8
-  for (int i = 0; i < a.splits; ++i) {
-    const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), i));
-    if (!(some >> i & 1) || !mine) continue;
-    const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(i) * d);
-    y[0] += wi * v.x;
-    y[1] += wi * v.y;
-    y[2] += wi * v.z;
-    y[3] += wi * v.w;
-  }
-  if (!mine) return;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
-  *reinterpret_cast<uint2*>(a.o + head * d + 4 * lane) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+  const int lanes = FEW ? join_lanes(a.pages.d) : kWave;
+  const int64_t head = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / lanes;
+  if (FEW)
+    join_few(a.shares, head, head < heads, a.pages.d, a.o);
+  else if (head < heads)
+    join_many(a.shares, head, a.pages.d, a.o);
 }
 
 // Shares of a stream: as many as keep every CU's waves on loads, each at least
@@ -319,7 +297,7 @@ using namespace bllm;
 extern "C" size_t bllm_attention_step_workspace(int64_t nseq, int64_t hq, int64_t hkv, int64_t d, int64_t positions) {
   if (nseq < 1 || nseq > kMaxSeqs || heads_check(hq, hkv, d) != BLLM_OK || positions < 1) return 0;
   const int64_t splits = splits_of(nseq, hkv * ceil_div(hq / hkv, 16), positions);
-  return 16 + (splits > 1 ? static_cast<size_t>(nseq * hq * splits) * (sizeof(float) * d + sizeof(float2)) : 0);
+  return shares_bytes(nseq * hq, splits, d);
 }
 
 extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64_t hq, int64_t hkv, int64_t d,
@@ -353,10 +331,8 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   // a window alone bounds the positions that a query sees
   int64_t positions = cols * page;
   if (a.mask.window && !prefix && window + 2 * kTile < positions) positions = window + 2 * kTile;
-  a.splits = splits_of(nseq, hkv * a.blocks, positions);
-  a.stat = static_cast<float2*>(ws);
-  a.part = reinterpret_cast<float*>(a.stat + (nseq * hq * a.splits + 1) / 2 * 2);
-  const dim3 grid(static_cast<unsigned>(hkv * a.blocks * a.splits), static_cast<unsigned>(nseq));
+  a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions));
+  const dim3 grid(static_cast<unsigned>(hkv * a.blocks * a.shares.splits), static_cast<unsigned>(nseq));
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool q8 = pages_dtype == BLLM_I8;
   if (d <= 64)
@@ -365,7 +341,10 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
     q8 ? step_launch<128, true>(a, grid, st) : step_launch<128, false>(a, grid, st);
   else
     q8 ? step_launch<256, true>(a, grid, st) : step_launch<256, false>(a, grid, st);
-  if (a.splits > 1)
-    hipLaunchKernelGGL(step_join, dim3(static_cast<unsigned>(ceil_div(nseq * hq, 4))), dim3(256), 0, st, a, nseq * hq);
+  const int64_t heads = nseq * hq;
+  if (a.shares.splits > kFewSplits)
+    hipLaunchKernelGGL(step_join<false>, dim3(static_cast<unsigned>(ceil_div(heads, 4))), dim3(256), 0, st, a, heads);
+  else if (a.shares.splits > 1)
+    hipLaunchKernelGGL(step_join<true>, dim3(static_cast<unsigned>(ceil_div(heads * join_lanes(a.pages.d), 256))), dim3(256), 0, st, a, heads);
   return launch_status();
 }
