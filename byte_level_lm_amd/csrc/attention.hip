@@ -444,11 +444,15 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
   }
 }
 
-// Shares of a query's keys: where the workgroups of whole queries would leave
-// CUs without three of them, shares of 256 keys or more do (8 pieces of 64 to 512 queries
-// of 12 heads behind 4096 keys: SPLIT_OFF us whole, SPLIT_ON us in 3 shares).
+// Shares of a query's keys: where the workgroups of whole queries would not
+// fill the CUs a few times over, as many as do, of 512 keys or more in the mean.
+// The oldest workgroup of a CU runs first, so that those that start together end one by
+// one; more of them than find room keep the CUs busy (8 pieces of 64 to 512 queries of
+// 12 heads behind 4096 keys: 290 us whole, 148 in 3 shares, 137 in 5, 145 in 8).  Shares of 256
+// keys cost more in their starts and their join than they spread (2048 queries of
+// 12 heads, causal: 57 us, 44 in shares of 512).
 int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq) {
-  const int64_t units = (total / kRows + nseq) * hq, want = ceil_div(5 * 256, units), most = keys / 256;
+  const int64_t units = (total / kRows + nseq) * hq, want = ceil_div(5 * 256, units), most = keys / 512;
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kFewSplits ? kFewSplits : n);
 }
@@ -521,8 +525,8 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.hkv = static_cast<int>(hkv);
   a.group = static_cast<int>(hq / hkv);
   a.d = static_cast<int>(d);
-  // a window alone bounds the keys that a query sees, with the workgroup's others
-  int64_t keys = total_k / nseq;
+  // keys that a query sees in the mean; a window alone bounds them, with the workgroup's others
+  int64_t keys = total_k / nseq - (causal ? total / nseq / 2 : 0);
   if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
   a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq));
   hipStream_t st = static_cast<hipStream_t>(stream);

@@ -550,6 +550,7 @@ def gated_delta_step(q, k, v, g, beta, state, *, state_out=None, slots=None, sca
 
 
 # ------------------------------------------------------------------ attention in serving
+# The same holds as for the mixer block: the checks below are a few comparisons each.
 
 def attention_workspace(nseq: int, total: int, total_k: int, hq: int, hkv: int, d: int) -> int:
     return int(L.lib().bllm_attention_workspace(nseq, total, total_k, hq, hkv, d))
@@ -560,47 +561,48 @@ def attention_step_workspace(nseq: int, hq: int, hkv: int, d: int, positions: in
     return int(L.lib().bllm_attention_step_workspace(nseq, hq, hkv, d, positions))
 
 
-def _here(t, *more):
-    """The tensors live on the current device, whose current stream the call goes to."""
-    for x in (t, *more):
-        if x is not None and not x.is_cuda:
-            raise ValueError("tensors must live on the GPU")
+def _stream_of(*ts):
+    """The current stream, of the device that all the tensors live on."""
     dev = torch.cuda.current_device()
-    for x in (t, *more):
-        if x is not None and x.get_device() != dev:
-            raise ValueError(f"tensors must live on the current device, {dev}, not {x.get_device()}")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors must live on the GPU")
+            raise ValueError(f"tensors must live on the current device, {dev}, not {t.get_device()}")
+    return _stream() if _raw_stream is None else _raw_stream(dev)
 
 
 def _offsets(name, t, nseq=None):
-    if t.dtype != torch.int64 or t.dim() != 1 or t.numel() < 2 or (nseq is not None and t.numel() != nseq + 1):
+    if t.dtype != torch.int64 or t.dim() != 1 or t.shape[0] < 2 or (nseq is not None and t.shape[0] != nseq + 1):
         raise ValueError(f"{name} must be int64 [{'nseq' if nseq is None else nseq} + 1]")
     if not t.is_cuda or not t.is_contiguous():
         _dev(t)
 
 
 def _pages(k_pages, v_pages, table, k_scale, v_scale):
-    """(dtype, npages, page, hkv, d) of a paged cache."""
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    """(dtype, npages, page, hkv, d, nseq, cols) of a paged cache."""
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype != dtype:
         raise ValueError("k_pages and v_pages must be [npages, heads, page, d], of one shape and dtype")
     _dev(k_pages, v_pages)
-    npages, hkv, page, d = k_pages.shape
-    if k_pages.dtype == torch.int8:
+    if dtype == torch.int8:
         if k_scale is None or v_scale is None:
             raise ValueError("8-bit pages need k_scale and v_scale")
-        _is("k_scale", k_scale, k_pages.shape[:3], torch.float32)
-        _is("v_scale", v_scale, k_pages.shape[:3], torch.float32)
+        _is("k_scale", k_scale, shape[:3], torch.float32)
+        _is("v_scale", v_scale, shape[:3], torch.float32)
         dt = L.I8
-    elif k_pages.dtype == torch.bfloat16:
+    elif dtype == torch.bfloat16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale go with 8-bit pages")
         dt = L.BF16
     else:
-        raise TypeError(f"unsupported dtype of pages {k_pages.dtype}")
+        raise TypeError(f"unsupported dtype of pages {dtype}")
     if table.dim() != 2 or table.dtype != torch.int32:
         raise ValueError("table must be int32 [nseq, cols]")
     if not table.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    return dt, npages, page, hkv, d
+    npages, hkv, page, d = shape
+    return (dt, npages, page, hkv, d, *table.shape)
 
 
 def kv_write(k, v, k_pages, v_pages, table, *, offsets=None, start=None, k_scale=None, v_scale=None):
@@ -608,10 +610,10 @@ def kv_write(k, v, k_pages, v_pages, table, *, offsets=None, start=None, k_scale
     row i of sequence s to position start[s] + i, which is row p % page of page table[s, p // page].  offsets
     int64 [nseq + 1]; without them one row of each stream.  int8 pages take the rows in 8 bits with their scales
     fp32 [npages, heads, page].  Returns (k_pages, v_pages), written in place."""
-    dt, npages, page, hkv, d = _pages(k_pages, v_pages, table, k_scale, v_scale)
+    dt, npages, page, hkv, d, nseq, cols = _pages(k_pages, v_pages, table, k_scale, v_scale)
     if k.dim() != 3 or k.dtype != v.dtype:
         raise ValueError("k and v must be [total, heads, d] of one dtype")
-    total, (nseq, cols) = k.shape[0], table.shape
+    total = k.shape[0]
     ks, vs = _token_stride("k", k, total, hkv, d), _token_stride("v", v, total, hkv, d)
     if offsets is not None:
         _offsets("offsets", offsets, nseq)
@@ -619,10 +621,10 @@ def kv_write(k, v, k_pages, v_pages, table, *, offsets=None, start=None, k_scale
         raise ValueError(f"without offsets k and v have one row of each of the {nseq} streams")
     if start is not None:
         _is("start", start, (nseq,), torch.int32)
-    _here(k, v, k_pages, v_pages, table, k_scale, v_scale, offsets, start)
+    stream = _stream_of(k, v, k_pages, v_pages, table, k_scale, v_scale, offsets, start)
     rc = L.lib().bllm_kv_write(k.data_ptr(), v.data_ptr(), _dt(k), _ptr(offsets), nseq, total, hkv, d, ks, vs,
                                _ptr(start), table.data_ptr(), cols, dt, npages, page, k_pages.data_ptr(),
-                               v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), _stream())
+                               v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), stream)
     L.check("bllm_kv_write", rc)
     return k_pages, v_pages
 
@@ -631,18 +633,17 @@ def kv_read(k_pages, v_pages, table, offsets, total: int, *, start=None, k_scale
             v_out=None):
     """The positions start[s] .. of every sequence back as packed rows: returns (k, v), bf16 [total, heads, d], of
     which sequence s has rows offsets[s] .. offsets[s + 1] - 1.  Positions without a page are zeros."""
-    dt, npages, page, hkv, d = _pages(k_pages, v_pages, table, k_scale, v_scale)
-    nseq, cols = table.shape
+    dt, npages, page, hkv, d, nseq, cols = _pages(k_pages, v_pages, table, k_scale, v_scale)
     _offsets("offsets", offsets, nseq)
     if start is not None:
         _is("start", start, (nseq,), torch.int32)
     shape = (int(total), hkv, d)
     k_out = _out("k_out", k_out, shape, torch.bfloat16, k_pages)
     v_out = _out("v_out", v_out, shape, torch.bfloat16, k_pages)
-    _here(k_pages, v_pages, table, k_scale, v_scale, offsets, start, k_out, v_out)
+    stream = _stream_of(k_pages, v_pages, table, k_scale, v_scale, offsets, start, k_out, v_out)
     rc = L.lib().bllm_kv_read(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), dt, npages, page,
                               hkv, d, table.data_ptr(), cols, offsets.data_ptr(), nseq, shape[0], _ptr(start), L.BF16,
-                              k_out.data_ptr(), v_out.data_ptr(), _stream())
+                              k_out.data_ptr(), v_out.data_ptr(), stream)
     L.check("bllm_kv_read", rc)
     return k_out, v_out
 
@@ -687,11 +688,11 @@ def attention(q, k, v, offsets, *, k_offsets=None, scale=None, causal: bool = Tr
     window, cap = _mask_args(nseq, hq, window, cap, slopes, prefix)
     o_out = _out("o_out", o_out, (total, hq, d), q.dtype, q)
     w = _ws(attention_workspace(nseq, total, total_k, hq, hkv, d), ws, q.device)
-    _here(q, k, v, offsets, k_offsets, slopes, prefix, o_out, w)
+    stream = _stream_of(q, k, v, offsets, k_offsets, slopes, prefix, o_out, w)
     rc = L.lib().bllm_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), offsets.data_ptr(), _ptr(k_offsets),
                                 nseq, total, total_k, hq, hkv, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
                                 1 if causal else 0, window, cap, _ptr(slopes), _ptr(prefix), o_out.data_ptr(),
-                                w.data_ptr(), _nbytes(w), _stream())
+                                w.data_ptr(), _nbytes(w), stream)
     L.check("bllm_attention", rc)
     return o_out
 
@@ -701,20 +702,20 @@ def attention_step(q, k_pages, v_pages, table, lengths, *, k_scale=None, v_scale
     """Attention of one new token of each stream, q [nseq, hq, d], over the first lengths[s] (int32 [nseq]) positions
     of its pages, the new token's own among them.  Other arguments as ``attention`` and ``kv_write``.  Returns
     o [nseq, hq, d]."""
-    dt, npages, page, hkv, d = _pages(k_pages, v_pages, table, k_scale, v_scale)
+    dt, npages, page, hkv, d, nseq, cols = _pages(k_pages, v_pages, table, k_scale, v_scale)
     if q.dim() != 3:
         raise ValueError("q must be [nseq, heads, d]")
-    (nseq, cols), hq = table.shape, q.shape[1]
+    hq = q.shape[1]
     qs = _token_stride("q", q, nseq, hq, d)
     _is("lengths", lengths, (nseq,), torch.int32)
     window, cap = _mask_args(nseq, hq, window, cap, slopes, prefix)
     o_out = _out("o_out", o_out, (nseq, hq, d), q.dtype, q)
     w = _ws(attention_step_workspace(nseq, hq, hkv, d, cols * page), ws, q.device)
-    _here(q, k_pages, v_pages, table, lengths, k_scale, v_scale, slopes, prefix, o_out, w)
+    stream = _stream_of(q, k_pages, v_pages, table, lengths, k_scale, v_scale, slopes, prefix, o_out, w)
     rc = L.lib().bllm_attention_step(q.data_ptr(), _dt(q), nseq, hq, hkv, d, qs, k_pages.data_ptr(),
                                      v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), dt, npages, page,
                                      table.data_ptr(), cols, lengths.data_ptr(), d ** -0.5 if scale is None else scale,
                                      window, cap, _ptr(slopes), _ptr(prefix), o_out.data_ptr(), w.data_ptr(),
-                                     _nbytes(w), _stream())
+                                     _nbytes(w), stream)
     L.check("bllm_attention_step", rc)
     return o_out
