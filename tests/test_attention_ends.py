@@ -1,0 +1,163 @@
+"""The ends of the attention calls' ranges: the most streams, heads and workgroups, calls beside each other, the same
+call twice, workspaces of the size that the library names, and what a call may not touch."""
+import numpy as np
+import pytest
+
+import oracle
+from tests.helpers import say, to_dev, to_np
+from tests.test_gpu_attention import _bf16, _cache, _check, _dev16, _offsets, _strided, _table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def B():
+    import byte_level_lm_amd as B
+    B.lib()
+    return B
+
+
+def test_more_workgroups_than_one_launch_has_threads_for(B):
+    """65535 sequences of one token and 1024 heads: one key each, so that the output is its value."""
+    import torch
+    n, hq, d = 65535, 1024, 8
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(n, hq, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    kv = torch.randn(n, 2, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    say("attention of", n * hq, "workgroups")
+    o = B.attention(q, kv, kv, torch.arange(n + 1, device="cuda"))
+    assert torch.equal(o.view(n, 2, hq // 2, d), kv[:, :, None].expand(-1, -1, hq // 2, -1))
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_the_most_streams_take_a_step(B, q8):
+    import torch
+    n, h, d = 65535, 24, 16
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    shape = (n, h, 16, d)
+    pools = [torch.zeros(shape, device="cuda", dtype=torch.int8 if q8 else torch.bfloat16) for _ in range(2)]
+    sc = {x: torch.zeros(shape[:3], device="cuda") if q8 else None for x in ("k_scale", "v_scale")}
+    table = torch.randperm(n, device="cuda", generator=gen).to(torch.int32)[:, None].contiguous()
+    k = torch.randn(n, h, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    start = torch.randint(0, 16, (n,), device="cuda", generator=gen, dtype=torch.int32)
+    say("write and step of", n, "streams")
+    B.kv_write(k, k, *pools, table, start=start, **sc)
+    back, _ = B.kv_read(*pools, table, torch.arange(n + 1, device="cuda"), n, start=start, **sc)
+    assert q8 or torch.equal(back, k)
+    start.zero_()
+    B.kv_write(k, k, *pools, table, start=start, **sc)
+    o = B.attention_step(k, *pools, table, start + 1, **sc)
+    back, _ = B.kv_read(*pools, table, torch.arange(n + 1, device="cuda"), n, **sc)
+    # one key of weight 1: its value, whose two terms and rounding to bf16 are that of the row read back
+    assert torch.equal(o, back)
+
+
+@pytest.mark.parametrize("nseq", [63, 64, 65, 5000])
+def test_many_short_sequences(B, nseq):
+    rng = np.random.default_rng(nseq)
+    lengths = rng.integers(0, 4, nseq)
+    keys = lengths + rng.integers(0, 3, nseq) * rng.integers(0, 2, nseq)
+    off, koff, d = _offsets(lengths), _offsets(keys), 32
+    q, k, v = _bf16(rng, (int(off[-1]), 2, d)), _bf16(rng, (int(koff[-1]), 1, d)), _bf16(rng, (int(koff[-1]), 1, d))
+    want = oracle.attention(q, k, v, off, k_offsets=koff, sizes=True)
+    _check(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff)), want, 2.0 ** -8, d)
+    table, npages = _table(rng, keys, 16)
+    pools = [_dev16(np.zeros((npages, 1, 16, d), np.float32)) for _ in range(2)]
+    B.kv_write(_dev16(k), _dev16(v), *pools, to_dev(table), offsets=to_dev(koff))
+    for got, x in zip(B.kv_read(*pools, to_dev(table), to_dev(koff), int(koff[-1])), (k, v)):
+        assert np.array_equal(to_np(got), x)
+
+
+def test_the_same_call_gives_the_same_bits_and_calls_beside_each_other_too(B):
+    """Shares of a query's keys are joined in one order, whatever ends first."""
+    import torch
+    rng = np.random.default_rng(3)
+    lengths = [5000, 17, 3000]
+    pages, scales, table, dev, sc = _cache(rng, lengths, 2, 128, 64, True)
+    q, n, dtable = _dev16(_bf16(rng, (3, 6, 128))), to_dev(np.array(lengths, np.int32)), to_dev(table)
+    off, koff = to_dev(_offsets([40, 3, 90])), to_dev(_offsets([4000, 3, 2000]))
+    pq, pk, pv = (_dev16(_bf16(rng, (m, h, 128))) for m, h in ((133, 6), (6003, 2), (6003, 2)))
+
+    def both():
+        return (B.attention_step(q, *dev, dtable, n, **sc), B.attention(pq, pk, pv, off, k_offsets=koff))
+    first = both()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(both())
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, b) for o in outs for a, b in zip(o, first))
+
+
+@pytest.mark.parametrize("nseq,hq,hkv,d,positions", [(1, 12, 4, 128, 2048), (3, 5, 1, 40, 960), (300, 8, 8, 64, 64), (1, 1, 1, 8, 65536)])
+def test_calls_stay_inside_the_workspaces_whose_size_the_library_names(B, nseq, hq, hkv, d, positions):
+    import torch
+    rng = np.random.default_rng(d)
+    lengths = np.minimum(rng.integers(1, 400, nseq), positions)
+    page = 64
+    pages, scales, table, dev, sc = _cache(rng, lengths, hkv, d, page, False, cols=positions // page)
+    q = _bf16(rng, (nseq, hq, d))
+    size = B.attention_step_workspace(nseq, hq, hkv, d, positions)
+    buf = torch.full((size + 4096,), 77, device="cuda", dtype=torch.uint8)
+    o = B.attention_step(_dev16(q), *dev, to_dev(table), to_dev(lengths.astype(np.int32)), ws=buf[:size])
+    assert torch.all(buf[size:] == 77)
+    _check(o, oracle.attention_step(q, *pages, table, lengths, sizes=True), 2.0 ** -16, d)
+    if nseq > 3:
+        return
+    qlen = np.minimum(lengths, 30)
+    off, koff = _offsets(qlen), _offsets(lengths + positions // 2)
+    total, total_k = int(off[-1]), int(koff[-1])
+    q, k, v = _bf16(rng, (total, hq, d)), _bf16(rng, (total_k, hkv, d)), _bf16(rng, (total_k, hkv, d))
+    size = B.attention_workspace(nseq, total, total_k, hq, hkv, d)
+    buf = torch.full((size + 4096,), 77, device="cuda", dtype=torch.uint8)
+    o = B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff), ws=buf[:size])
+    assert torch.all(buf[size:] == 77)
+    _check(o, oracle.attention(q, k, v, off, k_offsets=koff, sizes=True), 2.0 ** -8, d)
+    with pytest.raises(ValueError, match="workspace"):
+        B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff), ws=buf[:size - 1])
+
+
+@pytest.mark.parametrize("lengths,keys", [([90], [6000]), ([2, 0, 33], [3000, 0, 5000])])
+@pytest.mark.parametrize("more", [{}, {"window": 700}, {"window": 600, "prefix": 1000}, {"causal": False}, {"cap": 3.0, "slopes": True}],
+                         ids=lambda m: "-".join(m) or "plain")
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_shares_of_long_keys(B, lengths, keys, more, d):
+    """Few queries behind many keys go in shares; some shares hold no key that a query sees."""
+    from tests.test_gpu_attention import _mask
+    rng = np.random.default_rng(sum(keys) + d)
+    off, koff = _offsets(lengths), _offsets(keys)
+    q = _bf16(rng, (int(off[-1]) + 3, 4, d), 1.5)
+    k, v = (_bf16(rng, (int(koff[-1]), 2, d)) for _ in range(2))
+    host, dev = _mask(more, rng, len(lengths), 4)
+    n = int(off[-1])
+    want = oracle.attention(q[:n], k, v, off, k_offsets=koff, sizes=True, **host)
+    import torch
+    out = torch.full((n + 3, 4, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    B.attention(_dev16(q), *_strided(k, v), to_dev(off), k_offsets=to_dev(koff), o_out=out, **dev)
+    assert torch.all(out[n:] == 7.0)  # behind the last sequence
+    _check(out[:n], want, 2.0 ** -8, d, host.get("slopes"), max(keys))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_that_are_not_seen_have_no_part_in_shares(B, d):
+    """As in one piece: v of a key behind the window, of another sequence, or of a later position is not finite."""
+    rng = np.random.default_rng(d + 1)
+    off, koff = _offsets([20, 9]), _offsets([5000, 3000])
+    q, k, v = _bf16(rng, (29, 2, d)), _bf16(rng, (8000, 1, d)), _bf16(rng, (8000, 1, d))
+    want = oracle.attention(q, k, v, off, k_offsets=koff, window=1500, sizes=True)
+    v2 = v.copy()
+    v2[100:3400] = np.inf     # in front of every query's window
+    v2[4999] = np.nan         # the last key of sequence 0: its last query sees it
+    v2[5000 + 2995, 0, 5] = -np.inf  # seen by the last five queries of sequence 1
+    o = to_np(B.attention(_dev16(q), _dev16(k), _dev16(v2), to_dev(off), k_offsets=to_dev(koff), window=1500)).astype(np.float64)
+    lost = np.zeros(o.shape, bool)
+    lost[19] = True
+    lost[24:29, :, 5] = True
+    assert not np.isfinite(o[lost]).any()
+    o[lost] = want[0][lost]
+    _check(to_dev(o), want, 2.0 ** -8, d)
