@@ -33,7 +33,8 @@ struct AttArgs {
   const int64_t *offsets, *k_offsets;
   uint16_t* o;
   int64_t total, total_k, q_stride, k_stride, v_stride;
-  int64_t first, units, slots;   // this launch's first unit of work, all of them, slots of a workgroup's queries
+  int64_t first;                 // this launch's first slot of a workgroup's queries
+  uint32_t slots, units;         // its slots and units of work
   int nseq, hq, hkv, group, d;
   Mask mask;
   Shares shares;
@@ -169,20 +170,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
 
   // Unit of work: kRun neighbours go to one XCD.  Units of a key head follow
   // each other, of these a sequence's, the last queries (with the most keys) first.
-  int64_t unit = a.first + blockIdx.x;
+  uint32_t unit = blockIdx.x;
   {
-    const int64_t full = a.units / (kRun * kXcds) * (kRun * kXcds);
+    const uint32_t full = a.units / (kRun * kXcds) * (kRun * kXcds);
     if (unit < full) {
-      const int64_t in = unit % (kRun * kXcds);
+      const uint32_t in = unit % (kRun * kXcds);
       unit += (in % kXcds) * kRun + in / kXcds - in;
     }
   }
   const int split = SPLIT ? static_cast<int>(unit % a.shares.splits) : 0;
   if (SPLIT) unit /= a.shares.splits;
-  const int64_t per = a.slots * a.group;
-  const int kh = static_cast<int>(unit / per);
-  const int64_t slot = unit % per / a.group;
-  const int h = kh * a.group + static_cast<int>(unit % a.group);
+  const uint32_t kh = unit / (a.slots * a.group), in_head = unit - kh * a.slots * a.group, in_slots = in_head / a.group;
+  const int64_t slot = a.first + in_slots;
+  const int h = static_cast<int>(kh * a.group + in_head - in_slots * a.group);
   int64_t t0, t1, k0, k1;
   const int s = find_rows(a, slot, &t0, &t1, &k0, &k1);
   const int n = static_cast<int>(t1 - t0), keys = static_cast<int>(k1 - k0);
@@ -468,15 +468,20 @@ void launch_as(const AttArgs& a, dim3 grid, hipStream_t st) {
 template <int D>
 void launch(AttArgs a, hipStream_t st) {
   constexpr int64_t kMost = (int64_t(1) << 32) / (64 * kWaves) - 1;  // workgroups that one launch has threads for
-  a.slots = a.total / kRows + a.nseq;  // sequence s has slots offsets[s] / kRows + s and on
-  a.units = a.slots * a.hq * a.shares.splits;
-  if (a.shares.splits > 1) {  // few units by the rule of splits_of
-    launch_as<D, true>(a, dim3(static_cast<unsigned>(a.units)), st);
-    hipLaunchKernelGGL(prompt_join, dim3(static_cast<unsigned>(ceil_div(a.total * a.hq * join_lanes(a.d), 64 * kWaves))), dim3(64 * kWaves), 0, st, a);
-    return;
+  const int64_t slots = a.total / kRows + a.nseq;  // sequence s has slots offsets[s] / kRows + s and on
+  const int64_t each = static_cast<int64_t>(a.hq) * a.shares.splits, most = kMost / each;
+  for (a.first = 0; a.first < slots; a.first += most) {
+    a.slots = static_cast<uint32_t>(slots - a.first < most ? slots - a.first : most);
+    a.units = static_cast<uint32_t>(a.slots * each);
+    if (a.shares.splits > 1)
+      launch_as<D, true>(a, dim3(a.units), st);
+    else
+      launch_as<D, false>(a, dim3(a.units), st);
   }
-  for (a.first = 0; a.first < a.units; a.first += kMost)
-    launch_as<D, false>(a, dim3(static_cast<unsigned>(a.units - a.first < kMost ? a.units - a.first : kMost)), st);
+  if (a.shares.splits > 1) {  // few queries, by the rule of splits_of
+    const int64_t threads = a.total * a.hq * join_lanes(a.d);
+    hipLaunchKernelGGL(prompt_join, dim3(static_cast<unsigned>(ceil_div(threads, 64 * kWaves))), dim3(64 * kWaves), 0, st, a);
+  }
 }
 
 }  // namespace
