@@ -237,6 +237,7 @@ inline int pages_check(const void* k_pages, const void* v_pages, const float* k_
 inline int mask_make(double scale, int causal, int64_t window, double cap, const float* slopes, const int32_t* prefix,
                      Mask* m) {
   if (scale != scale || window < 0 || !(cap >= 0.0 && cap <= 3.0e38)) return BLLM_E_INVAL;
+  if (cap != 0.0 && !(cap >= 0.0009765625 && cap <= 1024.0)) return BLLM_E_NOTSUP;  // capped() is off by 2^-22 cap
   // a window past every distance is none
   *m = Mask{static_cast<float>(scale), static_cast<float>(cap), slopes, prefix,
             static_cast<int>(window > kMaxTokens ? 0 : window), causal != 0};

@@ -2,10 +2,18 @@
 //
 //   s_ij = scale q_i.k_j (capped, lowered by distance),  o_i = sum_j 2^{x_ij - m_i} v_j / sum_j 2^{x_ij - m_i},  x = s log2 e
 //
-// Bound by the matrix cores, with the exponentials close behind: 32 keys cost a
-// wave 32 exponentials' issue beside 16 instructions of 32 x 32 x 16.  A
-// workgroup has 128 queries of a head, a wave 32 of them; tiles of BN keys go through LDS, two
-// buffers of them filled without registers, in one pass with the running maximum and sum.
+// A workgroup has 128 queries of a head, a wave 32 of them; tiles of 32 keys go
+// through LDS, two buffers of them filled without registers, in one pass with
+// the running maximum and sum.  With d = 128, 32 keys are 16 matrix instructions of
+// 32 x 32 x 16 (512 cycles) and 16 exponentials a lane with what they need (some 480) for a
+// wave, which three waves a SIMD run beside each other.  What bounds it then is the card's
+// power: 32 sequences of 2048 tokens, 12 heads on 4, causal: 445 us, 930 TFLOP/s, the
+// matrix cores busy 47 % of 859 thousand cycles at 1.85 GHz (the same instructions with less to
+// move, without the loads, run at 2.3).  With d = 64 the vector instructions do: window of 512
+// over 16 ragged sequences of up to 8192 bytes, 8 heads, 117 us, 600 TFLOP/s.  Tried and
+// no faster: 256 queries a workgroup, 64 a wave (registers of one wave a SIMD), tiles of
+// 64 keys, the next tile's first product between this one's exponentials, the sum by
+// a matrix instruction (480 us), priorities.
 //
 // Registers: scores come as S^T = K Q^T, of which a lane (half h of the wave)
 // has its query lane % 32 and keys 8 (r / 4) + 4 h + r % 4 of each 32.  The second product
@@ -117,8 +125,7 @@ __device__ inline int find_rows(const AttArgs& a, int64_t slot, int64_t* t0, int
 // A query on its own, where v has values that are not finite: products with a
 // weight of zero would carry them to queries that do not see their keys.  A
 // wave takes 64 keys at a time, a lane a key, then a lane four columns of v.
-__device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t k0, int t, Sight see,
-                                                      float slope) {
+__device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t k0, int t, Sight see, float slope) {
   const int lane = lane_id(), kh = h / a.group, d = a.d;
   const uint16_t* q = a.q + row * a.q_stride + static_cast<int64_t>(h) * d;
   float m = -INFINITY, l = 0.0f, o[4] = {};
@@ -150,9 +157,10 @@ __device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t
         for (int e = 0; e < 4; ++e) o[e] = fmaf(w, bf16_to_f32(v[e]), o[e]);
     }
   }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   if (4 * lane < d)
     *reinterpret_cast<uint2*>(a.o + (row * a.hq + h) * d + 4 * lane) =
-        make_uint2(pack2(o[0] / l, o[1] / l), pack2(o[2] / l, o[3] / l));
+        make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
 }
 
 // GEN: with a cap or slopes.  SPLIT: a share of the tiles, to be joined.
@@ -212,17 +220,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   const int whole0 = uniform(w1.lo <= front ? 0 : w1.lo), whole1 = uniform(max(w0.hi + 1, w1.lo <= front ? front : 0) - BN);
   const int seen0 = uniform(some ? front : 0), seen1 = uniform(w0.lo - BN + 1), seen2 = uniform(some ? w1.hi : -1);
 
-  // queries: 8 values of each 16, negated for a negative scale, so that the largest product has the largest score
-  bf16x8 fq[NS];
-  {
-    const uint16_t* q = a.q + (t0 + i0 + qi) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
-    const uint32_t sign = a.mask.scale < 0.0f ? 0x80008000u : 0u;
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const uint4 z = i0 + qi < n && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
-      fq[i] = as_frag(make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign));
-    }
-  }
+  bf16x8 fq[NS];                                         // queries: 8 values of each 16
   const int t = p0 + qi;
   const Sight see = sight(a.mask, t, keys, front);
   // x = c1 times the product; with GEN the product becomes x itself
@@ -242,7 +240,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   const int kbytes = static_cast<int>(2 * a.k_stride), vbytes = static_cast<int>(2 * a.v_stride);
   const char* kb = reinterpret_cast<const char*>(a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * a.d);
   const char* vb = reinterpret_cast<const char*>(a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * a.d);
-  // rows past the end read as zero (behind the last tile too, of which then nothing is read)
+  // rows past the end read as zero
   const auto load = [&](const char* from, int rows, int bytes, const uint32_t (&at)[U], uint16_t* to) __attribute__((always_inline)) {
     const Buffer b = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(from), 0, rows * bytes, 0x00027000);
 #pragma unroll
@@ -291,7 +289,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int j = 8 * (r / 4) + r % 4;
-          x[r] = ((j >= lo) & (j <= hi)) | (j < ahead) ? x[r] : -INFINITY;
+          x[r] = (((j >= lo) & (j <= hi)) | (j < ahead)) ? x[r] : -INFINITY;
         }
       } else {  // one edge or both
         if (j0 + BN - 1 > w0.hi) {
@@ -344,7 +342,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   int j1 = begin * BN < ahead ? begin * BN : from + begin * BN - ahead;
   const char *kj = kb + static_cast<int64_t>(j1) * kbytes, *vj = vb + static_cast<int64_t>(j1) * vbytes;
   const auto load_next = [&](uint16_t* K, uint16_t* V) __attribute__((always_inline)) {
-    const int rows = max(uniform(min(keys - j1, BN)), 0);
+    const int rows = min(keys - j1, BN);
     load(kj, rows, kbytes, ko, K);
     load(vj, rows, vbytes, vo, V);
     int by = BN;
@@ -354,12 +352,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
     vj += static_cast<int64_t>(by) * vbytes;
   };
   int j2 = j1;  // the tile that the products are at
-  // one tile, with the next one's loads on their way
-  const auto step = [&](uint16_t* nK, uint16_t* nV, const uint16_t* cK, const uint16_t* cV) __attribute__((always_inline)) {
+  // one tile, with the loads of the next, if there is one, on their way
+  const auto step = [&](bool more, uint16_t* nK, uint16_t* nV, const uint16_t* cK, const uint16_t* cV) __attribute__((always_inline)) {
     const int j0 = j2;
     j2 = j1;
     landed_barrier();
-    load_next(nK, nV);
+    if (more) load_next(nK, nV);
     if (sees(j0)) {
       floatx16 x;
       uint32_t p[8];
@@ -370,9 +368,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
     }
   };
   if (tiles > 0) load_next(sK0, sV0);
+  // the queries behind them, negated for a negative scale, so that the largest product has the largest score
+  {
+    const uint16_t* q = a.q + (t0 + i0 + qi) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
+    const uint32_t sign = a.mask.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const uint4 z = i0 + qi < n && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
+      fq[i] = as_frag(make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign));
+    }
+  }
   for (int i = 0; i < tiles; i += 2) {
-    step(sK1, sV1, sK0, sV0);
-    if (i + 1 < tiles) step(sK0, sV0, sK1, sV1);
+    step(i + 1 < tiles, sK1, sV1, sK0, sV0);
+    if (i + 1 < tiles) step(i + 2 < tiles, sK0, sV0, sK1, sV1);
   }
   if (!some) return;
 
@@ -503,12 +511,12 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
                               double scale, int causal, int64_t window, double cap, const float* slopes,
                               const int32_t* prefix, void* o_out, void* ws, size_t ws_bytes, void* stream) {
   AttArgs a{};
-  const int rc = heads_check(hq, hkv, d);
-  if (rc == BLLM_E_INVAL || nseq < 1 || total < 0 || total_k < 0 || !offsets || (!k_offsets && total != total_k) ||
+  const int rc = heads_check(hq, hkv, d), mc = mask_make(scale, causal, window, cap, slopes, prefix, &a.mask);
+  if (rc == BLLM_E_INVAL || mc == BLLM_E_INVAL || nseq < 1 || total < 0 || total_k < 0 || !offsets || (!k_offsets && total != total_k) ||
       (total > 0 && (!q || !o_out)) || (total_k > 0 && (!k || !v)) || q_stride < hq * d || k_stride < hkv * d ||
-      v_stride < hkv * d || mask_make(scale, causal, window, cap, slopes, prefix, &a.mask) != BLLM_OK)
+      v_stride < hkv * d)
     return BLLM_E_INVAL;
-  if (rc != BLLM_OK || dtype != BLLM_BF16 || nseq > kMaxSeqs || total > kMaxTokens || total_k > kMaxTokens ||
+  if (rc != BLLM_OK || mc != BLLM_OK || dtype != BLLM_BF16 || nseq > kMaxSeqs || total > kMaxTokens || total_k > kMaxTokens ||
       !stride_ok(q_stride) || !stride_ok(k_stride) || !stride_ok(v_stride) || !aligned16(q) || !aligned16(k) ||
       !aligned16(v) || !aligned16(o_out) || !aligned16(ws))
     return BLLM_E_NOTSUP;

@@ -308,13 +308,12 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
                                    void* ws, size_t ws_bytes, void* stream) {
   StepArgs a{};
   const int rc = heads_check(hq, hkv, d);
-  if (rc == BLLM_E_INVAL || !q || !lengths || !o_out || q_stride < hq * d ||
-      mask_make(scale, 1, window, cap, slopes, prefix, &a.mask) != BLLM_OK)
-    return BLLM_E_INVAL;
+  const int mc = mask_make(scale, 1, window, cap, slopes, prefix, &a.mask);
+  if (rc == BLLM_E_INVAL || mc == BLLM_E_INVAL || !q || !lengths || !o_out || q_stride < hq * d) return BLLM_E_INVAL;
   const int pc = pages_check(k_pages, v_pages, k_scale, v_scale, pages_dtype, npages, page, hkv, d, table, cols, nseq,
                              &a.pages);
   if (pc != BLLM_OK) return pc;
-  if (rc != BLLM_OK || dtype != BLLM_BF16 || !stride_ok(q_stride) || !aligned16(q) || !aligned16(o_out) || !aligned16(ws))
+  if (rc != BLLM_OK || mc != BLLM_OK || dtype != BLLM_BF16 || !stride_ok(q_stride) || !aligned16(q) || !aligned16(o_out) || !aligned16(ws))
     return BLLM_E_NOTSUP;
   if (!ws || ws_bytes < bllm_attention_step_workspace(nseq, hq, hkv, d, cols * page)) return BLLM_E_WS;
   a.q = static_cast<const uint16_t*>(q);

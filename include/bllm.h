@@ -580,6 +580,7 @@ int bllm_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
  * k_offsets: int64 [nseq+1] device, of the keys and values, or NULL: the
  *            queries' (then total_k = total).
  * prefix   : int32 [nseq] device or NULL;  slopes : fp32 [hq] device or NULL.
+ * cap      : 0 (none) or 2^-10 .. 1024; capped scores are off by 2^-22 cap.
  * o_out    : bf16 [total x hq x d], dense.
  * ws       : bllm_attention_workspace(nseq, total, total_k, hq, hkv, d) bytes.
  * Numbers  : products of bf16 values, sums, maxima and the softmax's sum in
@@ -591,7 +592,7 @@ int bllm_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
  *            multiple of hkv, strides shorter than the heads, NaN scale, window
  *            below 0, cap below 0 or not finite, total_k other than total without
  *            k_offsets; BLLM_E_NOTSUP outside the limits above or off 16
- *            bytes; BLLM_E_WS.
+ *            bytes, other caps; BLLM_E_WS.
  */
 size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t total_k, int64_t hq, int64_t hkv, int64_t d);
 int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,

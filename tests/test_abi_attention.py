@@ -60,7 +60,7 @@ def test_attention_refusals(L):
         assert att(**bad) == -1, bad
     for bad in (dict(dt=0), dict(dt=2), dict(d=60), dict(d=264, qs=2048, ks=1024, vs=1024), dict(qs=260), dict(ks=1 << 22),
                 dict(q=ODD), dict(k=ODD), dict(v=ODD), dict(o=ODD), dict(nseq=65536), dict(total=(1 << 30) + 1),
-                dict(total_k=(1 << 30) + 1), dict(hq=2048, hkv=2, qs=1 << 20)):
+                dict(total_k=(1 << 30) + 1), dict(hq=2048, hkv=2, qs=1 << 20), dict(cap=1025.0), dict(cap=1e-4), dict(ws=ODD)):
         assert att(**bad) == -2, bad
     assert att(ws=None) == att(wsb=8) == -3
     assert att(total=0, q=None, o=None) == 0
@@ -77,7 +77,7 @@ def test_step_refusals(L):
                 dict(cap=-2.0), dict(cols=0)):
         assert step(**bad) == -1, bad
     for bad in (dict(dt=0), dict(d=60), dict(page=17), dict(pdt=0), dict(q=ODD), dict(o=ODD), dict(kp=ODD), dict(qs=1 << 22),
-                dict(nseq=65536), dict(cols=1 << 26), dict(hq=2048, qs=1 << 18)):
+                dict(nseq=65536), dict(cols=1 << 26), dict(hq=2048, qs=1 << 18), dict(cap=2000.0), dict(ws=ODD)):
         assert step(**bad) == -2, bad
     assert step(ws=None) == step(wsb=8) == -3
     assert L.bllm_attention_step_workspace(0, 4, 2, 64, 256) == 0 and L.bllm_attention_step_workspace(2, 4, 2, 64, 256) > 0

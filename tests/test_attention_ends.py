@@ -161,3 +161,28 @@ def test_keys_that_are_not_seen_have_no_part_in_shares(B, d):
     assert not np.isfinite(o[lost]).any()
     o[lost] = want[0][lost]
     _check(to_dev(o), want, 2.0 ** -8, d)
+
+
+@pytest.mark.parametrize("keys", [3, 700, 3000])
+def test_queries_without_keys_beside_values_that_are_not_finite(B, keys):
+    """More queries than keys: the first see none and get zeros, whatever the others' keys hold."""
+    rng = np.random.default_rng(keys)
+    n, d = keys + 45, 64
+    off, koff = _offsets([n]), _offsets([keys])
+    q, k, v = _bf16(rng, (n, 1, d)), _bf16(rng, (keys, 1, d)), _bf16(rng, (keys, 1, d))
+    v[0] = np.nan
+    for window in (None, 2):
+        o = to_np(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff), window=window))
+        assert not o[:45].any() and np.isnan(o[45]).all()
+        assert window is None or np.isfinite(o[45 + window:]).all()
+
+
+def test_keys_without_weight_and_one_key_alone(B):
+    """One key: its value bit for bit, whatever the score. Far scores: the others' weights vanish."""
+    rng = np.random.default_rng(77)
+    for d in (8, 64, 128, 256):
+        q, k, v = _bf16(rng, (90, 3, d), 30.0), _bf16(rng, (90, 1, d), 30.0), _bf16(rng, (90, 1, d))
+        o = B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(_offsets([90])), window=1)
+        assert np.array_equal(to_np(o), np.repeat(v, 3, axis=1))
+        want = oracle.attention(q, k, v, _offsets([90]), scale=1.0, sizes=True)  # scores of some 900 sqrt(d)
+        _check(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(_offsets([90])), scale=1.0), want, 2.0 ** -8, d)
