@@ -28,7 +28,6 @@ FILE_FLAGS = {
     # MFMA results in plain registers: with one workgroup a CU the compiler would
     # keep the scan's accumulators in AGPRs and copy them for every VALU use
     "delta.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
-    "attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
 }
 
 

@@ -129,7 +129,8 @@ __host__ __device__ inline int join_lanes(int d) { return d <= 32 ? 8 : d <= 64 
 
 // Joins a query's shares.  Up to kFewSplits of them: join_lanes(d) lanes of a wave, with all
 // their loads in flight at once (beside those of the wave's other queries); more: a wave, whose
-// groups of lanes take the shares in turn.  True where scores were finite and an output is not.
+// groups of lanes take the shares in turn (61 streams of 5 shares, 8 heads of 64: 18.4 us the
+// first way, 19.9 the second; 64 shares have no registers for the first).  True where scores were finite and an output is not.
 constexpr int kFewSplits = 8;
 
 __device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int d, uint16_t* o) {

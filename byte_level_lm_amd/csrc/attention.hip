@@ -13,7 +13,8 @@
 // over 16 ragged sequences of up to 8192 bytes, 8 heads, 117 us, 600 TFLOP/s.  Tried and
 // no faster: 256 queries a workgroup, 64 a wave (registers of one wave a SIMD), tiles of
 // 64 keys, the next tile's first product between this one's exponentials, the sum by
-// a matrix instruction (480 us), priorities.
+// a matrix instruction (480 us), priorities, loads two tiles ahead in three buffers (461 us; without
+// any loads 342, so that what they cost is the way into LDS, not its latency).
 //
 // Registers: scores come as S^T = K Q^T, of which a lane (half h of the wave)
 // has its query lane % 32 and keys 8 (r / 4) + 4 h + r % 4 of each 32.  The second product
@@ -32,9 +33,13 @@ typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr int kWaves = 4, kRows = 32 * kWaves;  // queries of a workgroup
 constexpr int BN = 32;           // keys of a tile
 constexpr int kXcds = 8;
-constexpr int kRun = 64;         // neighbouring workgroups that one XCD takes in a row
+// Neighbouring workgroups that one XCD takes in a row, so that they share its L2: window of 512 117 us
+// (in order of the grid 124), 32 x 2048 chunks 445 (452); in runs of 256 an XCD ends late (16 x 2048, d 256: 423 us, 384).
+constexpr int kRun = 64;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset past every buffer: reads as zero
-constexpr float kSlack = 8.0f;   // how far (log2) scores may pass the maximum that weights are taken against
+// How far (log2) scores may pass the maximum that weights are taken against: weights up to 256
+// lose nothing, and O is scaled anew seldom (32 x 2048 chunks 445 us, 495 with 0).
+constexpr float kSlack = 8.0f;
 
 struct AttArgs {
   const uint16_t *q, *k, *v;
@@ -163,7 +168,8 @@ __device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t
         make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
 }
 
-// GEN: with a cap or slopes.  SPLIT: a share of the tiles, to be joined.
+// GEN: with a cap or slopes (their branches alone: 32 x 2048 chunks 469 us, 445 without).  SPLIT: a
+// share of the tiles, to be joined.  Three workgroups a CU with d = 128 take 458 us, two 500; a fourth has no registers.
 template <int D, bool GEN, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void prompt_tiles(AttArgs a) {
   constexpr int NS = D / 16;               // steps of the first product

@@ -2,7 +2,10 @@
 //
 //   s_j = scale q.k_j (capped, lowered by distance),  o = sum_j 2^{x_j - m} v_j / sum_j 2^{x_j - m},  x = s log2 e
 //
-// Bound by the cache's bytes, each read once.  The keys that a stream sees are
+// Bound by the cache's bytes, each read once: 8 streams of 65536 positions, 12 heads on 4 of
+// 128, bf16: 180 us and 6 for the join, 5.8 TB/s; 256 streams of 256 to 2048 positions in
+// 8 bits: 67 us, 4.9 TB/s (codes to bf16 by vector instructions, 35 % of their cycles); one
+// stream of 2048: 5.4 us and 3.4.  The keys that a stream sees are
 // cut into `splits` equal shares, each a workgroup of up to 16 query heads of one key
 // head; its four waves take tiles of 32 keys in turn, straight from memory
 // into the matrix instructions' registers, with a running maximum and sum of
@@ -52,9 +55,12 @@ struct Seen {
   __device__ inline bool all(int j) const { return (j + kTile <= front) | ((j >= lo) & (j + kTile <= n)); }
 };
 
-// GEN: with a cap or slopes
+// GEN: with a cap or slopes.  The workgroups of a CU that registers are kept for: the most
+// that spill nothing in the loop.  bf16: 4 of them spill (8 x 65536 positions 200 us, with 3
+// 189), 2 have too few loads on their way (61 streams with a window of 512 21 us, 18); 8 bits: 256 streams
+// 69 us with 4, 76 with 3; d > 128 has room for 2 in LDS (8 bits, 8 x 32768: 107 us, 123 with the registers of one).
 template <int D, bool Q8, bool GEN>
-__global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 1 : Q8 ? 4 : 3) void step_share(StepArgs a) {
+__global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void step_share(StepArgs a) {
   constexpr int VP = D / 16;               // values of a row that a lane has of V
   constexpr int VW = Q8 ? VP / 4 : VP / 2; // their 32-bit words
   constexpr int KP = Q8 ? D / 64 : D / 32; // 16-byte pieces of a row that a lane has of K
@@ -184,7 +190,8 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 1 : Q8 ? 4 : 3) void ste
       for (int n = 0; n < VP; ++n) o[n] *= fall;
     }
     const float base = m == -INFINITY ? 0.0f : m;
-    // weights in two bf16 terms: 16 bits, at an instruction that the loads leave time for
+    // weights in two bf16 terms, 16 bits: the second costs no time where the bytes bound (256 streams
+    // of 8-bit pages 68 us, 67 with one) and 47 us instead of 44 where rows are the shortest (64 streams, d 64, 8 bits)
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -263,6 +270,7 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 1 : Q8 ? 4 : 3) void ste
   }
 }
 
+// FEW: up to kFewSplits shares
 template <bool FEW>
 __global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
   const int lanes = FEW ? join_lanes(a.pages.d) : kWave;
@@ -273,10 +281,14 @@ __global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
     join_many(a.shares, head, a.pages.d, a.o);
 }
 
-// Shares of a stream: as many as keep every CU's waves on loads, each at least
-// a tile a wave.
-int splits_of(int64_t nseq, int64_t heads, int64_t positions) {
-  const int64_t most = ceil_div(positions, kTile * kStepWaves), want = ceil_div(1024, nseq * heads);
+// Shares of a stream, each at least a tile a wave: as many as give a workgroup to each
+// place for one (LDS has room for 8, 4 or 2 of them a CU).  8 streams of 65536 positions, d 128:
+// 970 us whole, 189 in these 32 shares, 188 in 16, 192 in 64.  8 of 32768, d 256, 8 bits: 626 whole,
+// 107 in 16, 110 in 32.  64 streams of 4096 to 16384, d 64, 8 bits, 2 heads, whose longest ones
+// end last: 196 whole, 47 in 16, 49 in 8.
+int splits_of(int64_t nseq, int64_t heads, int64_t positions, int64_t d) {
+  const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 4 : 8);
+  const int64_t most = ceil_div(positions, kTile * kStepWaves), want = ceil_div(places, nseq * heads);
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
@@ -296,7 +308,7 @@ using namespace bllm;
 
 extern "C" size_t bllm_attention_step_workspace(int64_t nseq, int64_t hq, int64_t hkv, int64_t d, int64_t positions) {
   if (nseq < 1 || nseq > kMaxSeqs || heads_check(hq, hkv, d) != BLLM_OK || positions < 1) return 0;
-  const int64_t splits = splits_of(nseq, hkv * ceil_div(hq / hkv, 16), positions);
+  const int64_t splits = splits_of(nseq, hkv * ceil_div(hq / hkv, 16), positions, d);
   return shares_bytes(nseq * hq, splits, d);
 }
 
@@ -330,7 +342,7 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   // a window alone bounds the positions that a query sees
   int64_t positions = cols * page;
   if (a.mask.window && !prefix && window + 2 * kTile < positions) positions = window + 2 * kTile;
-  a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions));
+  a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions, d));
   const dim3 grid(static_cast<unsigned>(hkv * a.blocks * a.shares.splits), static_cast<unsigned>(nseq));
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool q8 = pages_dtype == BLLM_I8;

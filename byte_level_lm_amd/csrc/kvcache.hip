@@ -3,7 +3,8 @@
 //   a = max |x|,  code = rne(x * (127 * (1 / a))),  scale = a / 127
 // (the arithmetic of the rows of norm.hip).
 //
-// Bound by the bytes.  A group of G lanes has a row, one 16-byte piece of bf16
+// Bound by the bytes: 65536 tokens of 4 heads of 128 in bf16 45 us (6.0 TB/s) written, 44 read; in
+// 8 bits 44 (4.6 TB/s, the vector instructions of the codes for 3/4 of it) and 37 (5.6).  A group of G lanes has a row, one 16-byte piece of bf16
 // a lane; a workgroup finds the places of its tokens once, then moves all
 // their rows, several loads a lane in flight.
 #include "attention.h"
@@ -13,7 +14,7 @@ namespace {
 
 constexpr float kTiny = 1e-30f;  // a row whose largest value is below this becomes zeros with scale 0
 constexpr int kThreads = 256;
-constexpr int kFlight = 4;       // rows a lane has in flight
+constexpr int kFlight = 4;       // rows a lane has in flight (131072 8-bit rows read: 2 take 111 us, 4 94, 8 106)
 constexpr int kMaxTile = 64;     // tokens of a workgroup
 
 struct KvArgs {
@@ -151,7 +152,8 @@ __global__ __launch_bounds__(kThreads) void kv_move(KvArgs a) {
 template <bool WRITE, bool Q8>
 void launch_as(KvArgs a, hipStream_t st) {
   const int pieces = a.pages.d / 8, g = pieces <= 8 ? 8 : pieces <= 16 ? 16 : 32;
-  // tokens of a workgroup: two rounds of its loads, less where that leaves CUs idle
+  // tokens of a workgroup: two rounds of its loads (131072 tokens of 8-bit rows read: 95 us, one round
+  // 96, four 100), less where that leaves CUs idle (32 tokens written: 3.5 us alone, 4.7 without this)
   const int64_t round = kFlight * (kThreads / g);
   int64_t tile = 2 * round / (2 * a.pages.hkv);
   const int64_t spread = a.total / 1024;
