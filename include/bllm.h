@@ -526,6 +526,7 @@ int bllm_gated_delta_step(const void* q, const void* k, const void* v, const flo
  *         with 8-bit pages) up to 256; page 16, 32, 64, 128 or 256; cols * page,
  *         total and total_k at most 2^30; hq, hkv at most 1024, nseq at most 65535;
  *         token strides multiples of 8, below 2^22; npages below 2^31.
+ * What a call writes (pages, outputs, its workspace) overlaps no other argument.
  */
 
 /*
