@@ -30,7 +30,7 @@ typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t Buffer;
 
-constexpr int kWaves = 4, kRows = 32 * kWaves;  // queries of a workgroup
+constexpr int kWaves = 4, kRows = 32 * kWaves;  // rows of a workgroup
 constexpr int BN = 32;           // keys of a tile
 constexpr int kXcds = 8;
 // Neighbouring workgroups that one XCD takes in a row, so that they share its L2: window of 512 117 us
@@ -46,8 +46,10 @@ struct AttArgs {
   const int64_t *offsets, *k_offsets;
   uint16_t* o;
   int64_t total, total_k, q_stride, k_stride, v_stride;
-  int64_t first;                 // this launch's first slot of a workgroup's queries
+  int64_t first;                 // this launch's first slot of a workgroup's rows
   uint32_t slots, units;         // its slots and units of work
+  double inv_group;              // 1 / group
+  uint32_t small_inv;            // 2^21 / group, rounded up
   int nseq, hq, hkv, group, d;
   Mask mask;
   Shares shares;
@@ -113,7 +115,7 @@ __device__ inline int find_rows(const AttArgs& a, int64_t slot, int64_t* t0, int
   if (a.nseq < kWave) {
     const int i = min(lane_id(), a.nseq);
     const int64_t off = cut(a.offsets[i], a.total), k_off = cut(a.k_offsets[i], a.total_k);
-    const uint64_t before = __ballot(lane_id() < a.nseq && off / kRows + i <= slot);
+    const uint64_t before = __ballot(lane_id() < a.nseq && off * a.group / kRows + i <= slot);
     const int s = max(static_cast<int>(__popcll(before)) - 1, 0);
     *t0 = lane_value(off, s);
     *t1 = max(lane_value(off, s + 1), *t0);
@@ -121,7 +123,7 @@ __device__ inline int find_rows(const AttArgs& a, int64_t slot, int64_t* t0, int
     *k1 = max(lane_value(k_off, s + 1), *k0);
     return s;
   }
-  const int s = uniform(wave_find(a.nseq, slot, [&](int i) { return cut(a.offsets[i], a.total) / kRows + i; }));
+  const int s = uniform(wave_find(a.nseq, slot, [&](int i) { return cut(a.offsets[i], a.total) * a.group / kRows + i; }));
   seq_rows(a.offsets, s, a.total, t0, t1);
   seq_rows(a.k_offsets, s, a.total_k, k0, k1);
   return s;
@@ -194,20 +196,27 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   }
   const int split = SPLIT ? static_cast<int>(unit % a.shares.splits) : 0;
   if (SPLIT) unit /= a.shares.splits;
-  const uint32_t kh = unit / (a.slots * a.group), in_head = unit - kh * a.slots * a.group, in_slots = in_head / a.group;
-  const int64_t slot = a.first + in_slots;
-  const int h = static_cast<int>(kh * a.group + in_head - in_slots * a.group);
+  const uint32_t kh = unit / a.slots;
+  const int64_t slot = a.first + (unit - kh * a.slots);
   int64_t t0, t1, k0, k1;
   const int s = find_rows(a, slot, &t0, &t1, &k0, &k1);
   const int n = static_cast<int>(t1 - t0), keys = static_cast<int>(k1 - k0);
-  const int back = static_cast<int>(slot - (t0 / kRows + s)), blocks = (n + kRows - 1) / kRows;
+  // the sequence's rows: a query's heads of this key head, then the next query's
+  const int64_t rows = static_cast<int64_t>(n) * a.group;
+  const int64_t back = slot - (t0 * a.group / kRows + s), blocks = (rows + kRows - 1) / kRows;
   if (back < 0 || back >= blocks) return;
-  const int first = (blocks - 1 - back) * kRows;
+  const int64_t first = (blocks - 1 - back) * kRows;     // below 2^40: the product below is off by less than half of 1 / group
+  const int left = static_cast<int>(min(rows - first, int64_t(kRows)));
+  const int query0 = uniform(static_cast<int>((static_cast<double>(first) + 0.5) * a.inv_group));
+  const int rest = static_cast<int>(first - static_cast<int64_t>(query0) * a.group);
+  // query and head of row r, 0 .. kRows - 1 (rest + r < 2^11, so that the product's error stays below 1 / group)
+  const auto query_of = [&](int r) { return query0 + static_cast<int>((static_cast<uint32_t>(rest + r) * a.small_inv) >> 21); };
+  const auto head_of = [&](int r, int query) { return static_cast<int>(kh) * a.group + rest + r - (query - query0) * a.group; };
   const int shift = keys - n;                            // position of query 0
   const int front = a.mask.prefix ? uniform(min(max(a.mask.prefix[s], 0), keys)) : 0;
 
   // the keys that some query of the workgroup sees, in tiles: from 0 to `ahead`, then from `from` to `to`
-  const Sight low = sight(a.mask, first + shift, keys, front), high = sight(a.mask, min(first + kRows, n) - 1 + shift, keys, front);
+  const Sight low = sight(a.mask, query0 + shift, keys, front), high = sight(a.mask, query_of(left - 1) + shift, keys, front);
   int from = max(low.lo, 0) / BN * BN, ahead = (front + BN - 1) / BN * BN;
   const int to = max(high.hi + 1, front);
   if (ahead >= from) from = ahead;
@@ -218,21 +227,22 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
     begin = split * share;
     tiles = max(min(share, tiles - begin), 0);
   }
-  // the wave's own queries
-  const int i0 = first + 32 * w, p0 = i0 + shift, p1 = min(i0 + 32, n) - 1 + shift;
-  const bool some = i0 < n;
+  // the wave's own rows, and the lane's
+  const int r0 = 32 * w, p0 = query_of(r0) + shift, p1 = query_of(min(r0 + 32, left) - 1) + shift;
+  const int query = query_of(r0 + qi), h = head_of(r0 + qi, query);
+  const bool some = r0 < left, mine = r0 + qi < left;
   const Sight w0 = sight(a.mask, p0, keys, front), w1 = sight(a.mask, p1, keys, front);
   // tiles that every query of the wave sees whole (at least these), and tiles of which some query sees a key
   const int whole0 = uniform(w1.lo <= front ? 0 : w1.lo), whole1 = uniform(max(w0.hi + 1, w1.lo <= front ? front : 0) - BN);
   const int seen0 = uniform(some ? front : 0), seen1 = uniform(w0.lo - BN + 1), seen2 = uniform(some ? w1.hi : -1);
 
   bf16x8 fq[NS];                                         // queries: 8 values of each 16
-  const int t = p0 + qi;
+  const int t = query + shift;
   const Sight see = sight(a.mask, t, keys, front);
   // x = c1 times the product; with GEN the product becomes x itself
   const float size = fabsf(a.mask.scale), c1 = GEN ? 1.0f : fmaxf(size * kLog2e, 1e-30f);
   const float cap2 = GEN ? a.mask.cap * kLog2e : 0.0f, to_cap = GEN && cap2 != 0.0f ? 2.0f * kLog2e / a.mask.cap * size : 0.0f;
-  const float slope2 = GEN && a.mask.slopes ? a.mask.slopes[h] * kLog2e : 0.0f;
+  const float slope2 = GEN && a.mask.slopes && mine ? a.mask.slopes[h] * kLog2e : 0.0f;
 
   // loads: where the lane's piece of each 1 KB lies
   uint32_t ko[U], vo[U];
@@ -282,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r] *= size * kLog2e;
       }
-      if (slope2 != 0.0f) {
+      if (a.mask.slopes) {
         const float far = static_cast<float>(t - j0 - 4 * half);
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r] = fmaf(-slope2, fabsf(far - static_cast<float>(8 * (r / 4) + r % 4)), x[r]);
@@ -376,11 +386,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   if (tiles > 0) load_next(sK0, sV0);
   // the queries behind them, negated for a negative scale, so that the largest product has the largest score
   {
-    const uint16_t* q = a.q + (t0 + i0 + qi) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
+    const uint16_t* q = a.q + (t0 + query) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
     const uint32_t sign = a.mask.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const uint4 z = i0 + qi < n && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
+      const uint4 z = mine && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
       fq[i] = as_frag(make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign));
     }
   }
@@ -392,10 +402,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
 
   l = sum_xor32(l);
   if (SPLIT) {
-    if (i0 + qi < n) {
-      const int64_t query = (t0 + i0 + qi) * a.hq + h;
-      if (half == 0) a.shares.stat[query * a.shares.splits + split] = make_float2(m, l);
-      float* out = a.shares.part + (query * a.shares.splits + split) * a.d + 4 * half;
+    if (mine) {
+      const int64_t at = ((t0 + query) * a.hq + h) * a.shares.splits + split;
+      if (half == 0) a.shares.stat[at] = make_float2(m, l);
+      float* out = a.shares.part + at * a.d + 4 * half;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -413,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
     for (int r = 0; r < 16; ++r) odd = fmaf(o[b][r], 0.0f, odd);  // 0 x infinity and 0 x NaN are NaN
   odd = sum_xor32(odd);
   // lanes of the lower half take columns 0 .. 7 of each 16, of the upper half 8 .. 15
-  uint16_t* out = a.o + ((t0 + i0 + qi) * a.hq + h) * a.d + 8 * half;
+  uint16_t* out = a.o + ((t0 + query) * a.hq + h) * a.d + 8 * half;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -423,16 +433,17 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
       for (int r = 0; r < 4; ++r) z[r] = pack2(o[b][8 * e + 2 * r] * inv, o[b][8 * e + 2 * r + 1] * inv);
       const auto u = __builtin_amdgcn_permlane32_swap(z[0], z[2], false, false);
       const auto v = __builtin_amdgcn_permlane32_swap(z[1], z[3], false, false);
-      if (i0 + qi < n && 32 * b + 16 * e + 8 * half < a.d)
+      if (mine && 32 * b + 16 * e + 8 * half < a.d)
         *reinterpret_cast<uint4*>(out + 32 * b + 16 * e) = make_uint4(u[0], v[0], u[1], v[1]);
     }
   // scores were finite and outputs are not: those queries once more, one by one
-  uint64_t again = __ballot(half == 0 && i0 + qi < n && odd != 0.0f && fabsf(l) < INFINITY);
+  uint64_t again = __ballot(half == 0 && mine && odd != 0.0f && fabsf(l) < INFINITY);
   if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores above
   while (again) {
     const int i = __builtin_ctzll(again);
     again &= again - 1;
-    query_alone(a, t0 + i0 + i, h, k0, p0 + i, sight(a.mask, p0 + i, keys, front), a.mask.slopes ? a.mask.slopes[h] : 0.0f);
+    const int qs = query_of(r0 + i), hs = head_of(r0 + i, qs);
+    query_alone(a, t0 + qs, hs, k0, qs + shift, sight(a.mask, qs + shift, keys, front), a.mask.slopes ? a.mask.slopes[hs] : 0.0f);
   }
 }
 
@@ -465,8 +476,8 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
 // 12 heads behind 4096 keys: 290 us whole, 148 in 3 shares, 137 in 5, 145 in 8).  Shares of 256
 // keys cost more in their starts and their join than they spread (2048 queries of
 // 12 heads, causal: 57 us, 44 in shares of 512).
-int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq) {
-  const int64_t units = (total / kRows + nseq) * hq, want = ceil_div(5 * 256, units), most = keys / 512;
+int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv) {
+  const int64_t units = (total * (hq / hkv) / kRows + nseq) * hkv, want = ceil_div(5 * 256, units), most = keys / 512;
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kFewSplits ? kFewSplits : n);
 }
@@ -482,8 +493,8 @@ void launch_as(const AttArgs& a, dim3 grid, hipStream_t st) {
 template <int D>
 void launch(AttArgs a, hipStream_t st) {
   constexpr int64_t kMost = (int64_t(1) << 32) / (64 * kWaves) - 1;  // workgroups that one launch has threads for
-  const int64_t slots = a.total / kRows + a.nseq;  // sequence s has slots offsets[s] / kRows + s and on
-  const int64_t each = static_cast<int64_t>(a.hq) * a.shares.splits, most = kMost / each;
+  const int64_t slots = a.total * a.group / kRows + a.nseq;  // sequence s has slots offsets[s] * group / kRows + s and on
+  const int64_t each = static_cast<int64_t>(a.hkv) * a.shares.splits, most = kMost / each;
   for (a.first = 0; a.first < slots; a.first += most) {
     a.slots = static_cast<uint32_t>(slots - a.first < most ? slots - a.first : most);
     a.units = static_cast<uint32_t>(a.slots * each);
@@ -508,7 +519,7 @@ extern "C" size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t 
   if (nseq < 1 || nseq > kMaxSeqs || total < 0 || total > kMaxTokens || total_k < 0 || total_k > kMaxTokens ||
       heads_check(hq, hkv, d) != BLLM_OK)
     return 0;
-  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq), d);
+  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq, hkv), d);
 }
 
 extern "C" int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,
@@ -544,10 +555,12 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.hkv = static_cast<int>(hkv);
   a.group = static_cast<int>(hq / hkv);
   a.d = static_cast<int>(d);
+  a.inv_group = 1.0 / a.group;
+  a.small_inv = ((1u << 21) + a.group - 1) / a.group;
   // keys that a query sees in the mean; a window alone bounds them, with the workgroup's others
   int64_t keys = total_k / nseq - (causal ? total / nseq / 2 : 0);
   if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
-  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq));
+  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq, hkv));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d <= 64)
     launch<64>(a, st);
