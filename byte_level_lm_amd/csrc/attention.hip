@@ -2,7 +2,8 @@
 //
 //   s_ij = scale q_i.k_j (capped, lowered by distance),  o_i = sum_j 2^{x_ij - m_i} v_j / sum_j 2^{x_ij - m_i},  x = s log2 e
 //
-// A workgroup has 128 queries of a head, a wave 32 of them; tiles of 32 keys go
+// A workgroup has 128 rows, a wave 32 of them: queries with all heads of a key head (rows of one
+// head: 64 prompts of 75 to 300, 12 heads on 4, 33 us, 30 so; 16 x 2048, d 256, 388 and 366).  Tiles of 32 keys go
 // through LDS, two buffers of them filled without registers, in one pass with
 // the running maximum and sum.  With d = 128, 32 keys are 16 matrix instructions of
 // 32 x 32 x 16 (512 cycles) and 16 exponentials a lane with what they need (some 480) for a
@@ -17,7 +18,7 @@
 // any loads 342, so that what they cost is the way into LDS, not its latency).
 //
 // Registers: scores come as S^T = K Q^T, of which a lane (half h of the wave)
-// has its query lane % 32 and keys 8 (r / 4) + 4 h + r % 4 of each 32.  The second product
+// has its row lane % 32 and keys 8 (r / 4) + 4 h + r % 4 of each 32.  The second product
 // O^T = V^T P^T takes 16 keys in the order 4 h + {0..3}, 8 + 4 h + {0..3}: the
 // weights as the lane has them, and V's columns by transposing LDS reads.  So
 // weights never leave their lane, and maximum, sum and the factor of O are one number a lane.
@@ -447,11 +448,12 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   }
 }
 
+template <bool FEW>
 __global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
-  const int lanes = join_lanes(a.d);
+  const int lanes = FEW ? join_lanes(a.d) : kWave;
   const int64_t query = (static_cast<int64_t>(blockIdx.x) * 64 * kWaves + threadIdx.x) / lanes, row = query / a.hq;
   const bool mine = row < a.total && row >= a.offsets[0] && row < a.offsets[a.nseq];
-  uint64_t again = __ballot(join_few(a.shares, query, mine, a.d, a.o));
+  uint64_t again = __ballot(FEW ? join_few(a.shares, query, mine, a.d, a.o) : mine && join_many(a.shares, query, a.d, a.o));
   if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores of the join
   while (again) {  // scores were finite and outputs are not: those queries once more, one by one
     const int64_t first = lane_value(query, __builtin_ctzll(again));
@@ -469,17 +471,16 @@ __global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
   }
 }
 
-// Shares of a query's keys: where the workgroups of whole queries would not
-// fill the CUs a few times over, as many as do, of 512 keys or more in the mean.
-// The oldest workgroup of a CU runs first, so that those that start together end one by
-// one; more of them than find room keep the CUs busy (8 pieces of 64 to 512 queries of
-// 12 heads behind 4096 keys: 290 us whole, 148 in 3 shares, 137 in 5, 145 in 8).  Shares of 256
-// keys cost more in their starts and their join than they spread (2048 queries of
-// 12 heads, causal: 57 us, 44 in shares of 512).
-int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv) {
-  const int64_t units = (total * (hq / hkv) / kRows + nseq) * hkv, want = ceil_div(5 * 256, units), most = keys / 512;
+// Shares of a query's keys: where the workgroups of whole queries are fewer than their
+// places on the card (4, 3 or 2 a CU, by registers), as many as fill these once, of 384 keys or more in the
+// mean.  One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 125 us in 15 shares, 145 in 23; 8 pieces
+// of 64 to 512 behind 4096: 251 whole, 131 in 4, 135 in 5; 16 queries behind 65536: 164 in 8, 35 in 64.  Shares of
+// 256 keys at least: 2048 queries, causal, 45.4 us, 43.8 so; of 512: 64 behind 8192 24.2, 22.3 so.
+int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv, int64_t d) {
+  const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 3 : 4);
+  const int64_t units = (total * (hq / hkv) / kRows + nseq) * hkv, want = ceil_div(places, units), most = keys / 384;
   const int64_t n = want < most ? want : most;
-  return static_cast<int>(n < 1 ? 1 : n > kFewSplits ? kFewSplits : n);
+  return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
 
 template <int D, bool SPLIT>
@@ -504,8 +505,12 @@ void launch(AttArgs a, hipStream_t st) {
       launch_as<D, false>(a, dim3(a.units), st);
   }
   if (a.shares.splits > 1) {  // few queries, by the rule of splits_of
-    const int64_t threads = a.total * a.hq * join_lanes(a.d);
-    hipLaunchKernelGGL(prompt_join, dim3(static_cast<unsigned>(ceil_div(threads, 64 * kWaves))), dim3(64 * kWaves), 0, st, a);
+    const bool few = a.shares.splits <= kFewSplits;
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.total * a.hq * (few ? join_lanes(a.d) : kWave), 64 * kWaves)));
+    if (few)
+      hipLaunchKernelGGL(prompt_join<true>, grid, dim3(64 * kWaves), 0, st, a);
+    else
+      hipLaunchKernelGGL(prompt_join<false>, grid, dim3(64 * kWaves), 0, st, a);
   }
 }
 
@@ -519,7 +524,7 @@ extern "C" size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t 
   if (nseq < 1 || nseq > kMaxSeqs || total < 0 || total > kMaxTokens || total_k < 0 || total_k > kMaxTokens ||
       heads_check(hq, hkv, d) != BLLM_OK)
     return 0;
-  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq, hkv), d);
+  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq, hkv, d), d);
 }
 
 extern "C" int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,
@@ -560,7 +565,7 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   // keys that a query sees in the mean; a window alone bounds them, with the workgroup's others
   int64_t keys = total_k / nseq - (causal ? total / nseq / 2 : 0);
   if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
-  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq, hkv));
+  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq, hkv, d));
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d <= 64)
     launch<64>(a, st);

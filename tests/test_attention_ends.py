@@ -29,6 +29,16 @@ def test_more_workgroups_than_one_launch_has_threads_for(B):
     assert torch.equal(o.view(n, 2, hq // 2, d), kv[:, :, None].expand(-1, -1, hq // 2, -1))
 
 
+def test_more_workgroups_than_one_launch_has_threads_for_with_a_key_head_each(B):
+    """The same with as many key heads, whose rows share no workgroup."""
+    import torch
+    n, h, d = 65535, 1024, 8
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(n, h, d, device="cuda", generator=gen, dtype=torch.bfloat16)
+    say("attention of", n * h, "workgroups")
+    assert torch.equal(B.attention(q, q, q, torch.arange(n + 1, device="cuda")), q)
+
+
 @pytest.mark.parametrize("q8", [False, True])
 def test_the_most_streams_take_a_step(B, q8):
     import torch
@@ -186,3 +196,36 @@ def test_keys_without_weight_and_one_key_alone(B):
         assert np.array_equal(to_np(o), np.repeat(v, 3, axis=1))
         want = oracle.attention(q, k, v, _offsets([90]), scale=1.0, sizes=True)  # scores of some 900 sqrt(d)
         _check(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(_offsets([90])), scale=1.0), want, 2.0 ** -8, d)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(7, 1, 24), (10, 2, 64), (9, 3, 128), (1024, 1, 8), (300, 2, 16), (33, 1, 256)])
+@pytest.mark.parametrize("more", [{}, {"window": 9, "prefix": 7}, {"cap": 2.0, "slopes": True}, {"causal": False}],
+                         ids=lambda m: "-".join(m) or "plain")
+def test_any_number_of_heads_to_a_key_head(B, hq, hkv, d, more):
+    """A workgroup's rows are queries with all their heads: its first and last query may have only some there."""
+    from tests.test_gpu_attention import _mask
+    rng = np.random.default_rng(hq + d)
+    lengths, keys = ([1, 0, 40, 3], [70, 5, 40, 2]) if hq < 100 else ([1, 0, 3], [40, 5, 3])
+    off, koff = _offsets(lengths), _offsets(keys)
+    q = _bf16(rng, (int(off[-1]), hq, d), 1.5)
+    k, v = (_bf16(rng, (int(koff[-1]), hkv, d)) for _ in range(2))
+    host, dev = _mask(more, rng, len(lengths), hq)
+    want = oracle.attention(q, k, v, off, k_offsets=koff, sizes=True, **host)
+    o = B.attention(_dev16(q), *_strided(k, v), to_dev(off), k_offsets=to_dev(koff), **dev)
+    _check(o, want, 2.0 ** -8, d, host.get("slopes"), max(keys))
+
+
+def test_values_that_are_not_finite_and_heads_that_share_their_rows(B):
+    """Only queries that see such a value have it, in every head."""
+    rng = np.random.default_rng(8)
+    off = _offsets([30])
+    q, k, v = _bf16(rng, (30, 6, 32)), _bf16(rng, (30, 2, 32)), _bf16(rng, (30, 2, 32))
+    want = oracle.attention(q, k, v, off, sizes=True)
+    v2 = v.copy()
+    v2[21, 1, 3] = np.nan     # key head 1: heads 3, 4 and 5
+    o = to_np(B.attention(_dev16(q), _dev16(k), _dev16(v2), to_dev(off))).astype(np.float64)
+    lost = np.zeros(o.shape, bool)
+    lost[21:, 3:, 3] = True
+    assert np.isnan(o[lost]).all()
+    o[lost] = want[0][lost]
+    _check(to_dev(o), want, 2.0 ** -8, 32)
