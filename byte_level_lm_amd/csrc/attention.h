@@ -109,7 +109,7 @@ __device__ inline float capped(float x, float cap, float two_over_cap_log2e) {
 
 // ---------------------------------------------------------------- shares of a query's keys
 
-constexpr int kMaxSplits = 64;   // the lanes of a wave, which joins them
+constexpr int kMaxSplits = 256;  // the lanes of a workgroup, which joins them
 
 // What each of a query's shares of keys gave (queries: row * hq + head)
 struct Shares {
@@ -128,9 +128,11 @@ inline Shares shares_at(void* ws, int64_t queries, int64_t splits) {
 __host__ __device__ inline int join_lanes(int d) { return d <= 32 ? 8 : d <= 64 ? 16 : d <= 128 ? 32 : 64; }  // of four values each
 
 // Joins a query's shares.  Up to kFewSplits of them: join_lanes(d) lanes of a wave, with all
-// their loads in flight at once (beside those of the wave's other queries); more: a wave, whose
-// groups of lanes take the shares in turn (61 streams of 5 shares, 8 heads of 64: 18.4 us the
-// first way, 19.9 the second; 64 shares have no registers for the first).  True where scores were finite and an output is not.
+// their loads in flight at once (beside those of the wave's other queries).  More: WAVES waves, whose groups of
+// lanes take the shares in turn; one has up to 64 of them, four are the workgroup.  Each of threads_to_join's
+// sides: 61 streams of 5 shares, 8 heads of 64: 18.4 us in lanes, 19.9 in waves; 4 pieces of 64 to 512 queries of 8
+// heads of 64 behind 8192 keys, 11 shares: 41 in waves, 54 in workgroups; 8 queries of 256 shares (262144 positions, one
+// key head): 31 in workgroups, 71 in the 64 shares that a wave can join.  True where scores were finite and an output is not.
 constexpr int kFewSplits = 8;
 
 __device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int d, uint16_t* o) {
@@ -169,43 +171,87 @@ __device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int 
   return odd;
 }
 
+template <int WAVES>
 __device__ inline bool join_many(const Shares& sh, int64_t query, int d, uint16_t* o) {
-  const int lane = lane_id(), lanes = join_lanes(d), col = 4 * (lane & (lanes - 1));
-  const float2 st = lane < sh.splits ? sh.stat[query * sh.splits + lane] : make_float2(-INFINITY, 0.0f);
+  __shared__ float sO[WAVES][256];
+  __shared__ float2 sStat[WAVES];
+  // a wave's share i is share w + WAVES i of the query's
+  const int lane = lane_id(), w = WAVES > 1 ? uniform(threadIdx.x >> 6) : 0, lanes = join_lanes(d), col = 4 * (lane & (lanes - 1));
+  const int n = (sh.splits - w + WAVES - 1) / WAVES;
+  const float2* stat = sh.stat + query * sh.splits + w;
+  const float2 st = lane < n ? stat[WAVES * lane] : make_float2(-INFINITY, 0.0f);
   float top = st.y == 0.0f ? -INFINITY : st.x;
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
   const float weight = st.y == 0.0f ? 0.0f : exp2_fast(st.x - (top == -INFINITY ? 0.0f : top));
   const float sum = wave_sum(weight * st.y);
   const bool mine = col < d;
-  const float* part = sh.part + query * sh.splits * d + (mine ? col : 0);
+  const float* part = sh.part + (query * sh.splits + w) * d + (mine ? col : 0);
   float y[4] = {};
-  for (int i0 = 0; i0 < sh.splits; i0 += 8 * kWave / lanes) {
+  for (int i0 = 0; i0 < n; i0 += 8 * kWave / lanes) {
     float4 v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int i = i0 + u * (kWave / lanes) + lane / lanes;
-      v[u] = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(min(i, sh.splits - 1)) * d);
+      v[u] = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(WAVES * min(i, n - 1)) * d);
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int i = i0 + u * (kWave / lanes) + lane / lanes;
-      const float w = __shfl(weight, i & 63, kWave);
-      const bool some = __shfl(st.y, i & 63, kWave) != 0.0f && i < sh.splits;
-      y[0] = some ? fmaf(w, v[u].x, y[0]) : y[0];
-      y[1] = some ? fmaf(w, v[u].y, y[1]) : y[1];
-      y[2] = some ? fmaf(w, v[u].z, y[2]) : y[2];
-      y[3] = some ? fmaf(w, v[u].w, y[3]) : y[3];
+      const float f = __shfl(weight, i & 63, kWave);
+      const bool some = __shfl(st.y, i & 63, kWave) != 0.0f && i < n;
+      y[0] = some ? fmaf(f, v[u].x, y[0]) : y[0];
+      y[1] = some ? fmaf(f, v[u].y, y[1]) : y[1];
+      y[2] = some ? fmaf(f, v[u].z, y[2]) : y[2];
+      y[3] = some ? fmaf(f, v[u].w, y[3]) : y[3];
     }
   }
   for (int off = lanes; off < kWave; off <<= 1)
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] += __shfl_xor(y[e], off, kWave);
-  const bool odd = mine && (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(sum) < INFINITY;
+  float l = sum;
+  if (WAVES > 1) {
+    if (mine && lane < lanes) *reinterpret_cast<float4*>(&sO[w][col]) = make_float4(y[0], y[1], y[2], y[3]);
+    if (lane == 0) sStat[w] = make_float2(top, sum);
+    __syncthreads();
+    if (w > 0) return false;
+    float all = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
-  if (mine && lane < lanes) *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+    for (int i = 0; i < WAVES; ++i) all = sStat[i].y == 0.0f ? all : fmaxf(all, sStat[i].x);
+    l = y[0] = y[1] = y[2] = y[3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      if (sStat[i].y == 0.0f || !mine) continue;
+      const float f = exp2_fast(sStat[i].x - (all == -INFINITY ? 0.0f : all));
+      const float4 v = *reinterpret_cast<const float4*>(&sO[i][col]);
+      l = fmaf(f, sStat[i].y, l);
+      y[0] = fmaf(f, v.x, y[0]);
+      y[1] = fmaf(f, v.y, y[1]);
+      y[2] = fmaf(f, v.z, y[2]);
+      y[3] = fmaf(f, v.w, y[3]);
+    }
+  }
+  if (!mine || lane >= lanes) return false;
+  const bool odd = (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(l) < INFINITY;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] / l;
+  *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
   return odd;
+}
+
+// Threads for each query of a join: join_lanes(d) of them, a wave or a workgroup of 256.
+inline int threads_to_join(const Shares& sh, int64_t queries, int d) {
+  return sh.splits <= kFewSplits ? join_lanes(d) : sh.splits > kWave || queries <= 2048 ? 256 : kWave;
+}
+// In a kernel of 256 threads with THREADS of them a query (0: join_lanes(d)): the thread's query, and its join.
+template <int THREADS>
+__device__ inline int64_t joined_query(int d) {
+  return (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / (THREADS ? THREADS : join_lanes(d));
+}
+template <int THREADS>
+__device__ inline bool join(const Shares& sh, int64_t query, bool there, int d, uint16_t* o) {
+  if (THREADS == 0) return join_few(sh, query, there, d, o);
+  return there && join_many<THREADS == 256 ? 4 : 1>(sh, query, d, o);
 }
 
 inline bool page_shift(int64_t page, int* shift) {

@@ -448,12 +448,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   }
 }
 
-template <bool FEW>
-__global__ __launch_bounds__(64 * kWaves) void prompt_join(AttArgs a) {
-  const int lanes = FEW ? join_lanes(a.d) : kWave;
-  const int64_t query = (static_cast<int64_t>(blockIdx.x) * 64 * kWaves + threadIdx.x) / lanes, row = query / a.hq;
+template <int THREADS>
+__global__ __launch_bounds__(256) void prompt_join(AttArgs a) {
+  const int64_t query = joined_query<THREADS>(a.d), row = query / a.hq;
   const bool mine = row < a.total && row >= a.offsets[0] && row < a.offsets[a.nseq];
-  uint64_t again = __ballot(FEW ? join_few(a.shares, query, mine, a.d, a.o) : mine && join_many(a.shares, query, a.d, a.o));
+  uint64_t again = __ballot(join<THREADS>(a.shares, query, mine, a.d, a.o));
   if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores of the join
   while (again) {  // scores were finite and outputs are not: those queries once more, one by one
     const int64_t first = lane_value(query, __builtin_ctzll(again));
@@ -505,12 +504,14 @@ void launch(AttArgs a, hipStream_t st) {
       launch_as<D, false>(a, dim3(a.units), st);
   }
   if (a.shares.splits > 1) {  // few queries, by the rule of splits_of
-    const bool few = a.shares.splits <= kFewSplits;
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.total * a.hq * (few ? join_lanes(a.d) : kWave), 64 * kWaves)));
-    if (few)
-      hipLaunchKernelGGL(prompt_join<true>, grid, dim3(64 * kWaves), 0, st, a);
+    const int threads = threads_to_join(a.shares, a.total * a.hq, a.d);
+    const dim3 grid(static_cast<unsigned>(ceil_div(a.total * a.hq * threads, 256)));
+    if (a.shares.splits <= kFewSplits)
+      hipLaunchKernelGGL(prompt_join<0>, grid, dim3(256), 0, st, a);
+    else if (threads == kWave)
+      hipLaunchKernelGGL(prompt_join<kWave>, grid, dim3(256), 0, st, a);
     else
-      hipLaunchKernelGGL(prompt_join<false>, grid, dim3(64 * kWaves), 0, st, a);
+      hipLaunchKernelGGL(prompt_join<256>, grid, dim3(256), 0, st, a);
   }
 }
 

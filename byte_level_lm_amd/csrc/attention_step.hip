@@ -270,22 +270,17 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void ste
   }
 }
 
-// FEW: up to kFewSplits shares
-template <bool FEW>
+template <int THREADS>
 __global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
-  const int lanes = FEW ? join_lanes(a.pages.d) : kWave;
-  const int64_t head = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / lanes;
-  if (FEW)
-    join_few(a.shares, head, head < heads, a.pages.d, a.o);
-  else if (head < heads)
-    join_many(a.shares, head, a.pages.d, a.o);
+  const int64_t head = joined_query<THREADS>(a.pages.d);
+  join<THREADS>(a.shares, head, head < heads, a.pages.d, a.o);
 }
 
 // Shares of a stream, each at least a tile a wave: as many as give a workgroup to each
 // place for one (LDS has room for 8, 4 or 2 of them a CU).  8 streams of 65536 positions, d 128:
 // 970 us whole, 189 in these 32 shares, 188 in 16, 192 in 64.  8 of 32768, d 256, 8 bits: 626 whole,
 // 107 in 16, 110 in 32.  64 streams of 4096 to 16384, d 64, 8 bits, 2 heads, whose longest ones
-// end last: 196 whole, 47 in 16, 49 in 8.
+// end last: 196 whole, 47 in 16, 49 in 8.  One stream of 262144, d 128, one key head: 31 in 256, 71 in 64.
 int splits_of(int64_t nseq, int64_t heads, int64_t positions, int64_t d) {
   const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 4 : 8);
   const int64_t most = ceil_div(positions, kTile * kStepWaves), want = ceil_div(places, nseq * heads);
@@ -353,9 +348,15 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   else
     q8 ? step_launch<256, true>(a, grid, st) : step_launch<256, false>(a, grid, st);
   const int64_t heads = nseq * hq;
-  if (a.shares.splits > kFewSplits)
-    hipLaunchKernelGGL(step_join<false>, dim3(static_cast<unsigned>(ceil_div(heads, 4))), dim3(256), 0, st, a, heads);
-  else if (a.shares.splits > 1)
-    hipLaunchKernelGGL(step_join<true>, dim3(static_cast<unsigned>(ceil_div(heads * join_lanes(a.pages.d), 256))), dim3(256), 0, st, a, heads);
+  if (a.shares.splits > 1) {
+    const int threads = threads_to_join(a.shares, heads, a.pages.d);
+    const dim3 joins(static_cast<unsigned>(ceil_div(heads * threads, 256)));
+    if (a.shares.splits <= kFewSplits)
+      hipLaunchKernelGGL(step_join<0>, joins, dim3(256), 0, st, a, heads);
+    else if (threads == kWave)
+      hipLaunchKernelGGL(step_join<kWave>, joins, dim3(256), 0, st, a, heads);
+    else
+      hipLaunchKernelGGL(step_join<256>, joins, dim3(256), 0, st, a, heads);
+  }
   return launch_status();
 }

@@ -229,3 +229,20 @@ def test_values_that_are_not_finite_and_heads_that_share_their_rows(B):
     assert np.isnan(o[lost]).all()
     o[lost] = want[0][lost]
     _check(to_dev(o), want, 2.0 ** -8, 32)
+
+
+@pytest.mark.parametrize("d,q8", [(16, False), (16, True), (72, False), (128, True), (256, False)])
+def test_one_long_stream(B, d, q8):
+    """More shares of one stream's keys than a wave has lanes, in a step and for few queries."""
+    rng = np.random.default_rng(d)
+    n = 40001
+    pages, scales, table, dev, sc = _cache(rng, [n], 1, d, 64, q8)
+    q, lengths = _bf16(rng, (1, 3, d)), np.array([n], np.int32)
+    want = oracle.attention_step(q, *pages, table, lengths, k_scale=scales[0], v_scale=scales[1], sizes=True)
+    _check(B.attention_step(_dev16(q), *dev, to_dev(table), to_dev(lengths), **sc), want, 2.0 ** -16, d)
+    if q8:
+        return
+    off, koff = _offsets([2]), _offsets([n])
+    q, k, v = _bf16(rng, (2, 3, d)), _bf16(rng, (n, 1, d)), _bf16(rng, (n, 1, d))
+    want = oracle.attention(q, k, v, off, k_offsets=koff, sizes=True)
+    _check(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff)), want, 2.0 ** -8, d)
