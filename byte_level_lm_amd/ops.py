@@ -389,10 +389,12 @@ def _is(name, t, shape, dtype):
 
 def _out(name, t, shape, dtype, like):
     """The caller's output, or a new one on the device of ``like``."""
-    if t is None:
-        if like.shape == shape:  # half the time of building the shape again
+    if t is None:  # without the shape and the dtype where they are like's: half the time
+        if like.shape == shape:
+            if like.dtype == dtype and like.is_contiguous():
+                return torch.empty_like(like)
             return torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
     _is(name, t, shape, dtype)
     return t
 
@@ -639,13 +641,22 @@ def kv_read(k_pages, v_pages, table, offsets, total: int, *, start=None, k_scale
         _is("start", start, (nseq,), torch.int32)
     shape = (int(total), hkv, d)
     k_out = _out("k_out", k_out, shape, torch.bfloat16, k_pages)
-    v_out = _out("v_out", v_out, shape, torch.bfloat16, k_pages)
+    v_out = _out("v_out", v_out, shape, torch.bfloat16, k_out)
     stream = _stream_of(k_pages, v_pages, table, k_scale, v_scale, offsets, start, k_out, v_out)
     rc = L.lib().bllm_kv_read(k_pages.data_ptr(), v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), dt, npages, page,
                               hkv, d, table.data_ptr(), cols, offsets.data_ptr(), nseq, shape[0], _ptr(start), L.BF16,
                               k_out.data_ptr(), v_out.data_ptr(), stream)
     L.check("bllm_kv_read", rc)
     return k_out, v_out
+
+
+def _scratch(nbytes: int, ws, like):
+    """The caller's workspace, or a new one (in like's dtype, the quickest to make), and its bytes."""
+    if ws is None:
+        each = like.element_size()
+        n = (nbytes + 15) // each
+        return like.new_empty(n), n * each
+    return _ws(nbytes, ws, like.device), _nbytes(ws)
 
 
 def _mask_args(nseq, hq, window, cap, slopes, prefix):
@@ -687,12 +698,12 @@ def attention(q, k, v, offsets, *, k_offsets=None, scale=None, causal: bool = Tr
         raise ValueError("k and v of other lengths than q need k_offsets")
     window, cap = _mask_args(nseq, hq, window, cap, slopes, prefix)
     o_out = _out("o_out", o_out, (total, hq, d), q.dtype, q)
-    w = _ws(attention_workspace(nseq, total, total_k, hq, hkv, d), ws, q.device)
+    w, w_bytes = _scratch(L.lib().bllm_attention_workspace(nseq, total, total_k, hq, hkv, d), ws, q)
     stream = _stream_of(q, k, v, offsets, k_offsets, slopes, prefix, o_out, w)
     rc = L.lib().bllm_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), offsets.data_ptr(), _ptr(k_offsets),
                                 nseq, total, total_k, hq, hkv, d, qs, ks, vs, d ** -0.5 if scale is None else scale,
                                 1 if causal else 0, window, cap, _ptr(slopes), _ptr(prefix), o_out.data_ptr(),
-                                w.data_ptr(), _nbytes(w), stream)
+                                w.data_ptr(), w_bytes, stream)
     L.check("bllm_attention", rc)
     return o_out
 
@@ -710,12 +721,12 @@ def attention_step(q, k_pages, v_pages, table, lengths, *, k_scale=None, v_scale
     _is("lengths", lengths, (nseq,), torch.int32)
     window, cap = _mask_args(nseq, hq, window, cap, slopes, prefix)
     o_out = _out("o_out", o_out, (nseq, hq, d), q.dtype, q)
-    w = _ws(attention_step_workspace(nseq, hq, hkv, d, cols * page), ws, q.device)
+    w, w_bytes = _scratch(L.lib().bllm_attention_step_workspace(nseq, hq, hkv, d, cols * page), ws, q)
     stream = _stream_of(q, k_pages, v_pages, table, lengths, k_scale, v_scale, slopes, prefix, o_out, w)
     rc = L.lib().bllm_attention_step(q.data_ptr(), _dt(q), nseq, hq, hkv, d, qs, k_pages.data_ptr(),
                                      v_pages.data_ptr(), _ptr(k_scale), _ptr(v_scale), dt, npages, page,
                                      table.data_ptr(), cols, lengths.data_ptr(), d ** -0.5 if scale is None else scale,
                                      window, cap, _ptr(slopes), _ptr(prefix), o_out.data_ptr(), w.data_ptr(),
-                                     _nbytes(w), stream)
+                                     w_bytes, stream)
     L.check("bllm_attention_step", rc)
     return o_out
