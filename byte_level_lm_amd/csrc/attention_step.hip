@@ -283,6 +283,9 @@ __global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
 // end last: 196 whole, 47 in 16, 49 in 8.  One stream of 262144, d 128, one key head: 31 in 256, 71 in 64.
 int splits_of(int64_t nseq, int64_t heads, int64_t positions, int64_t d) {
   const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 4 : 8);
+  // few tiles a wave take no longer than a second launch (640 positions, 12 heads on 4 of 128: 13.3 us whole, 15.8 in
+  // shares; d 256: 20.5 and 16.0)
+  if (positions <= (d > 128 ? 2 : 5) * kTile * kStepWaves) return 1;
   const int64_t most = ceil_div(positions, kTile * kStepWaves), want = ceil_div(places, nseq * heads);
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
@@ -334,9 +337,12 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   a.hq = static_cast<int>(hq);
   a.group = static_cast<int>(hq / hkv);
   a.blocks = (a.group + 15) / 16;
-  // a window alone bounds the positions that a query sees
+  // The positions that a query sees: a window bounds them but for a prefix, which is taken to be
+  // short where whole streams fill the CUs (window of 512, 61 streams of up to 8192, 8 heads of 64: with a prefix of 5
+  // 15.9 us so, 17.8 with shares for the whole cache; with one of 4096 57 and 42).  16 streams of 12
+  // heads on 4 of 128 with a prefix of 4096: 18.9 in shares, 61 whole.
   int64_t positions = cols * page;
-  if (a.mask.window && !prefix && window + 2 * kTile < positions) positions = window + 2 * kTile;
+  if (a.mask.window && (!prefix || nseq * hkv * a.blocks >= 256) && window + 2 * kTile < positions) positions = window + 2 * kTile;
   a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions, d));
   const dim3 grid(static_cast<unsigned>(hkv * a.blocks * a.shares.splits), static_cast<unsigned>(nseq));
   hipStream_t st = static_cast<hipStream_t>(stream);
