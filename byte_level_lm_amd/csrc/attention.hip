@@ -470,14 +470,15 @@ __global__ __launch_bounds__(256) void prompt_join(AttArgs a) {
   }
 }
 
-// Shares of a query's keys: where the workgroups of whole queries are fewer than their
-// places on the card (4, 3 or 2 a CU, by registers), as many as fill these once, of 384 keys or more in the
-// mean.  One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 125 us in 15 shares, 145 in 23; 8 pieces
-// of 64 to 512 behind 4096: 251 whole, 131 in 4, 135 in 5; 16 queries behind 65536: 164 in 8, 35 in 64.  Shares of
-// 256 keys at least: 2048 queries, causal, 45.4 us, 43.8 so; of 512: 64 behind 8192 24.2, 22.3 so.
+// Shares of a query's keys, of 384 or more in the mean: as many as the workgroups of whole queries
+// find places for on the card (4, 3 or 2 a CU, by registers), since a few that begin late cost a round.
+// One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 125 us in 15 shares, 145 in 23; 8 pieces
+// of 64 to 512 behind 4096: 251 whole, 125 in 3, 129 in 4, 136 in 6; 3 x 2048, causal: 69 whole, 81 in 2; 16 queries behind
+// 65536: 164 in 8, 35 in 64.  Shares of 256 keys at least: 2048 queries, causal, 45.4 us, 43.8 so; of 512: 64 behind 8192 24.2, 22.3 so.
 int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv, int64_t d) {
   const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 3 : 4);
-  const int64_t units = (total * (hq / hkv) / kRows + nseq) * hkv, want = ceil_div(places, units), most = keys / 384;
+  // half a workgroup more a sequence, for its last rows
+  const int64_t units = (total * (hq / hkv) / kRows + (nseq + 1) / 2) * hkv, want = places / units, most = keys / 384;
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
