@@ -8,10 +8,11 @@
 // the running maximum and sum.  With d = 128, 32 keys are 16 matrix instructions of
 // 32 x 32 x 16 (512 cycles) and 16 exponentials a lane with what they need (some 480) for a
 // wave, which three waves a SIMD run beside each other.  What bounds it then is the card's
-// power: 32 sequences of 2048 tokens, 12 heads on 4, causal: 445 us, 930 TFLOP/s, the
-// matrix cores busy 47 % of 859 thousand cycles at 1.85 GHz (the same instructions with less to
-// move, without the loads, run at 2.3).  With d = 64 the vector instructions do: window of 512
-// over 16 ragged sequences of up to 8192 bytes, 8 heads, 117 us, 600 TFLOP/s.  Tried and
+// power: 32 sequences of 2048 tokens, 12 heads on 4, causal: 440 us, 945 TFLOP/s, the
+// matrix cores busy 48 % of the cycles at 1.65 to 1.85 GHz (the same instructions with less to
+// move, without the loads, run at 2.3).  With d = 64 it is a tile's way through a wave: window of 512
+// over 16 ragged sequences of up to 8192 bytes, 8 heads, 118 us, 637 TFLOP/s, 28 % matrix and 53 % vector
+// instructions.  With cap and slopes the latter: 8 pieces of 64 to 512 queries behind 4096 keys 118 us, 520 TFLOP/s.  Tried and
 // no faster: 256 queries a workgroup, 64 a wave (registers of one wave a SIMD), tiles of
 // 64 keys, the next tile's first product between this one's exponentials, the sum by
 // a matrix instruction (480 us), priorities, loads two tiles ahead in three buffers (461 us; without
