@@ -246,3 +246,54 @@ def test_one_long_stream(B, d, q8):
     q, k, v = _bf16(rng, (2, 3, d)), _bf16(rng, (n, 1, d)), _bf16(rng, (n, 1, d))
     want = oracle.attention(q, k, v, off, k_offsets=koff, sizes=True)
     _check(B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff)), want, 2.0 ** -8, d)
+
+
+@pytest.mark.parametrize("keys", [None, [90, 0, 2600]])
+def test_rows_in_front_of_the_first_sequence(B, keys):
+    """Offsets that begin behind row 0: the rows in front are no sequence's, and are left, in one piece and in shares."""
+    import torch
+    rng = np.random.default_rng(5)
+    ahead, lengths = 150, [40, 0, 20]
+    off = _offsets(lengths) + ahead
+    koff = off if keys is None else _offsets(keys) + 7
+    total, total_k = int(off[-1]) + 9, int(koff[-1]) + (9 if keys is None else 1)
+    q, k, v = _bf16(rng, (total, 6, 64)), _bf16(rng, (total_k, 2, 64)), _bf16(rng, (total_k, 2, 64))
+    inside = slice(ahead, int(off[-1]))
+    want = oracle.attention(q[inside], k[koff[0]:], v[koff[0]:], off - ahead, k_offsets=koff - koff[0], sizes=True)
+    out = torch.full((total, 6, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    B.attention(_dev16(q), _dev16(k), _dev16(v), to_dev(off), k_offsets=to_dev(koff), o_out=out)
+    assert torch.all(out[:ahead] == 7.0) and torch.all(out[off[-1]:] == 7.0)
+    _check(out[inside], want, 2.0 ** -8, 64)
+    table, npages = _table(rng, lengths, 16)
+    pools = [torch.full((npages, 2, 16, 64), 3.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    rows = _dev16(_bf16(rng, (total, 2, 64)))
+    B.kv_write(rows, rows, *pools, to_dev(table), offsets=to_dev(off))
+    assert int((pools[0] == 3.0).all(-1).sum()) == npages * 2 * 16 - 2 * sum(lengths)
+    back = [torch.full((total, 2, 64), 5.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    B.kv_read(*pools, to_dev(table), to_dev(off), total, k_out=back[0], v_out=back[1])
+    for x in back:
+        assert torch.equal(x[inside], rows[inside]) and torch.all(x[:ahead] == 5.0) and torch.all(x[off[-1]:] == 5.0)
+
+
+def test_steps_and_prompts_of_many_shares_in_a_graph(B):
+    """A captured step and prompt whose keys go in many shares, with workspaces of their own, replayed over new values."""
+    import torch
+    rng = np.random.default_rng(6)
+    pages, scales, table, dev, sc = _cache(rng, [9000], 1, 64, 32, True)
+    dtable, n = to_dev(table), to_dev(np.array([9000], np.int32))
+    off, koff = to_dev(_offsets([5])), to_dev(_offsets([12000]))
+    q, pq, pk, pv = (_dev16(_bf16(rng, (m, h, 64))) for m, h in ((1, 4), (5, 4), (12000, 2), (12000, 2)))
+
+    def both():
+        return B.attention_step(q, *dev, dtable, n, **sc), B.attention(pq, pk, pv, off, k_offsets=koff)
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = both()
+    for length in (9000, 1, 0, 4321):
+        n.fill_(length)
+        q.copy_(_dev16(_bf16(rng, (1, 4, 64))))
+        pq.copy_(_dev16(_bf16(rng, (5, 4, 64))))
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, both()))
