@@ -13,7 +13,7 @@
 // move, without the loads, run at 2.3).  With d = 64 it is a tile's way through a wave: window of 512
 // over 16 ragged sequences of up to 8192 bytes, 8 heads, 118 us, 637 TFLOP/s, 28 % matrix and 53 % vector
 // instructions.  With cap and slopes the latter: 8 pieces of 64 to 512 queries behind 4096 keys 118 us, 520 TFLOP/s.  Tried and
-// no faster: 256 queries a workgroup, 64 a wave (registers of one wave a SIMD), tiles of
+// no faster: 256 rows a workgroup (489 and 130 us), 64 rows (514 and 119), 64 a wave (registers of one wave a SIMD), tiles of
 // 64 keys, the next tile's first product between this one's exponentials, the sum by
 // a matrix instruction (480 us), priorities, loads two tiles ahead in three buffers (461 us; without
 // any loads 342, so that what they cost is the way into LDS, not its latency).
