@@ -254,6 +254,15 @@ __device__ inline bool join(const Shares& sh, int64_t query, bool there, int d, 
   return there && join_many<THREADS == 256 ? 4 : 1>(sh, query, d, o);
 }
 
+// A launch by its function, without the call configuration of <<<>>>, which costs the host 0.2 of 3.4 us.  Arguments cost
+// it too, 0.35 us for 100 bytes, and 256 more of them go along where a kernel asks for gridDim.
+template <typename Args>
+inline void launch_kernel(void (*kernel)(Args), int64_t groups, int64_t rows, int threads, hipStream_t st, Args a) {
+  void* args[] = {&a};
+  (void)hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<unsigned>(groups), static_cast<unsigned>(rows)),
+                        dim3(static_cast<unsigned>(threads)), args, 0, st);
+}
+
 inline bool page_shift(int64_t page, int* shift) {
   for (*shift = 4; *shift <= 8; ++*shift)
     if (page == int64_t(1) << *shift) return true;

@@ -485,11 +485,9 @@ int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv
 }
 
 template <int D, bool SPLIT>
-void launch_as(const AttArgs& a, dim3 grid, hipStream_t st) {
-  if (a.mask.cap > 0.0f || a.mask.slopes)
-    hipLaunchKernelGGL((prompt_tiles<D, true, SPLIT>), grid, dim3(64 * kWaves), 0, st, a);
-  else
-    hipLaunchKernelGGL((prompt_tiles<D, false, SPLIT>), grid, dim3(64 * kWaves), 0, st, a);
+void launch_as(const AttArgs& a, hipStream_t st) {
+  launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? prompt_tiles<D, true, SPLIT> : prompt_tiles<D, false, SPLIT>, a.units, 1,
+                64 * kWaves, st, a);
 }
 
 template <int D>
@@ -501,19 +499,14 @@ void launch(AttArgs a, hipStream_t st) {
     a.slots = static_cast<uint32_t>(slots - a.first < most ? slots - a.first : most);
     a.units = static_cast<uint32_t>(a.slots * each);
     if (a.shares.splits > 1)
-      launch_as<D, true>(a, dim3(a.units), st);
+      launch_as<D, true>(a, st);
     else
-      launch_as<D, false>(a, dim3(a.units), st);
+      launch_as<D, false>(a, st);
   }
   if (a.shares.splits > 1) {  // few queries, by the rule of splits_of
     const int threads = threads_to_join(a.shares, a.total * a.hq, a.d);
-    const dim3 grid(static_cast<unsigned>(ceil_div(a.total * a.hq * threads, 256)));
-    if (a.shares.splits <= kFewSplits)
-      hipLaunchKernelGGL(prompt_join<0>, grid, dim3(256), 0, st, a);
-    else if (threads == kWave)
-      hipLaunchKernelGGL(prompt_join<kWave>, grid, dim3(256), 0, st, a);
-    else
-      hipLaunchKernelGGL(prompt_join<256>, grid, dim3(256), 0, st, a);
+    launch_kernel(a.shares.splits <= kFewSplits ? prompt_join<0> : threads == kWave ? prompt_join<kWave> : prompt_join<256>,
+                  ceil_div(a.total * a.hq * threads, 256), 1, 256, st, a);
   }
 }
 

@@ -270,10 +270,15 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void ste
   }
 }
 
+struct JoinArgs {
+  Shares shares;
+  uint16_t* o;
+  int heads, d;
+};
 template <int THREADS>
-__global__ __launch_bounds__(256) void step_join(StepArgs a, int64_t heads) {
-  const int64_t head = joined_query<THREADS>(a.pages.d);
-  join<THREADS>(a.shares, head, head < heads, a.pages.d, a.o);
+__global__ __launch_bounds__(256) void step_join(JoinArgs a) {
+  const int64_t head = joined_query<THREADS>(a.d);
+  join<THREADS>(a.shares, head, head < a.heads, a.d, a.o);
 }
 
 // Shares of a stream, each at least a tile a wave: as many as give a workgroup to each
@@ -292,11 +297,9 @@ int splits_of(int64_t nseq, int64_t heads, int64_t positions, int64_t d) {
 }
 
 template <int D, bool Q8>
-void step_launch(const StepArgs& a, dim3 grid, hipStream_t st) {
-  if (a.mask.cap > 0.0f || a.mask.slopes)
-    hipLaunchKernelGGL((step_share<D, Q8, true>), grid, dim3(64 * kStepWaves), 0, st, a);
-  else
-    hipLaunchKernelGGL((step_share<D, Q8, false>), grid, dim3(64 * kStepWaves), 0, st, a);
+void step_launch(const StepArgs& a, int64_t groups, int64_t nseq, hipStream_t st) {
+  launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? step_share<D, Q8, true> : step_share<D, Q8, false>, groups, nseq,
+                64 * kStepWaves, st, a);
 }
 
 }  // namespace
@@ -344,25 +347,20 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   int64_t positions = cols * page;
   if (a.mask.window && (!prefix || nseq * hkv * a.blocks >= 256) && window + 2 * kTile < positions) positions = window + 2 * kTile;
   a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions, d));
-  const dim3 grid(static_cast<unsigned>(hkv * a.blocks * a.shares.splits), static_cast<unsigned>(nseq));
+  const int64_t groups = hkv * a.blocks * a.shares.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool q8 = pages_dtype == BLLM_I8;
   if (d <= 64)
-    q8 ? step_launch<64, true>(a, grid, st) : step_launch<64, false>(a, grid, st);
+    q8 ? step_launch<64, true>(a, groups, nseq, st) : step_launch<64, false>(a, groups, nseq, st);
   else if (d <= 128)
-    q8 ? step_launch<128, true>(a, grid, st) : step_launch<128, false>(a, grid, st);
+    q8 ? step_launch<128, true>(a, groups, nseq, st) : step_launch<128, false>(a, groups, nseq, st);
   else
-    q8 ? step_launch<256, true>(a, grid, st) : step_launch<256, false>(a, grid, st);
+    q8 ? step_launch<256, true>(a, groups, nseq, st) : step_launch<256, false>(a, groups, nseq, st);
   const int64_t heads = nseq * hq;
   if (a.shares.splits > 1) {
     const int threads = threads_to_join(a.shares, heads, a.pages.d);
-    const dim3 joins(static_cast<unsigned>(ceil_div(heads * threads, 256)));
-    if (a.shares.splits <= kFewSplits)
-      hipLaunchKernelGGL(step_join<0>, joins, dim3(256), 0, st, a, heads);
-    else if (threads == kWave)
-      hipLaunchKernelGGL(step_join<kWave>, joins, dim3(256), 0, st, a, heads);
-    else
-      hipLaunchKernelGGL(step_join<256>, joins, dim3(256), 0, st, a, heads);
+    launch_kernel(a.shares.splits <= kFewSplits ? step_join<0> : threads == kWave ? step_join<kWave> : step_join<256>,
+                  ceil_div(heads * threads, 256), 1, 256, st, JoinArgs{a.shares, a.o, static_cast<int>(heads), a.pages.d});
   }
   return launch_status();
 }

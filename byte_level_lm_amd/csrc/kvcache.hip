@@ -20,13 +20,13 @@ constexpr int kMaxTile = 64;     // tokens of a workgroup
 struct KvArgs {
   Pages pages;
   uint16_t *k, *v;               // packed rows
-  int64_t k_stride, v_stride;    // between tokens
+  int k_stride, v_stride;        // between tokens
   void *k_pages, *v_pages;
   float *k_scale, *v_scale;      // or null
   const int64_t* offsets;        // or null: one row of each stream
   const int32_t* start;          // or null
-  int64_t total;
-  int nseq, tile;                // tokens of a workgroup
+  int total, nseq;
+  int tile, groups;              // tokens of a workgroup, workgroups
 };
 
 __device__ inline uint4 codes_to_bf16(uint2 c, float scale) {
@@ -52,9 +52,9 @@ __global__ __launch_bounds__(kThreads) void kv_move(KvArgs a) {
   __shared__ int64_t sRow[kMaxTile];  // the page row of each token (head 0), -1: none, -2: not a sequence's
   const int hkv = a.pages.hkv, rows = 2 * hkv * a.tile, group = threadIdx.x / G, in = threadIdx.x % G;
   const bool mine = in * 8 < a.pages.d;
-  const int64_t tiles = (a.total + a.tile - 1) / a.tile;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t first = tile * a.tile;
+  const int tiles = (a.total + a.tile - 1) / a.tile;
+  for (int tile = blockIdx.x; tile < tiles; tile += a.groups) {
+    const int64_t first = static_cast<int64_t>(tile) * a.tile;
     if (threadIdx.x < kWave) {
       const int64_t t = first + threadIdx.x;
       int s = static_cast<int>(t);
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(kThreads) void kv_move(KvArgs a) {
       bool has = threadIdx.x < a.tile && t < a.total;
       if (a.offsets) {
         const auto slot = [&](int i) { return a.offsets[i]; };
-        const int64_t last = min(first + a.tile, a.total) - 1;
+        const int64_t last = min(first + a.tile, static_cast<int64_t>(a.total)) - 1;
         const int s0 = wave_find(a.nseq, first, slot), s1 = max(s0, wave_find(a.nseq, last, slot));
         s = s0 + upper_seq(a.offsets + s0, s1 - s0 + 1, t);
         at = t - a.offsets[s];
@@ -160,13 +160,9 @@ void launch_as(KvArgs a, hipStream_t st) {
   tile = tile > spread ? spread : tile;
   a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
   const int64_t tiles = ceil_div(a.total, a.tile);
-  const dim3 grid(static_cast<unsigned>(tiles < (1 << 20) ? tiles : 1 << 20));
-  if (g == 8)
-    hipLaunchKernelGGL((kv_move<WRITE, Q8, 8>), grid, dim3(kThreads), 0, st, a);
-  else if (g == 16)
-    hipLaunchKernelGGL((kv_move<WRITE, Q8, 16>), grid, dim3(kThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((kv_move<WRITE, Q8, 32>), grid, dim3(kThreads), 0, st, a);
+  a.groups = static_cast<int>(tiles < (1 << 20) ? tiles : 1 << 20);
+  launch_kernel(g == 8 ? kv_move<WRITE, Q8, 8> : g == 16 ? kv_move<WRITE, Q8, 16> : kv_move<WRITE, Q8, 32>, a.groups, 1,
+                kThreads, st, a);
 }
 
 template <bool WRITE>
@@ -201,15 +197,15 @@ extern "C" int bllm_kv_write(const void* k, const void* v, int dtype, const int6
     return BLLM_E_NOTSUP;
   a.k = static_cast<uint16_t*>(const_cast<void*>(k));
   a.v = static_cast<uint16_t*>(const_cast<void*>(v));
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
+  a.k_stride = static_cast<int>(k_stride);
+  a.v_stride = static_cast<int>(v_stride);
   a.k_pages = k_pages;
   a.v_pages = v_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.offsets = offsets;
   a.start = start;
-  a.total = total;
+  a.total = static_cast<int>(total);
   a.nseq = static_cast<int>(nseq);
   return launch<true>(a, stream);
 }
@@ -226,14 +222,14 @@ extern "C" int bllm_kv_read(const void* k_pages, const void* v_pages, const floa
   if (dtype != BLLM_BF16 || total > kMaxTokens || !aligned16(k_out) || !aligned16(v_out)) return BLLM_E_NOTSUP;
   a.k = static_cast<uint16_t*>(k_out);
   a.v = static_cast<uint16_t*>(v_out);
-  a.k_stride = a.v_stride = hkv * d;
+  a.k_stride = a.v_stride = static_cast<int>(hkv * d);
   a.k_pages = const_cast<void*>(k_pages);
   a.v_pages = const_cast<void*>(v_pages);
   a.k_scale = const_cast<float*>(k_scale);
   a.v_scale = const_cast<float*>(v_scale);
   a.offsets = offsets;
   a.start = start;
-  a.total = total;
+  a.total = static_cast<int>(total);
   a.nseq = static_cast<int>(nseq);
   return launch<false>(a, stream);
 }
