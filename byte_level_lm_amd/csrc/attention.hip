@@ -561,7 +561,9 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   // keys that a query sees in the mean; a window alone bounds them, with the workgroup's others
   int64_t keys = total_k / nseq - (causal ? total / nseq / 2 : 0);
   if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
-  a.shares = shares_at(ws, total * hq, splits_of(nseq, total, keys, hq, hkv, d));
+  const int splits = splits_of(nseq, total, keys, hq, hkv, d);
+  if (ws_bytes < shares_bytes(total * hq, splits, d)) return BLLM_E_WS;  // not so: fewer keys take no more shares
+  a.shares = shares_at(ws, total * hq, splits);
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (d <= 64)
     launch<64>(a, st);

@@ -346,7 +346,9 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   // heads on 4 of 128 with a prefix of 4096: 18.9 in shares, 61 whole.
   int64_t positions = cols * page;
   if (a.mask.window && (!prefix || nseq * hkv * a.blocks >= 256) && window + 2 * kTile < positions) positions = window + 2 * kTile;
-  a.shares = shares_at(ws, nseq * hq, splits_of(nseq, hkv * a.blocks, positions, d));
+  const int splits = splits_of(nseq, hkv * a.blocks, positions, d);
+  if (ws_bytes < shares_bytes(nseq * hq, splits, d)) return BLLM_E_WS;  // not so: fewer positions take no more shares
+  a.shares = shares_at(ws, nseq * hq, splits);
   const int64_t groups = hkv * a.blocks * a.shares.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool q8 = pages_dtype == BLLM_I8;
