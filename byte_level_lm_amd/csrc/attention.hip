@@ -476,10 +476,16 @@ __global__ __launch_bounds__(256) void prompt_join(AttArgs a) {
 // One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 125 us in 15 shares, 145 in 23; 8 pieces
 // of 64 to 512 behind 4096: 251 whole, 125 in 3, 129 in 4, 136 in 6; 3 x 2048, causal: 69 whole, 81 in 2; 16 queries behind
 // 65536: 164 in 8, 35 in 64.  Shares of 256 keys at least: 2048 queries, causal, 45.4 us, 43.8 so; of 512: 64 behind 8192 24.2, 22.3 so.
-int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t hq, int64_t hkv, int64_t d) {
+// Their parts' way to memory and back makes more of them dear (8 x 3339, 2 heads of 256: 231 us whole, 280 in 2), less
+// so where rows are short, whose number is rounded (8192 queries of 8 heads of 64: 130 whole, 122 in 2). Where few
+// rows leave most places empty a long sequence among short ones, which the mean hides, has up to 4 (5 of 531 to 2125, 2 heads of
+// 32: 35 us, 19 so).
+int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t last, int64_t hq, int64_t hkv, int64_t d) {
   const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 3 : 4);
   // half a workgroup more a sequence, for its last rows
-  const int64_t units = (total * (hq / hkv) / kRows + (nseq + 1) / 2) * hkv, want = places / units, most = keys / 384;
+  const int64_t units = (total * (hq / hkv) / kRows + (nseq + 1) / 2) * hkv, want = (places + (d > 64 ? 0 : units / 2)) / units;
+  int64_t most = keys / 384;
+  if (4 * units <= places && most < 4) most = last / 192 < 4 ? last / 192 : 4;
   const int64_t n = want < most ? want : most;
   return static_cast<int>(n < 1 ? 1 : n > kMaxSplits ? kMaxSplits : n);
 }
@@ -520,7 +526,7 @@ extern "C" size_t bllm_attention_workspace(int64_t nseq, int64_t total, int64_t 
   if (nseq < 1 || nseq > kMaxSeqs || total < 0 || total > kMaxTokens || total_k < 0 || total_k > kMaxTokens ||
       heads_check(hq, hkv, d) != BLLM_OK)
     return 0;
-  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, hq, hkv, d), d);
+  return shares_bytes(total * hq, splits_of(nseq, total, total_k / nseq, total_k / nseq, hq, hkv, d), d);
 }
 
 extern "C" int bllm_attention(const void* q, const void* k, const void* v, int dtype, const int64_t* offsets,
@@ -558,10 +564,12 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   a.d = static_cast<int>(d);
   a.inv_group = 1.0 / a.group;
   a.small_inv = ((1u << 21) + a.group - 1) / a.group;
-  // keys that a query sees in the mean; a window alone bounds them, with the workgroup's others
+  // keys that a sequence's last query sees and its queries in the mean; a window alone bounds them, with the workgroup's others
+  int64_t last = total_k / nseq;
+  if (a.mask.window && !prefix && a.mask.window + kRows < last) last = a.mask.window + kRows;
   int64_t keys = total_k / nseq - (causal ? total / nseq / 2 : 0);
-  if (a.mask.window && !prefix && a.mask.window + kRows < keys) keys = a.mask.window + kRows;
-  const int splits = splits_of(nseq, total, keys, hq, hkv, d);
+  if (last < keys) keys = last;
+  const int splits = splits_of(nseq, total, keys, last, hq, hkv, d);
   if (ws_bytes < shares_bytes(total * hq, splits, d)) return BLLM_E_WS;  // not so: fewer keys take no more shares
   a.shares = shares_at(ws, total * hq, splits);
   hipStream_t st = static_cast<hipStream_t>(stream);
