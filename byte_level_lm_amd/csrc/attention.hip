@@ -53,6 +53,7 @@ struct AttArgs {
   double inv_group;              // 1 / group
   uint32_t small_inv;            // 2^21 / group, rounded up
   int nseq, hq, hkv, group, d;
+  int ranked;                    // units of work in the order of their rows' place in a sequence, the last first
   Mask mask;
   Shares shares;
 };
@@ -131,6 +132,39 @@ __device__ inline int find_rows(const AttArgs& a, int64_t slot, int64_t* t0, int
   return s;
 }
 
+// The sequence and the block of rows that come at place `at` where the blocks of up to 63
+// sequences are ordered by their index, the highest first (-1: no block).  place_of(b) blocks have an index of b or more.
+__device__ inline int find_ranked(const AttArgs& a, int64_t at, int* block, int64_t* t0, int64_t* t1, int64_t* k0, int64_t* k1) {
+  const auto cut = [](int64_t v, int64_t most) { return min(max(v, int64_t(0)), most); };
+  const int i = min(lane_id(), a.nseq), next = min(lane_id() + 1, a.nseq);
+  const int64_t off = cut(a.offsets[i], a.total), end = max(cut(a.offsets[next], a.total), off);
+  const int64_t k_off = cut(a.k_offsets[i], a.total_k), k_end = max(cut(a.k_offsets[next], a.total_k), k_off);
+  const int blocks = static_cast<int>(((end - off) * a.group + kRows - 1) / kRows);
+  const auto place_of = [&](int b) {
+    int sum;
+    wave_incl_scan(max(blocks - b, 0), sum);
+    return sum;
+  };
+  if (at >= place_of(0)) return -1;
+  int lo = 0, hi = static_cast<int>(a.slots);  // place_of(lo) > at >= place_of(hi)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (place_of(mid) > at) lo = mid; else hi = mid;
+  }
+  // of the sequences with such a block the one that is the rest's; scans and ballots with every lane
+  const int64_t rest = at - place_of(lo + 1);
+  const uint64_t with = __ballot(blocks > lo);
+  const uint64_t its = __ballot((blocks > lo) & (lanes_below(with) == rest));
+  if (its == 0) return -1;
+  const int s = static_cast<int>(__builtin_ctzll(its));
+  *block = lo;
+  *t0 = lane_value(off, s);
+  *t1 = lane_value(end, s);
+  *k0 = lane_value(k_off, s);
+  *k1 = lane_value(k_end, s);
+  return s;
+}
+
 // A query on its own, where v has values that are not finite: products with a
 // weight of zero would carry them to queries that do not see their keys.  A
 // wave takes 64 keys at a time, a lane a key, then a lane four columns of v.
@@ -190,7 +224,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   // each other, of these a sequence's, the last queries (with the most keys) first.
   uint32_t unit = blockIdx.x;
   {
-    const uint32_t full = a.units / (kRun * kXcds) * (kRun * kXcds);
+    const uint32_t full = a.ranked ? 0 : a.units / (kRun * kXcds) * (kRun * kXcds);
     if (unit < full) {
       const uint32_t in = unit % (kRun * kXcds);
       unit += (in % kXcds) * kRun + in / kXcds - in;
@@ -198,16 +232,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   }
   const int split = SPLIT ? static_cast<int>(unit % a.shares.splits) : 0;
   if (SPLIT) unit /= a.shares.splits;
-  const uint32_t kh = unit / a.slots;
-  const int64_t slot = a.first + (unit - kh * a.slots);
+  const uint32_t kh = a.ranked ? unit % a.hkv : unit / a.slots;
+  const int64_t slot = a.ranked ? unit / a.hkv : a.first + (unit - kh * a.slots);
   int64_t t0, t1, k0, k1;
-  const int s = find_rows(a, slot, &t0, &t1, &k0, &k1);
+  int block = 0;
+  const int s = a.ranked ? find_ranked(a, slot, &block, &t0, &t1, &k0, &k1) : find_rows(a, slot, &t0, &t1, &k0, &k1);
+  if (s < 0) return;
   const int n = static_cast<int>(t1 - t0), keys = static_cast<int>(k1 - k0);
   // the sequence's rows: a query's heads of this key head, then the next query's
   const int64_t rows = static_cast<int64_t>(n) * a.group;
   const int64_t back = slot - (t0 * a.group / kRows + s), blocks = (rows + kRows - 1) / kRows;
-  if (back < 0 || back >= blocks) return;
-  const int64_t first = (blocks - 1 - back) * kRows;     // below 2^40: the product below is off by less than half of 1 / group
+  if (!a.ranked && (back < 0 || back >= blocks)) return;
+  const int64_t first = (a.ranked ? block : blocks - 1 - back) * kRows;  // below 2^40: the product below is off by less than half of 1 / group
   const int left = static_cast<int>(min(rows - first, int64_t(kRows)));
   const int query0 = uniform(static_cast<int>((static_cast<double>(first) + 0.5) * a.inv_group));
   const int rest = static_cast<int>(first - static_cast<int64_t>(query0) * a.group);
@@ -504,6 +540,14 @@ void launch(AttArgs a, hipStream_t st) {
   for (a.first = 0; a.first < slots; a.first += most) {
     a.slots = static_cast<uint32_t>(slots - a.first < most ? slots - a.first : most);
     a.units = static_cast<uint32_t>(a.slots * each);
+    // Causal prompts, whose last queries see the most keys, in the order of these, so that none of them begins
+    // late and no CU has several: 4 x 2048, 12 heads on 4 of 128, 75 us in order of the sequences, 64 so; 55 of up to 1320, 3 heads of 64,
+    // cap and slopes, 73 and 47; 16 x 2048, d 256, 363 and 341.  With more units neighbours' keys in L2 count for more
+    // (32 x 2048 chunks 437, 445 so), with fewer than CUs the search (2 x 2260, 2 heads of 64: 20.6, 22.8 so), and
+    // behind many keys all last equally long (8 of 200 to 256 behind 4096: 41.3, 45.7 so).
+    constexpr uint32_t kPlaces = 256 * (D == 256 ? 2 : D == 128 ? 3 : 4);
+    a.ranked = a.mask.causal && !a.mask.window && a.nseq < kWave && slots <= most && a.units <= 4096 && 5 * a.units >= 2 * kPlaces &&
+               2 * a.total >= a.total_k;
     if (a.shares.splits > 1)
       launch_as<D, true>(a, st);
     else

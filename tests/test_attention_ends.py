@@ -297,3 +297,18 @@ def test_steps_and_prompts_of_many_shares_in_a_graph(B):
         pq.copy_(_dev16(_bf16(rng, (5, 4, 64))))
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(outs, both()))
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 8, 4), (128, 6, 2), (200, 4, 2)])
+@pytest.mark.parametrize("more", [{}, {"prefix": 300}, {"cap": 4.0, "slopes": True}], ids=lambda m: "-".join(m) or "plain")
+def test_many_blocks_of_ragged_prompts(B, d, hq, hkv, more):
+    """Prompts whose blocks are taken in the order of their place, with empty and single ones among them, up to 63 of them."""
+    from tests.test_gpu_attention import _mask
+    rng = np.random.default_rng(d + hq)
+    lengths = np.concatenate([[0, 900, 1, 0, 130, 128, 700, 0], rng.integers(0, 300, 54), [0]])
+    assert len(lengths) == 63
+    off = _offsets(lengths)
+    q, k, v = (_bf16(rng, (int(off[-1]), h, d)) for h in (hq, hkv, hkv))
+    host, dev = _mask(more, rng, len(lengths), hq)
+    want = oracle.attention(q, k, v, off, sizes=True, **host)
+    _check(B.attention(_dev16(q), *_strided(k, v), to_dev(off), **dev), want, 2.0 ** -8, d, host.get("slopes"), 900)
