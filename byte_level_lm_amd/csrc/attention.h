@@ -132,10 +132,10 @@ __host__ __device__ inline int join_lanes(int d) { return d <= 32 ? 8 : d <= 64 
 // lanes take the shares in turn; one has up to 64 of them, four are the workgroup.  Each of threads_to_join's
 // sides: 61 streams of 5 shares, 8 heads of 64: 18.4 us in lanes, 19.9 in waves; 4 pieces of 64 to 512 queries of 8
 // heads of 64 behind 8192 keys, 11 shares: 41 in waves, 54 in workgroups; 8 queries of 256 shares (262144 positions, one
-// key head): 31 in workgroups, 71 in the 64 shares that a wave can join.  True where scores were finite and an output is not.
+// key head): 31 in workgroups, 71 in the 64 shares that a wave can join.
 constexpr int kFewSplits = 8;
 
-__device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int d, uint16_t* o) {
+__device__ inline void join_few(const Shares& sh, int64_t query, bool mine, int d, uint16_t* o) {
   const int lanes = join_lanes(d), in = lane_id() & (lanes - 1), col = 4 * in, first = lane_id() - in;
   if (!mine) query = 0;
   const float2 st = in < sh.splits ? sh.stat[query * sh.splits + in] : make_float2(-INFINITY, 0.0f);
@@ -163,16 +163,13 @@ __device__ inline bool join_few(const Shares& sh, int64_t query, bool mine, int 
       y[2] = some ? fmaf(w, v[i].z, y[2]) : y[2];
       y[3] = some ? fmaf(w, v[i].w, y[3]) : y[3];
     }
-  mine = mine && col < d;
-  const bool odd = mine && (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(sum) < INFINITY;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
-  if (mine) *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-  return odd;
+  if (mine && col < d) *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
 }
 
 template <int WAVES>
-__device__ inline bool join_many(const Shares& sh, int64_t query, int d, uint16_t* o) {
+__device__ inline void join_many(const Shares& sh, int64_t query, int d, uint16_t* o) {
   __shared__ float sO[WAVES][256];
   __shared__ float2 sStat[WAVES];
   // a wave's share i is share w + WAVES i of the query's
@@ -214,7 +211,7 @@ __device__ inline bool join_many(const Shares& sh, int64_t query, int d, uint16_
     if (mine && lane < lanes) *reinterpret_cast<float4*>(&sO[w][col]) = make_float4(y[0], y[1], y[2], y[3]);
     if (lane == 0) sStat[w] = make_float2(top, sum);
     __syncthreads();
-    if (w > 0) return false;
+    if (w > 0) return;
     float all = -INFINITY;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) all = sStat[i].y == 0.0f ? all : fmaxf(all, sStat[i].x);
@@ -231,12 +228,10 @@ __device__ inline bool join_many(const Shares& sh, int64_t query, int d, uint16_
       y[3] = fmaf(f, v.w, y[3]);
     }
   }
-  if (!mine || lane >= lanes) return false;
-  const bool odd = (y[0] + y[1] + y[2] + y[3]) * 0.0f != 0.0f && fabsf(l) < INFINITY;
+  if (!mine || lane >= lanes) return;
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = l == 0.0f ? 0.0f : y[e] / l;
   *reinterpret_cast<uint2*>(o + query * d + col) = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
-  return odd;
 }
 
 // Threads for each query of a join: join_lanes(d) of them, a wave or a workgroup of 256.
@@ -249,9 +244,11 @@ __device__ inline int64_t joined_query(int d) {
   return (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / (THREADS ? THREADS : join_lanes(d));
 }
 template <int THREADS>
-__device__ inline bool join(const Shares& sh, int64_t query, bool there, int d, uint16_t* o) {
-  if (THREADS == 0) return join_few(sh, query, there, d, o);
-  return there && join_many<THREADS == 256 ? 4 : 1>(sh, query, d, o);
+__device__ inline void join(const Shares& sh, int64_t query, bool there, int d, uint16_t* o) {
+  if (THREADS == 0)
+    join_few(sh, query, there, d, o);
+  else if (there)
+    join_many<THREADS == 256 ? 4 : 1>(sh, query, d, o);
 }
 
 // A launch by its function, without the call configuration of <<<>>>, which costs the host 0.2 of 3.4 us.  Arguments cost

@@ -165,46 +165,9 @@ __device__ inline int find_ranked(const AttArgs& a, int64_t at, int* block, int6
   return s;
 }
 
-// A query on its own, where v has values that are not finite: products with a
-// weight of zero would carry them to queries that do not see their keys.  A
-// wave takes 64 keys at a time, a lane a key, then a lane four columns of v.
-__device__ inline void query_alone(const AttArgs& a, int64_t row, int h, int64_t k0, int t, Sight see, float slope) {
-  const int lane = lane_id(), kh = h / a.group, d = a.d;
-  const uint16_t* q = a.q + row * a.q_stride + static_cast<int64_t>(h) * d;
-  float m = -INFINITY, l = 0.0f, o[4] = {};
-  for (int j0 = 0; j0 <= max(see.hi, see.front - 1); j0 += kWave) {
-    const int j = j0 + lane;
-    const bool has = see.has(j);
-    if (!__ballot(has)) continue;
-    float x = -INFINITY;
-    if (has) {
-      const uint16_t* k = a.k + (k0 + j) * a.k_stride + static_cast<int64_t>(kh) * d;
-      x = 0.0f;
-      for (int c = 0; c < d; ++c) x = fmaf(bf16_to_f32(q[c]), bf16_to_f32(k[c]), x);
-      x *= a.mask.scale;
-      if (a.mask.cap > 0.0f) x = capped(x, a.mask.cap, 2.0f * kLog2e / a.mask.cap);
-      x = (x - slope * static_cast<float>(abs(t - j))) * kLog2e;
-    }
-    float top = x;
-    for (int off = 32; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, kWave));
-    const float now = fmaxf(m, top), base = now == -INFINITY ? 0.0f : now, fall = exp2_fast(m - base);
-    const float p = exp2_fast(x - base);
-    l = l * fall + wave_sum(p);
-    m = now;
-    for (int e = 0; e < 4; ++e) o[e] *= fall;
-    for (int n = 0; n < kWave; ++n) {
-      if (!see.has(j0 + n)) continue;
-      const float w = __shfl(p, n, kWave);
-      const uint16_t* v = a.v + (k0 + j0 + n) * a.v_stride + static_cast<int64_t>(kh) * d + 4 * lane;
-      if (4 * lane < d)
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(w, bf16_to_f32(v[e]), o[e]);
-    }
-  }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (4 * lane < d)
-    *reinterpret_cast<uint2*>(a.o + (row * a.hq + h) * d + 4 * lane) =
-        make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
-}
+// an infinity or a NaN, of a bf16 value and in a pair of them
+__device__ inline bool not_finite(uint32_t v) { return (v & 0x7F80u) == 0x7F80u; }
+__device__ inline bool pair_not_finite(uint32_t v) { return not_finite(v) || not_finite(v >> 16); }
 
 // GEN: with a cap or slopes (their branches alone: 32 x 2048 chunks 469 us, 445 without).  SPLIT: a
 // share of the tiles, to be joined.  Three workgroups a CU with d = 128 take 458 us, two 500; a fourth has no registers.
@@ -321,7 +284,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
                                                   e ? x : floatx16{}, 0, 0, 0);
   };
   // scores of 32 keys made ready, and the maximum that their weights are taken against
-  const auto ready = [&](int j0, floatx16& x) __attribute__((always_inline)) {
+  const auto ready = [&](int j0, floatx16& x, float slack) __attribute__((always_inline)) {
     if (GEN) {  // the product becomes x: capped as in capped(), then lowered by the distance
       if (cap2 != 0.0f) {
 #pragma unroll
@@ -360,7 +323,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
 #pragma unroll
     for (int r = 0; r < 5; ++r) z[r] = fmaxf(fmaxf(x[3 * r], x[3 * r + 1]), x[3 * r + 2]);
     const float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), z[2]), fmaxf(fmaxf(z[3], z[4]), x[15])) * c1;
-    if (__any(top > m + kSlack)) {
+    if (__any(top > m + slack)) {
       const float now = fmaxf(m, max_xor32(top));
       base = now == -INFINITY ? 0.0f : now;
       const float fall = exp2_fast(m - base);
@@ -392,8 +355,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   };
   // some query of the wave sees a key of the tile?
   const auto sees = [&](int j0) { return j0 < seen0 || (j0 >= seen1 && j0 <= seen2); };
+  // the first key of the i-th tile
+  const auto tile_at = [&](int i) {
+    const int j = (begin + i) * BN;
+    return j < ahead ? j : from + j - ahead;
+  };
   // the tile that the loads are at; its first row of k and v
-  int j1 = begin * BN < ahead ? begin * BN : from + begin * BN - ahead;
+  int j1 = tile_at(0);
   const char *kj = kb + static_cast<int64_t>(j1) * kbytes, *vj = vb + static_cast<int64_t>(j1) * vbytes;
   const auto load_next = [&](uint16_t* K, uint16_t* V) __attribute__((always_inline)) {
     const int rows = min(keys - j1, BN);
@@ -416,22 +384,23 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
       floatx16 x;
       uint32_t p[8];
       products(cK, x);
-      ready(j0, x);
+      ready(j0, x, kSlack);
       weigh(x, p);
       apply(p, cV);
     }
   };
-  if (tiles > 0) load_next(sK0, sV0);
-  // the queries behind them, negated for a negative scale, so that the largest product has the largest score
-  {
-    const uint16_t* q = a.q + (t0 + query) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * half;
+  // the queries, negated for a negative scale, so that the largest product has the largest score
+  const auto load_queries = [&](int part, int query, int h) __attribute__((always_inline)) {
+    const uint16_t* q = a.q + (t0 + query) * a.q_stride + static_cast<int64_t>(h) * a.d + 8 * part;
     const uint32_t sign = a.mask.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
-      const uint4 z = mine && 16 * i + 8 * half < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
+      const uint4 z = mine && 16 * i + 8 * part < a.d ? *reinterpret_cast<const uint4*>(q + 16 * i) : make_uint4(0, 0, 0, 0);
       fq[i] = as_frag(make_uint4(z.x ^ sign, z.y ^ sign, z.z ^ sign, z.w ^ sign));
     }
-  }
+  };
+  if (tiles > 0) load_next(sK0, sV0);
+  load_queries(half, query, h);  // behind the first keys
   for (int i = 0; i < tiles; i += 2) {
     step(i + 1 < tiles, sK1, sV1, sK0, sV0);
     if (i + 1 < tiles) step(i + 2 < tiles, sK0, sV0, sK1, sV1);
@@ -439,6 +408,108 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   if (!some) return;
 
   l = sum_xor32(l);
+  // Scores were finite and outputs are not: v has values that are not.  In a tile that every query of the wave sees
+  // whole they belong in the outputs; in one with an edge they may have met the weight of zero of a
+  // query that does not see their key (0 x infinity is NaN).  Then the wave takes its tiles once more by itself,
+  // straight from memory (a call of which every wave does 4 to 15 times as long, one with a NaN in its first rows 1.1 to 1.5
+  // times), in the same order and with the same weights: queries which do not see such values have the
+  // bits that they have without them.  With no such value sums have passed fp32: once more with weights of 1 at most.
+  float odd = 0.0f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) odd = fmaf(o[b][r], 0.0f, odd);  // 0 x infinity and 0 x NaN are NaN
+  odd = sum_xor32(odd);
+  if (__any(mine && odd != 0.0f && fabsf(l) < INFINITY)) {
+    int me = lane;
+    __asm__ volatile("" : "+v"(me));  // the loop above keeps no register for what follows, the queries neither (d 256: 335 us, 387 and 421 else)
+    const int row = me & 31, part = me >> 5;
+    const uint16_t *kr = a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * a.d, *vr0 = a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * a.d;
+    bool belong = false, again = false;
+    for (int i = 0; i < tiles && !again; ++i) {
+      const int j0 = tile_at(i);
+      const bool whole = j0 >= whole0 && j0 <= whole1;
+      if (!sees(j0) || (whole && belong)) continue;
+      bool bad = false;
+      for (int c = me; c < BN * a.d / 8; c += 64) {
+        const int r = c / (a.d / 8), col = 8 * (c - r * (a.d / 8));
+        if (j0 + r >= keys) break;
+        const uint4 z = *reinterpret_cast<const uint4*>(vr0 + static_cast<int64_t>(j0 + r) * a.v_stride + col);
+        bad = bad || pair_not_finite(z.x) || pair_not_finite(z.y) || pair_not_finite(z.z) || pair_not_finite(z.w);
+      }
+      if (__any(bad)) (whole ? belong : again) = true;
+    }
+    if (again || !belong) {
+      const int qu = query_of(r0 + row);
+      load_queries(part, qu, head_of(r0 + row, qu));
+      m = -INFINITY;
+      base = l = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) o[b] = floatx16{};
+      for (int i = 0; i < tiles; ++i) {
+        const int j0 = tile_at(i);
+        if (!sees(j0)) continue;
+        int d = a.d, v_stride = static_cast<int>(a.v_stride);
+        __asm__ volatile("" : "+s"(d), "+s"(v_stride));  // or every place of a tile's values would be held across the loop
+        floatx16 x;
+        uint32_t p[8];
+        const uint16_t* kt = kr + static_cast<int64_t>(min(j0 + row, keys - 1)) * a.k_stride + 8 * part;
+#pragma unroll
+        for (int e = 0; e < NS; ++e) {
+          const uint4 z = 16 * e + 8 * part < d ? *reinterpret_cast<const uint4*>(kt + 16 * e) : make_uint4(0, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_frag(z), fq[e], e ? x : floatx16{}, 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        ready(j0, x, again ? kSlack : 0.0f);
+        weigh(x, p);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // 16 keys, of which the lane has 4 half + {0 .. 3} and 8 more on
+          const int jh = j0 + 16 * e + 4 * part;
+          const uint16_t* vt = vr0 + static_cast<int64_t>(min(jh, keys - 1)) * a.v_stride;
+          const int last = keys - 1 - jh;  // a tile's last keys may not be there
+          uint32_t none[4];  // 1 for keys that the query sees with a weight of zero
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int jr = jh + 8 * (r / 2) + 2 * (r % 2);
+            none[r] = ((p[4 * e + r] & 0xFFFFu) == 0 && see.has(jr) ? 0x3F80u : 0u) | (p[4 * e + r] >> 16 == 0 && see.has(jr + 1) ? 0x3F800000u : 0u);
+          }
+          const bf16x8 fp = as_frag(make_uint4(p[4 * e], p[4 * e + 1], p[4 * e + 2], p[4 * e + 3]));
+          const bf16x8 fn = as_frag(make_uint4(none[0], none[1], none[2], none[3]));
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            // a column of v in pairs of keys: its finite values, and 1 for those that are up (infinity, NaN), down (-infinity,
+            // NaN) and either.  In whole words and with every load made: with branches the registers spill
+            const int c = 32 * b + row;
+            uint32_t f[4], up[4], down[4], bad[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              const int j = 8 * (n / 2) + 2 * (n % 2), col = min(c, d - 1);
+              const uint32_t lo = vt[max(min(j, last), 0) * v_stride + col], hi = vt[max(min(j + 1, last), 0) * v_stride + col];
+              const uint32_t in = c < d ? (j <= last ? 0xFFFFu : 0u) | (j + 1 <= last ? 0xFFFF0000u : 0u) : 0u, v = (lo | hi << 16) & in;
+              const uint32_t odd = (((v & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u, sign = v >> 15 & 0x00010001u;
+              const uint32_t nan = (((v & 0x007F007Fu) + 0x007F007Fu) >> 7) & 0x00010001u;
+              f[n] = v & ~(odd * 0xFFFFu);
+              up[n] = (odd & (nan | ~sign)) * 0x3F80u;
+              down[n] = (odd & (nan | sign)) * 0x3F80u;
+              bad[n] = odd * 0x3F80u;
+            }
+            const auto frag = [](const uint32_t (&z)[4]) { return as_frag(make_uint4(z[0], z[1], z[2], z[3])); };
+            o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(f), fp, o[b], 0, 0, 0);
+            const auto meet = [&](const uint32_t (&z)[4], bf16x8 w, float value) __attribute__((always_inline)) {
+              const floatx16 sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag(z), w, floatx16{}, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[b][r] = sum[r] > 0.0f ? o[b][r] + value : o[b][r];
+              __builtin_amdgcn_sched_barrier(0);
+            };
+            meet(up, fp, INFINITY);
+            meet(down, fp, -INFINITY);
+            meet(bad, fn, NAN);  // zero times it
+          }
+        }
+      }
+      l = sum_xor32(l);
+    }
+  }
   if (SPLIT) {
     if (mine) {
       const int64_t at = ((t0 + query) * a.hq + h) * a.shares.splits + split;
@@ -454,12 +525,6 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
     return;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  float odd = 0.0f;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) odd = fmaf(o[b][r], 0.0f, odd);  // 0 x infinity and 0 x NaN are NaN
-  odd = sum_xor32(odd);
   // lanes of the lower half take columns 0 .. 7 of each 16, of the upper half 8 .. 15
   uint16_t* out = a.o + ((t0 + query) * a.hq + h) * a.d + 8 * half;
 #pragma unroll
@@ -474,37 +539,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
       if (mine && 32 * b + 16 * e + 8 * half < a.d)
         *reinterpret_cast<uint4*>(out + 32 * b + 16 * e) = make_uint4(u[0], v[0], u[1], v[1]);
     }
-  // scores were finite and outputs are not: those queries once more, one by one
-  uint64_t again = __ballot(half == 0 && mine && odd != 0.0f && fabsf(l) < INFINITY);
-  if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores above
-  while (again) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    const int qs = query_of(r0 + i), hs = head_of(r0 + i, qs);
-    query_alone(a, t0 + qs, hs, k0, qs + shift, sight(a.mask, qs + shift, keys, front), a.mask.slopes ? a.mask.slopes[hs] : 0.0f);
-  }
 }
 
 template <int THREADS>
 __global__ __launch_bounds__(256) void prompt_join(AttArgs a) {
   const int64_t query = joined_query<THREADS>(a.d), row = query / a.hq;
   const bool mine = row < a.total && row >= a.offsets[0] && row < a.offsets[a.nseq];
-  uint64_t again = __ballot(join<THREADS>(a.shares, query, mine, a.d, a.o));
-  if (again) __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "workgroup");  // behind the stores of the join
-  while (again) {  // scores were finite and outputs are not: those queries once more, one by one
-    const int64_t first = lane_value(query, __builtin_ctzll(again));
-    again &= ~__ballot(query == first);
-    const int64_t r = first / a.hq;
-    const int h = static_cast<int>(first - r * a.hq);
-    const int s = uniform(wave_find(a.nseq, r, [&](int i) { return a.offsets[i]; }));
-    int64_t t0, t1, k0, k1;
-    seq_rows(a.offsets, s, a.total, &t0, &t1);
-    seq_rows(a.k_offsets, s, a.total_k, &k0, &k1);
-    if (r < t0 || r >= t1) continue;
-    const int keys = static_cast<int>(k1 - k0), t = static_cast<int>(r - t0 + keys - (t1 - t0));
-    const int front = a.mask.prefix ? min(max(a.mask.prefix[s], 0), keys) : 0;
-    query_alone(a, r, h, k0, t, sight(a.mask, t, keys, front), a.mask.slopes ? a.mask.slopes[h] : 0.0f);
-  }
+  join<THREADS>(a.shares, query, mine, a.d, a.o);
 }
 
 // Shares of a query's keys, of 384 or more in the mean: as many as the workgroups of whole queries
