@@ -252,12 +252,18 @@ __device__ inline void join(const Shares& sh, int64_t query, bool there, int d, 
 }
 
 // A launch by its function, without the call configuration of <<<>>>, which costs the host 0.2 of 3.4 us.  Arguments cost
-// it too, 0.35 us for 100 bytes, and 256 more of them go along where a kernel asks for gridDim.
+// it too, 0.35 us for 100 bytes, and 256 more of them go along where a kernel asks for gridDim.  False where it failed:
+// then the call launches nothing more.
 template <typename Args>
-inline void launch_kernel(void (*kernel)(Args), int64_t groups, int64_t rows, int threads, hipStream_t st, Args a) {
+inline bool launch_kernel(void (*kernel)(Args), int64_t groups, int64_t rows, int threads, hipStream_t st, Args a) {
   void* args[] = {&a};
-  (void)hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<unsigned>(groups), static_cast<unsigned>(rows)),
-                        dim3(static_cast<unsigned>(threads)), args, 0, st);
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3(static_cast<unsigned>(groups), static_cast<unsigned>(rows)),
+                         dim3(static_cast<unsigned>(threads)), args, 0, st) == hipSuccess;
+}
+// a call's result; the runtime's error is taken either way
+inline int launched(bool all) {
+  const int status = launch_status();
+  return all ? status : BLLM_E_HIP;
 }
 
 inline bool page_shift(int64_t page, int* shift) {

@@ -568,13 +568,13 @@ int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t last, int64_t h
 }
 
 template <int D, bool SPLIT>
-void launch_as(const AttArgs& a, hipStream_t st) {
-  launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? prompt_tiles<D, true, SPLIT> : prompt_tiles<D, false, SPLIT>, a.units, 1,
-                64 * kWaves, st, a);
+bool launch_as(const AttArgs& a, hipStream_t st) {
+  return launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? prompt_tiles<D, true, SPLIT> : prompt_tiles<D, false, SPLIT>, a.units, 1,
+                       64 * kWaves, st, a);
 }
 
 template <int D>
-void launch(AttArgs a, hipStream_t st) {
+bool launch(AttArgs a, hipStream_t st) {
   constexpr int64_t kMost = (int64_t(1) << 32) / (64 * kWaves) - 1;  // workgroups that one launch has threads for
   const int64_t slots = a.total * a.group / kRows + a.nseq;  // sequence s has slots offsets[s] * group / kRows + s and on
   const int64_t each = static_cast<int64_t>(a.hkv) * a.shares.splits, most = kMost / each;
@@ -589,16 +589,13 @@ void launch(AttArgs a, hipStream_t st) {
     constexpr uint32_t kPlaces = 256 * (D == 256 ? 2 : D == 128 ? 3 : 4);
     a.ranked = a.mask.causal && !a.mask.window && a.nseq < kWave && slots <= most && a.units <= 4096 && 5 * a.units >= 2 * kPlaces &&
                2 * a.total >= a.total_k;
-    if (a.shares.splits > 1)
-      launch_as<D, true>(a, st);
-    else
-      launch_as<D, false>(a, st);
+    if (!(a.shares.splits > 1 ? launch_as<D, true>(a, st) : launch_as<D, false>(a, st))) return false;
   }
-  if (a.shares.splits > 1) {  // few queries, by the rule of splits_of
-    const int threads = threads_to_join(a.shares, a.total * a.hq, a.d);
-    launch_kernel(a.shares.splits <= kFewSplits ? prompt_join<0> : threads == kWave ? prompt_join<kWave> : prompt_join<256>,
-                  ceil_div(a.total * a.hq * threads, 256), 1, 256, st, a);
-  }
+  if (a.shares.splits == 1) return true;
+  // few queries, by the rule of splits_of
+  const int threads = threads_to_join(a.shares, a.total * a.hq, a.d);
+  return launch_kernel(a.shares.splits <= kFewSplits ? prompt_join<0> : threads == kWave ? prompt_join<kWave> : prompt_join<256>,
+                       ceil_div(a.total * a.hq * threads, 256), 1, 256, st, a);
 }
 
 }  // namespace
@@ -658,11 +655,5 @@ extern "C" int bllm_attention(const void* q, const void* k, const void* v, int d
   if (ws_bytes < shares_bytes(total * hq, splits, d)) return BLLM_E_WS;  // not so: fewer keys take no more shares
   a.shares = shares_at(ws, total * hq, splits);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (d <= 64)
-    launch<64>(a, st);
-  else if (d <= 128)
-    launch<128>(a, st);
-  else
-    launch<256>(a, st);
-  return launch_status();
+  return launched(d <= 64 ? launch<64>(a, st) : d <= 128 ? launch<128>(a, st) : launch<256>(a, st));
 }

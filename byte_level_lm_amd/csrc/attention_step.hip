@@ -297,9 +297,9 @@ int splits_of(int64_t nseq, int64_t heads, int64_t positions, int64_t d) {
 }
 
 template <int D, bool Q8>
-void step_launch(const StepArgs& a, int64_t groups, int64_t nseq, hipStream_t st) {
-  launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? step_share<D, Q8, true> : step_share<D, Q8, false>, groups, nseq,
-                64 * kStepWaves, st, a);
+bool step_launch(const StepArgs& a, int64_t groups, int64_t nseq, hipStream_t st) {
+  return launch_kernel(a.mask.cap > 0.0f || a.mask.slopes ? step_share<D, Q8, true> : step_share<D, Q8, false>, groups, nseq,
+                       64 * kStepWaves, st, a);
 }
 
 }  // namespace
@@ -352,17 +352,18 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   const int64_t groups = hkv * a.blocks * a.shares.splits;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const bool q8 = pages_dtype == BLLM_I8;
+  bool all;
   if (d <= 64)
-    q8 ? step_launch<64, true>(a, groups, nseq, st) : step_launch<64, false>(a, groups, nseq, st);
+    all = q8 ? step_launch<64, true>(a, groups, nseq, st) : step_launch<64, false>(a, groups, nseq, st);
   else if (d <= 128)
-    q8 ? step_launch<128, true>(a, groups, nseq, st) : step_launch<128, false>(a, groups, nseq, st);
+    all = q8 ? step_launch<128, true>(a, groups, nseq, st) : step_launch<128, false>(a, groups, nseq, st);
   else
-    q8 ? step_launch<256, true>(a, groups, nseq, st) : step_launch<256, false>(a, groups, nseq, st);
+    all = q8 ? step_launch<256, true>(a, groups, nseq, st) : step_launch<256, false>(a, groups, nseq, st);
   const int64_t heads = nseq * hq;
-  if (a.shares.splits > 1) {
+  if (all && a.shares.splits > 1) {
     const int threads = threads_to_join(a.shares, heads, a.pages.d);
-    launch_kernel(a.shares.splits <= kFewSplits ? step_join<0> : threads == kWave ? step_join<kWave> : step_join<256>,
-                  ceil_div(heads * threads, 256), 1, 256, st, JoinArgs{a.shares, a.o, static_cast<int>(heads), a.pages.d});
+    all = launch_kernel(a.shares.splits <= kFewSplits ? step_join<0> : threads == kWave ? step_join<kWave> : step_join<256>,
+                        ceil_div(heads * threads, 256), 1, 256, st, JoinArgs{a.shares, a.o, static_cast<int>(heads), a.pages.d});
   }
-  return launch_status();
+  return launched(all);
 }

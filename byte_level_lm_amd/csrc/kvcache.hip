@@ -150,7 +150,7 @@ __global__ __launch_bounds__(kThreads) void kv_move(KvArgs a) {
 }
 
 template <bool WRITE, bool Q8>
-void launch_as(KvArgs a, hipStream_t st) {
+bool launch_as(KvArgs a, hipStream_t st) {
   const int pieces = a.pages.d / 8, g = pieces <= 8 ? 8 : pieces <= 16 ? 16 : 32;
   // tokens of a workgroup: two rounds of its loads (131072 tokens of 8-bit rows read: 95 us, one round
   // 96, four 100), less where that leaves CUs idle (32 tokens written: 3.5 us alone, 4.7 without this)
@@ -161,19 +161,15 @@ void launch_as(KvArgs a, hipStream_t st) {
   a.tile = static_cast<int>(tile < 1 ? 1 : tile > kMaxTile ? kMaxTile : tile);
   const int64_t tiles = ceil_div(a.total, a.tile);
   a.groups = static_cast<int>(tiles < (1 << 20) ? tiles : 1 << 20);
-  launch_kernel(g == 8 ? kv_move<WRITE, Q8, 8> : g == 16 ? kv_move<WRITE, Q8, 16> : kv_move<WRITE, Q8, 32>, a.groups, 1,
-                kThreads, st, a);
+  return launch_kernel(g == 8 ? kv_move<WRITE, Q8, 8> : g == 16 ? kv_move<WRITE, Q8, 16> : kv_move<WRITE, Q8, 32>, a.groups, 1,
+                       kThreads, st, a);
 }
 
 template <bool WRITE>
 int launch(const KvArgs& a, void* stream) {
   if (a.total == 0) return BLLM_OK;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (a.k_scale)
-    launch_as<WRITE, true>(a, st);
-  else
-    launch_as<WRITE, false>(a, st);
-  return launch_status();
+  return launched(a.k_scale ? launch_as<WRITE, true>(a, st) : launch_as<WRITE, false>(a, st));
 }
 
 }  // namespace
