@@ -38,6 +38,13 @@ struct StepArgs {
   Mask mask;
 };
 
+// scales lie on 4 bytes, no more; the load is as wide all the same
+__device__ inline floatx4 four_floats(const float* p) {
+  floatx4 v;
+  __builtin_memcpy(&v, p, sizeof(v));
+  return v;
+}
+
 // The tiles that the last query of a stream sees: those of keys [0, front), then from `skip` on those of [lo, n).
 struct Seen {
   int n, lo, front, first, skip, tiles;
@@ -118,8 +125,8 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void ste
     if (Q8) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        ks[b] = *reinterpret_cast<const floatx4*>(a.k_scale + row[b] + 4 * g);
-        vs[b] = *reinterpret_cast<const floatx4*>(a.v_scale + row[b] + 4 * g);
+        ks[b] = four_floats(a.k_scale + row[b] + 4 * g);
+        vs[b] = four_floats(a.v_scale + row[b] + 4 * g);
       }
     }
 #pragma unroll
