@@ -347,12 +347,14 @@ extern "C" int bllm_attention_step(const void* q, int dtype, int64_t nseq, int64
   a.hq = static_cast<int>(hq);
   a.group = static_cast<int>(hq / hkv);
   a.blocks = (a.group + 15) / 16;
-  // The positions that a query sees: a window bounds them but for a prefix, which is taken to be
-  // short where whole streams fill the CUs (window of 512, 61 streams of up to 8192, 8 heads of 64: with a prefix of 5
-  // 15.9 us so, 17.8 with shares for the whole cache; with one of 4096 57 and 42).  16 streams of 12
-  // heads on 4 of 128 with a prefix of 4096: 18.9 in shares, 61 whole.
+  // The positions that a query sees: a window bounds them but for a prefix, whose length only the device knows.  It is taken to be
+  // short where a row of each workgroup makes 48 KB: whole streams then read a long one at the cache's rate too (window of 512, 488
+  // key heads of 64 in bf16, prefixes of 32768: 642 us whole, 663 in shares; of 5: 14.8 and 17.4; ragged streams lose,
+  // with prefixes of up to 4096 56 and 49, up to 32768 373 and 265).  With fewer bytes they do not: 256 key heads of 64
+  // in 8 bits, prefixes of 32768: 392 whole, 210 in shares, ragged 328 and 117; of 5: 9.0 and 14.8.
   int64_t positions = cols * page;
-  if (a.mask.window && (!prefix || nseq * hkv * a.blocks >= 256) && window + 2 * kTile < positions) positions = window + 2 * kTile;
+  const int64_t row_bytes = nseq * hkv * a.blocks * d * (pages_dtype == BLLM_I8 ? 1 : 2);
+  if (a.mask.window && (!prefix || row_bytes >= 48 << 10) && window + 2 * kTile < positions) positions = window + 2 * kTile;
   const int splits = splits_of(nseq, hkv * a.blocks, positions, d);
   if (ws_bytes < shares_bytes(nseq * hq, splits, d)) return BLLM_E_WS;  // not so: fewer positions take no more shares
   a.shares = shares_at(ws, nseq * hq, splits);
