@@ -656,6 +656,8 @@ def _scratch(nbytes: int, ws, like):
         each = like.element_size()
         n = (nbytes + 15) // each
         return like.new_empty(n), n * each
+    if not ws.is_contiguous():  # its bytes are counted by its elements, which then need not lie side by side
+        raise ValueError("ws must be contiguous")
     return _ws(nbytes, ws, like.device), _nbytes(ws)
 
 
