@@ -682,7 +682,7 @@ def attention(q, k, v, offsets, *, k_offsets=None, scale=None, causal: bool = Tr
     """Softmax attention over a ragged batch: q [total, hq, d], k and v [total_k, hkv, d] (bf16, tokens may be
     strided), offsets int64 [nseq + 1] of the queries and k_offsets of the keys (the queries' own without).  The last
     query of a sequence stands at its last key.  Keys are seen up to the query's position (causal), nearer than
-    window, or below prefix[s] (int32 [nseq]).  Scores are scaled by scale (d ** -0.5), capped to
+    window, or below prefix[s] (int32 [nseq]), these also by queries in front of them.  Scores are scaled by scale (d ** -0.5), capped to
     cap * tanh(score / cap), and lowered by slopes[h] (fp32 [hq]) times the distance.  Returns o [total, hq, d];
     queries that see no key get zeros."""
     if q.dim() != 3 or k.dim() != 3:

@@ -583,6 +583,10 @@ int bllm_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
  * k_offsets: int64 [nseq+1] device, of the keys and values, or NULL: the
  *            queries' (then total_k = total).
  * prefix   : int32 [nseq] device or NULL;  slopes : fp32 [hq] device or NULL.
+ *            Queries in front of a key below prefix[s] see it too, causal or not, so that a prompt in pieces
+ *            has the rows of the whole one where its first piece holds the prefix.  First keys that
+ *            stay visible behind a window, but not ahead of themselves: the first prefix[s] tokens of a
+ *            sequence in a call without window and prefix, the others in one with both (as the step's are).
  * cap      : 0 (none) or 2^-10 .. 1024; capped scores are off by 2^-22 cap.
  * o_out    : bf16 [total x hq x d], dense.
  * ws       : bllm_attention_workspace(nseq, total, total_k, hq, hkv, d) bytes.

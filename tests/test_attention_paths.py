@@ -103,3 +103,27 @@ def test_a_step_of_many_heads_in_many_shares(B, d, q8, more):
     want = oracle.attention_step(q, *pages, table, lengths, k_scale=scales[0], v_scale=scales[1], sizes=True, **host)
     o = B.attention_step(_dev16(q), *dev, to_dev(table), to_dev(lengths), **sc, **dmask)
     _check(o, want, 2.0 ** -16, d, host.get("slopes"), 2112)
+
+
+def test_first_keys_that_stay_visible_behind_a_window_and_are_not_seen_ahead(B):
+    """The first tokens in a call of their own without window and prefix, the others with both; then a step."""
+    from oracle.attention import _attend
+    rng = np.random.default_rng(1)
+    n, first, window, d = 200, 30, 16, 64
+    q, k, v = (_bf16(rng, (n, 2, d)) for _ in range(3))
+    t = np.arange(n)
+    near = t[:, None] - t[None, :]
+    seen = (near >= 0) & ((near < window) | (t < first)[None, :])
+    want = [np.stack(x, 1) for x in zip(*(_attend(*(a[:, h].astype(np.float64) for a in (q, k, v)), t, seen, d ** -0.5, None, 0.0, t)
+                                          for h in range(2)))]
+    off = [to_dev(_offsets([x])) for x in (first, n - first, n)]
+    prefix = to_dev(np.array([first], np.int32))
+    o = [B.attention(*(_dev16(a[:first]) for a in (q, k, v)), off[0]),
+         B.attention(_dev16(q[first:]), _dev16(k), _dev16(v), off[1], k_offsets=off[2], window=window, prefix=prefix)]
+    _check(to_dev(np.concatenate([to_np(x).astype(np.float64) for x in o])), want, 2.0 ** -8, d)
+    table = to_dev(np.arange(-(-n // 16), dtype=np.int32)[None])
+    pools = [_dev16(np.zeros((table.shape[1], 2, 16, d), np.float32)) for _ in range(2)]
+    B.kv_write(_dev16(k), _dev16(v), *pools, table, offsets=off[2])
+    for at in (0, 10, first, n - 1):
+        one = B.attention_step(_dev16(q[at:at + 1]), *pools, table, to_dev(np.array([at + 1], np.int32)), window=window, prefix=prefix)
+        _check(one, [x[at:at + 1] for x in want], 2.0 ** -8, d)
