@@ -2,19 +2,23 @@
 //
 //   s_ij = scale q_i.k_j (capped, lowered by distance),  o_i = sum_j 2^{x_ij - m_i} v_j / sum_j 2^{x_ij - m_i},  x = s log2 e
 //
-// A workgroup has 128 rows, a wave 32 of them: queries with all heads of a key head (rows of one
-// head: 64 prompts of 75 to 300, 12 heads on 4, 33 us, 30 so; 16 x 2048, d 256, 388 and 366).  Tiles of 32 keys go
+// Times are medians of a call among others without a profiler; both sides of a choice were taken in one run on one card.
+//
+// A workgroup has 128 rows, a wave 32 of them: queries with all heads of a key head (29 us for 64 prompts of 75 to 300, 12
+// heads on 4; when workgroups had rows of one head it took a tenth longer, 16 x 2048 with d 256 6 %).  Tiles of 32 keys go
 // through LDS, two buffers of them filled without registers, in one pass with
 // the running maximum and sum.  With d = 128, 32 keys are 16 matrix instructions of
 // 32 x 32 x 16 (512 cycles) and 16 exponentials a lane with what they need (some 480) for a
 // wave, which three waves a SIMD run beside each other.  What bounds it then is the card's
-// power: 32 sequences of 2048 tokens, 12 heads on 4, causal: 440 us, 945 TFLOP/s, the
+// power: 32 sequences of 2048 tokens, 12 heads on 4, causal: 440 us, 940 TFLOP/s, the
 // matrix cores busy 48 % of the cycles at 1.65 to 1.85 GHz (the same instructions with less to
-// move, without the loads, run at 2.3).  With d = 64 it is a tile's way through a wave: window of 512
-// over 16 ragged sequences of up to 8192 bytes, 8 heads, 118 us, 637 TFLOP/s, 28 % matrix and 53 % vector
-// instructions.  With cap and slopes the latter: 8 pieces of 64 to 512 queries behind 4096 keys 118 us, 520 TFLOP/s.  Tried and
-// no faster: 256 rows a workgroup (489 and 130 us), 64 rows (514 and 119), 64 a wave (registers of one wave a SIMD), tiles of
-// 64 keys, the next tile's first product between this one's exponentials, the sum by
+// move, without the loads, run at 2.3).  With d = 64 vector instructions take 60 % of the cycles beside 38 % of matrix ones (the
+// same sequences 258 us, 800 TFLOP/s); a window of 512 over 16 ragged sequences of up to 8192 bytes, 8 heads, 121 us, 620
+// TFLOP/s, 52 % and 28 %, the rest a tile's way through a wave.  With d = 256 registers leave two waves a SIMD, which
+// wait for half of their time (16 x 2048, 8 heads on 2, 334 us, 820 TFLOP/s).  With cap and slopes, 8 pieces of 64 to 512 queries behind 4096
+// keys 118 us, 510 TFLOP/s: 60 us are vector instructions, and units of uneven length leave 1.7 waves a SIMD in the mean of 3.  Tried and
+// no faster, each against its kernel of then (438 to 489 us): 256 rows a workgroup (489), 64 rows (514), 64 a wave (registers of one
+// wave a SIMD), tiles of 64 keys, the next tile's first product between this one's exponentials, the sum by
 // a matrix instruction (480 us), priorities, loads two tiles ahead in three buffers (461 us; without
 // any loads 342, so that what they cost is the way into LDS, not its latency).
 //
@@ -35,12 +39,12 @@ typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr int kWaves = 4, kRows = 32 * kWaves;  // rows of a workgroup
 constexpr int BN = 32;           // keys of a tile
 constexpr int kXcds = 8;
-// Neighbouring workgroups that one XCD takes in a row, so that they share its L2: window of 512 117 us
-// (in order of the grid 124), 32 x 2048 chunks 445 (452); in runs of 256 an XCD ends late (16 x 2048, d 256: 423 us, 384).
+// Neighbouring workgroups that one XCD takes in a row, so that they share its L2: window of 512 121.5 us
+// (in order of the grid 125), 32 x 2048 chunks 440 (449); runs of 256 are no better (121).
 constexpr int kRun = 64;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset past every buffer: reads as zero
 // How far (log2) scores may pass the maximum that weights are taken against: weights up to 256
-// lose nothing, and O is scaled anew seldom (32 x 2048 chunks 445 us, 495 with 0).
+// lose nothing, and O is scaled anew seldom (32 x 2048 chunks 440 us, 492 with 0; window of 512 121 and 132).
 constexpr float kSlack = 8.0f;
 
 struct AttArgs {
@@ -169,8 +173,8 @@ __device__ inline int find_ranked(const AttArgs& a, int64_t at, int* block, int6
 __device__ inline bool not_finite(uint32_t v) { return (v & 0x7F80u) == 0x7F80u; }
 __device__ inline bool pair_not_finite(uint32_t v) { return not_finite(v) || not_finite(v >> 16); }
 
-// GEN: with a cap or slopes (their branches alone: 32 x 2048 chunks 469 us, 445 without).  SPLIT: a
-// share of the tiles, to be joined.  Three workgroups a CU with d = 128 take 458 us, two 500; a fourth has no registers.
+// GEN: with a cap or slopes (their branches alone: 32 x 2048 chunks 473 us, 440 without).  SPLIT: a
+// share of the tiles, to be joined.  Three workgroups a CU with d = 128 take 440 us, two 479; a fourth has no registers.
 template <int D, bool GEN, bool SPLIT>
 __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void prompt_tiles(AttArgs a) {
   constexpr int NS = D / 16;               // steps of the first product
@@ -333,7 +337,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
       for (int b = 0; b < NB; ++b) o[b] *= fall;
     }
   };
-  // their weights, and the second product
+  // their weights, and the second product.  Weights are rounded to bf16, and their sum is of the rounded ones: outputs of 32 x 2048
+  // chunks are off by 0.21 % of their norm, 0.16 % of which is their own rounding.  A second bf16 term of each weight, as the step has
+  // it, leaves the 0.16 % and takes another product: 621 us, 440 so (window of 512 156 and 119; d 64 370 and 256)
   const auto weigh = [&](const floatx16& x, uint32_t (&p)[8]) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -411,7 +417,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
   // Scores were finite and outputs are not: v has values that are not.  In a tile that every query of the wave sees
   // whole they belong in the outputs; in one with an edge they may have met the weight of zero of a
   // query that does not see their key (0 x infinity is NaN).  Then the wave takes its tiles once more by itself,
-  // straight from memory (a call of which every wave does 4 to 15 times as long, one with a NaN in its first rows 1.1 to 1.5
+  // straight from memory (a call of which every wave does 3 to 11 times as long, one with a NaN in its first rows 1.1 to 1.7
   // times), in the same order and with the same weights: queries which do not see such values have the
   // bits that they have without them.  With no such value sums have passed fp32: once more with weights of 1 at most.
   float odd = 0.0f;
@@ -550,13 +556,13 @@ __global__ __launch_bounds__(256) void prompt_join(AttArgs a) {
 
 // Shares of a query's keys, of 384 or more in the mean: as many as the workgroups of whole queries
 // find places for on the card (4, 3 or 2 a CU, by registers), since a few that begin late cost a round.
-// One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 125 us in 15 shares, 145 in 23; 8 pieces
-// of 64 to 512 behind 4096: 251 whole, 125 in 3, 129 in 4, 136 in 6; 3 x 2048, causal: 69 whole, 81 in 2; 16 queries behind
-// 65536: 164 in 8, 35 in 64.  Shares of 256 keys at least: 2048 queries, causal, 45.4 us, 43.8 so; of 512: 64 behind 8192 24.2, 22.3 so.
-// Their parts' way to memory and back makes more of them dear (8 x 3339, 2 heads of 256: 231 us whole, 280 in 2), less
-// so where rows are short, whose number is rounded (8192 queries of 8 heads of 64: 130 whole, 122 in 2). Where few
+// One piece of 512 queries of 12 heads on 4 of 128 behind 32768 keys: 121 us in 15 shares, 141 in 23; 8 pieces
+// of 64 to 512 behind 4096: 168 whole, 118 in 3, 125 in 4, 126 in 6; 3 x 2048, causal: 56 whole, 76 in 2; 16 queries behind
+// 65536: 165 in 8, 34 in 64; 64 behind 8192: 24.4 in 16, 22.7 in 21.  Their parts' way to memory and back makes more of them dear, less
+// so where rows are short, whose number is rounded (8192 queries of 8 heads of 64: 128 whole, 99 in 2, 155 in 8). Where few
 // rows leave most places empty a long sequence among short ones, which the mean hides, has up to 4 (5 of 531 to 2125, 2 heads of
-// 32: 35 us, 19 so).
+// 32: 35 us, 19 so).  Lengths are the device's, and means hide them: 2048 queries, causal, go in 2 shares, 41 us, 37 in 3; 8 x 3339, 2
+// heads of 256, whole, 175, 162 in 2.
 int splits_of(int64_t nseq, int64_t total, int64_t keys, int64_t last, int64_t hq, int64_t hkv, int64_t d) {
   const int64_t places = 256 * (d > 128 ? 2 : d > 64 ? 3 : 4);
   // half a workgroup more a sequence, for its last rows
@@ -582,10 +588,11 @@ bool launch(AttArgs a, hipStream_t st) {
     a.slots = static_cast<uint32_t>(slots - a.first < most ? slots - a.first : most);
     a.units = static_cast<uint32_t>(a.slots * each);
     // Causal prompts, whose last queries see the most keys, in the order of these, so that none of them begins
-    // late and no CU has several: 4 x 2048, 12 heads on 4 of 128, 75 us in order of the sequences, 64 so; 55 of up to 1320, 3 heads of 64,
-    // cap and slopes, 73 and 47; 16 x 2048, d 256, 363 and 341.  With more units neighbours' keys in L2 count for more
-    // (32 x 2048 chunks 437, 445 so), with fewer than CUs the search (2 x 2260, 2 heads of 64: 20.6, 22.8 so), and
-    // behind many keys all last equally long (8 of 200 to 256 behind 4096: 41.3, 45.7 so).
+    // late and no CU has several: 4 x 2048, 12 heads on 4 of 128, 73 us in order of the sequences, 63 so; 55 of up to 1320, 3 heads of 64,
+    // cap and slopes, 68 and 45; 16 x 2048, d 256, 368 and 334.  With more units neighbours' keys in L2 count for more
+    // (48 x 2048 chunks 646, 689 so; 60: 797, 937; 32: 440 both), with fewer than CUs the search (2 x 2260, 2 heads of 64: 20.7, 21.2 so), and
+    // behind many keys most last equally long (8 of 200 to 256 behind 4096: 8 heads of 64 39.1, 41.4 so; 12 on 4 of 64 45.9, 47.0; but 12 on
+    // 4 of 128 84, 71).
     constexpr uint32_t kPlaces = 256 * (D == 256 ? 2 : D == 128 ? 3 : 4);
     a.ranked = a.mask.causal && !a.mask.window && a.nseq < kWave && slots <= most && a.units <= 4096 && 5 * a.units >= 2 * kPlaces &&
                2 * a.total >= a.total_k;

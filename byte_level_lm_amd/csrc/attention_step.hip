@@ -2,10 +2,10 @@
 //
 //   s_j = scale q.k_j (capped, lowered by distance),  o = sum_j 2^{x_j - m} v_j / sum_j 2^{x_j - m},  x = s log2 e
 //
-// Bound by the cache's bytes, each read once: 8 streams of 65536 positions, 12 heads on 4 of
-// 128, bf16: 180 us and 5 for the join, 5.8 TB/s; 256 streams of 256 to 2048 positions in
-// 8 bits: 67 us, 4.9 TB/s (codes to bf16 by vector instructions, 35 % of their cycles); one
-// stream of 2048: 5.4 us and 3.8.  The keys that a stream sees are
+// Bound by the cache's bytes, each read once (kernels' medians in a trace): 8 streams of 65536 positions, 12 heads on 4 of
+// 128, bf16: 184 us and 5 for the join, 5.8 TB/s; 256 streams of 256 to 2048 positions in
+// 8 bits: 69 us, 4.7 TB/s (codes to bf16 by vector instructions, 35 % of their cycles); one
+// stream of 2048: 5.5 us and 4.4.  The keys that a stream sees are
 // cut into `splits` equal shares, each a workgroup of up to 16 query heads of one key
 // head; its four waves take tiles of 32 keys in turn, straight from memory
 // into the matrix instructions' registers, with a running maximum and sum of

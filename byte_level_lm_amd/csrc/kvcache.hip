@@ -4,7 +4,7 @@
 // (the arithmetic of the rows of norm.hip).
 //
 // Bound by the bytes: 65536 tokens of 4 heads of 128 in bf16 45 us (6.0 TB/s) written, 44 read; in
-// 8 bits 44 (4.6 TB/s, the vector instructions of the codes for 3/4 of it) and 37 (5.6).  A group of G lanes has a row, one 16-byte piece of bf16
+// 8 bits written and read back 82 (43 and 39; the vector instructions of the codes take 3/4 of the cycles).  A group of G lanes has a row, one 16-byte piece of bf16
 // a lane; a workgroup finds the places of its tokens once, then moves all
 // their rows, several loads a lane in flight.
 #include "attention.h"

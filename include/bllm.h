@@ -574,8 +574,8 @@ int bllm_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
  *          window > 0)
  * A query that sees no key gets zeros.  A key that a query does not see has no
  * part in its output, whatever its rows hold (NaN and infinities too).  Values of v that are
- * not finite cost time where some queries of a tile see them and others do not: 1.1 to 1.5 times
- * the call with one row of them in front, up to 15 times with one in every tile.
+ * not finite cost time where some queries of a tile see them and others do not: 1.1 to 1.7 times
+ * the call with one row of them in front, up to 11 times with one in every tile.
  * Query head h uses key head h / (hq / hkv).
  * q        : bf16, token t of head i at t * q_stride + i * d; k and v likewise.
  * offsets  : int64 [nseq+1] device, ascending, of the queries; rows of o_out
