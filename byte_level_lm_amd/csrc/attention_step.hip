@@ -97,140 +97,144 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void ste
   float m = -INFINITY, l = 0.0f;
   floatx4 o[VP] = {};
   const int mask = (1 << a.pages.shift) - 1, elem = Q8 ? 1 : 2;
-  for (int tile = t0 + w; tile < t1; tile += kStepWaves) {
-    const int j0 = seen.key(tile);
-    // each half of a tile lies in one page
-    bool page[2];
-    int64_t row[2];
-    const char *kp[2], *vp[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int j = j0 + 16 * b, col = min(j >> a.pages.shift, a.pages.cols - 1);
-      const int id = __builtin_amdgcn_readfirstlane(a.pages.table[static_cast<int64_t>(s) * a.pages.cols + col]);
-      page[b] = id >= 0 && id < a.pages.npages;
-      row[b] = ((static_cast<int64_t>(page[b] ? id : 0) * a.pages.hkv + kh) << a.pages.shift) + (j & mask);
-      kp[b] = static_cast<const char*>(a.k_pages) + row[b] * d * elem;
-      vp[b] = static_cast<const char*>(a.v_pages) + row[b] * d * elem;
-    }
-    uint4 k[2][KP];
-    uint32_t v[8][VW];
-    floatx4 ks[2], vs[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < KP; ++i) {
-        const int at = 16 * (g + 4 * i);  // bytes
-        k[b][i] = at < d * elem ? *reinterpret_cast<const uint4*>(kp[b] + c * d * elem + at) : make_uint4(0, 0, 0, 0);
-      }
-    if (Q8) {
+  // the wave's tiles (twice: the weights' first terms so, no second ones)
+  const auto pass = [&](bool twice) __attribute__((always_inline)) {
+    for (int tile = t0 + w; tile < t1; tile += kStepWaves) {
+      const int j0 = seen.key(tile);
+      // each half of a tile lies in one page
+      bool page[2];
+      int64_t row[2];
+      const char *kp[2], *vp[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        ks[b] = four_floats(a.k_scale + row[b] + 4 * g);
-        vs[b] = four_floats(a.v_scale + row[b] + 4 * g);
+        const int j = j0 + 16 * b, col = min(j >> a.pages.shift, a.pages.cols - 1);
+        const int id = __builtin_amdgcn_readfirstlane(a.pages.table[static_cast<int64_t>(s) * a.pages.cols + col]);
+        page[b] = id >= 0 && id < a.pages.npages;
+        row[b] = ((static_cast<int64_t>(page[b] ? id : 0) * a.pages.hkv + kh) << a.pages.shift) + (j & mask);
+        kp[b] = static_cast<const char*>(a.k_pages) + row[b] * d * elem;
+        vp[b] = static_cast<const char*>(a.v_pages) + row[b] * d * elem;
       }
-    }
+      uint4 k[2][KP];
+      uint32_t v[8][VW];
+      floatx4 ks[2], vs[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const char* from = vp[e / 4] + ((4 * g + e % 4) * d + c * VP) * elem;
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int i = 0; i < VW; i += 4) {
-        constexpr int N = VW < 4 ? VW : 4;
-        if (c * VP + i * 4 / elem < d)
-          __builtin_memcpy(&v[e][i], __builtin_assume_aligned(from + 4 * i, 4 * N), 4 * N);
-        else
-          __builtin_memset(&v[e][i], 0, 4 * N);
-      }
-    }
-
-    floatx4 x[2] = {};
+        for (int i = 0; i < KP; ++i) {
+          const int at = 16 * (g + 4 * i);  // bytes
+          k[b][i] = at < d * elem ? *reinterpret_cast<const uint4*>(kp[b] + c * d * elem + at) : make_uint4(0, 0, 0, 0);
+        }
+      if (Q8) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < KP; ++i) {
-        if (!Q8) {
-          x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(k[b][i]), as_frag(fq[i]), x[b], 0, 0, 0);
-        } else {
-          const uint32_t u[4] = {k[b][i].x, k[b][i].y, k[b][i].z, k[b][i].w};
-          uint32_t f[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {  // codes are exact in bf16: the upper halves of their floats
-            const float lo = static_cast<float>(static_cast<int8_t>(u[j / 2] >> (16 * (j % 2))));
-            const float hi = static_cast<float>(static_cast<int8_t>(u[j / 2] >> (16 * (j % 2) + 8)));
-            f[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
-          }
-          x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(make_uint4(f[0], f[1], f[2], f[3])), as_frag(fq[2 * i]), x[b], 0, 0, 0);
-          x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(make_uint4(f[4], f[5], f[6], f[7])), as_frag(fq[2 * i + 1]), x[b], 0, 0, 0);
+        for (int b = 0; b < 2; ++b) {
+          ks[b] = four_floats(a.k_scale + row[b] + 4 * g);
+          vs[b] = four_floats(a.v_scale + row[b] + 4 * g);
         }
       }
-
-    const bool whole = seen.all(j0) && page[0] && page[1];
-    float p[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int b = e / 4, r = e % 4, j = j0 + 16 * b + 4 * g + r;
-      p[e] = x[b][r] * (Q8 ? c1 * ks[b][r] : c1);
-      if (GEN) {
-        if (c2 != 0.0f) p[e] = capped(p[e], a.mask.cap, c2);
-        p[e] = (p[e] - slope * static_cast<float>(abs(t - j))) * kLog2e;
-      }
-    }
-    if (!whole) {
-      // keys that the query does not see: no score, and zeros for what their rows hold
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool has = page[e / 4] & seen.has(j0 + 16 * (e / 4) + 4 * g + e % 4);
-        p[e] = has ? p[e] : -INFINITY;
-        if (Q8) vs[e / 4][e % 4] = has ? vs[e / 4][e % 4] : 0.0f;
+        const char* from = vp[e / 4] + ((4 * g + e % 4) * d + c * VP) * elem;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) v[e][i] &= has ? ~0u : 0u;
-      }
-    }
-    float top = p[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
-    top = max_xor16(max_xor32(top));
-    if (__any(top > m)) {
-      const float now = fmaxf(m, top), fall = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
-      m = now;
-      l *= fall;
-#pragma unroll
-      for (int n = 0; n < VP; ++n) o[n] *= fall;
-    }
-    const float base = m == -INFINITY ? 0.0f : m;
-    // weights in two bf16 terms, 16 bits: the second costs no time where the bytes bound (256 streams
-    // of 8-bit pages 68 us, 67 with one) and 47 us instead of 44 where rows are the shortest (64 streams, d 64, 8 bits)
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      p[e] = exp2_fast(p[e] - base);
-      l += p[e];
-      if (Q8) p[e] *= vs[e / 4][e % 4];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      hi[e] = pack2(p[2 * e], p[2 * e + 1]);
-      lo[e] = pack2(p[2 * e] - low_half(hi[e]), p[2 * e + 1] - high_half(hi[e]));
-    }
-    const bf16x8 ph = as_frag(make_uint4(hi[0], hi[1], hi[2], hi[3])), pl = as_frag(make_uint4(lo[0], lo[1], lo[2], lo[3]));
-#pragma unroll
-    for (int n = 0; n < VP; ++n) {
-      uint32_t f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (Q8) {
-          const float x0 = static_cast<float>(static_cast<int8_t>(v[2 * e][n / 4] >> (8 * (n % 4))));
-          const float x1 = static_cast<float>(static_cast<int8_t>(v[2 * e + 1][n / 4] >> (8 * (n % 4))));
-          f[e] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
-        } else {
-          f[e] = __builtin_amdgcn_perm(v[2 * e + 1][n / 2], v[2 * e][n / 2], n % 2 ? 0x07060302 : 0x05040100);
+        for (int i = 0; i < VW; i += 4) {
+          constexpr int N = VW < 4 ? VW : 4;
+          if (c * VP + i * 4 / elem < d)
+            __builtin_memcpy(&v[e][i], __builtin_assume_aligned(from + 4 * i, 4 * N), 4 * N);
+          else
+            __builtin_memset(&v[e][i], 0, 4 * N);
         }
       }
-      const bf16x8 fv = as_frag(make_uint4(f[0], f[1], f[2], f[3]));
-      o[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, ph, o[n], 0, 0, 0);
-      o[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, pl, o[n], 0, 0, 0);
+
+      floatx4 x[2] = {};
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+          if (!Q8) {
+            x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(k[b][i]), as_frag(fq[i]), x[b], 0, 0, 0);
+          } else {
+            const uint32_t u[4] = {k[b][i].x, k[b][i].y, k[b][i].z, k[b][i].w};
+            uint32_t f[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // codes are exact in bf16: the upper halves of their floats
+              const float lo = static_cast<float>(static_cast<int8_t>(u[j / 2] >> (16 * (j % 2))));
+              const float hi = static_cast<float>(static_cast<int8_t>(u[j / 2] >> (16 * (j % 2) + 8)));
+              f[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302);
+            }
+            x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(make_uint4(f[0], f[1], f[2], f[3])), as_frag(fq[2 * i]), x[b], 0, 0, 0);
+            x[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(make_uint4(f[4], f[5], f[6], f[7])), as_frag(fq[2 * i + 1]), x[b], 0, 0, 0);
+          }
+        }
+
+      const bool whole = seen.all(j0) && page[0] && page[1];
+      float p[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int b = e / 4, r = e % 4, j = j0 + 16 * b + 4 * g + r;
+        p[e] = x[b][r] * (Q8 ? c1 * ks[b][r] : c1);
+        if (GEN) {
+          if (c2 != 0.0f) p[e] = capped(p[e], a.mask.cap, c2);
+          p[e] = (p[e] - slope * static_cast<float>(abs(t - j))) * kLog2e;
+        }
+      }
+      if (!whole) {
+        // keys that the query does not see: no score, and zeros for what their rows hold
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool has = page[e / 4] & seen.has(j0 + 16 * (e / 4) + 4 * g + e % 4);
+          p[e] = has ? p[e] : -INFINITY;
+          if (Q8) vs[e / 4][e % 4] = has ? vs[e / 4][e % 4] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < VW; ++i) v[e][i] &= has ? ~0u : 0u;
+        }
+      }
+      float top = p[0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) top = fmaxf(top, p[e]);
+      top = max_xor16(max_xor32(top));
+      if (__any(top > m)) {
+        const float now = fmaxf(m, top), fall = exp2_fast(m - (now == -INFINITY ? 0.0f : now));
+        m = now;
+        l *= fall;
+#pragma unroll
+        for (int n = 0; n < VP; ++n) o[n] *= fall;
+      }
+      const float base = m == -INFINITY ? 0.0f : m;
+      // weights in two bf16 terms, 16 bits: the second costs no time where the bytes bound (256 streams
+      // of 8-bit pages 68 us, 67 with one) and 47 us instead of 44 where rows are the shortest (64 streams, d 64, 8 bits)
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        p[e] = exp2_fast(p[e] - base);
+        l += p[e];
+        if (Q8) p[e] *= vs[e / 4][e % 4];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = pack2(p[2 * e], p[2 * e + 1]);
+        lo[e] = twice ? hi[e] : pack2(p[2 * e] - low_half(hi[e]), p[2 * e + 1] - high_half(hi[e]));
+      }
+      const bf16x8 ph = as_frag(make_uint4(hi[0], hi[1], hi[2], hi[3])), pl = as_frag(make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+      for (int n = 0; n < VP; ++n) {
+        uint32_t f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (Q8) {
+            const float x0 = static_cast<float>(static_cast<int8_t>(v[2 * e][n / 4] >> (8 * (n % 4))));
+            const float x1 = static_cast<float>(static_cast<int8_t>(v[2 * e + 1][n / 4] >> (8 * (n % 4))));
+            f[e] = __builtin_amdgcn_perm(__float_as_uint(x1), __float_as_uint(x0), 0x07060302);
+          } else {
+            f[e] = __builtin_amdgcn_perm(v[2 * e + 1][n / 2], v[2 * e][n / 2], n % 2 ? 0x07060302 : 0x05040100);
+          }
+        }
+        const bf16x8 fv = as_frag(make_uint4(f[0], f[1], f[2], f[3]));
+        o[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, ph, o[n], 0, 0, 0);
+        o[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fv, pl, o[n], 0, 0, 0);
+      }
     }
-  }
-  l = sum_xor16(sum_xor32(l));
+    l = sum_xor16(sum_xor32(l));
+  };
+  pass(false);
 
   // the waves' parts: lane (c, g) has values (4 g + r) VP + n of query c
 #pragma unroll
@@ -241,6 +245,27 @@ __global__ __launch_bounds__(64 * kStepWaves, D > 128 ? 2 : Q8 ? 4 : 3) void ste
   if (g == 0) {
     sM[w][c] = m;
     sL[w][c] = l;
+  }
+  // An infinity times a weight's second term, which may be zero or negative, undoes what it gave times the first, and an infinite scale has no
+  // second term.  Where scores are finite and outputs are not, the wave takes its tiles once more with the first term twice, for
+  // these outputs alone (what the look at them costs: 8 bits, d 128, slopes 72.5 us, 71 without; others up to 1 %).
+  float odd = 0.0f;
+#pragma unroll
+  for (int n = 0; n < VP; ++n)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) odd = fmaf(o[n][r], 0.0f, odd);  // 0 x infinity and 0 x NaN are NaN
+  if (__any(odd != 0.0f && fabsf(l) < INFINITY)) {
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int n = 0; n < VP; ++n) o[n] = floatx4{};
+    pass(true);
+    float* part = &sO[w][c * kPitch + 4 * g * VP];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int n = 0; n < VP; ++n)
+        if (!(fabsf(part[r * VP + n]) < INFINITY)) part[r * VP + n] = o[n][r];
   }
   __syncthreads();
   const int qi = threadIdx.x / 16, col = threadIdx.x % 16;  // a query's values in pieces of 8

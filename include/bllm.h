@@ -617,7 +617,7 @@ int bllm_attention(const void* q, const void* k, const void* v, int dtype, const
  * o_out   : bf16 [nseq x hq x d], dense.
  * ws      : bllm_attention_step_workspace(nseq, hq, hkv, d, cols * page) bytes.
  * Numbers : as bllm_attention, with the weights (times v's scales) in two bf16
- *           terms, 16 bits.
+ *           terms, 16 bits.  Values of v that are not finite and seen make the stream's tiles go twice.
  * Other arguments and errors as bllm_attention and bllm_kv_write.
  */
 size_t bllm_attention_step_workspace(int64_t nseq, int64_t hq, int64_t hkv, int64_t d, int64_t positions);
